@@ -82,7 +82,8 @@ typedef enum {
                                 MOE_NOALLOC_SCRATCH_BYTES of workspace */
 } moe_status;
 
-typedef enum { MOE_F16 = 1, MOE_BF16 = 2 } moe_dtype;
+/* MOE_F32: logits of the gate and outputs of moe_lora_add only */
+typedef enum { MOE_F16 = 1, MOE_BF16 = 2, MOE_F32 = 3 } moe_dtype;
 
 /* k argument value selecting the entropy-adaptive top-1/2/3 routing */
 #define MOE_K_ENTROPY (-1)
@@ -356,6 +357,145 @@ moe_status moe_layer_forward_noalloc(const void* x, moe_dtype dt, int32_t T, int
                                      int32_t E, int32_t k, const moe_route_opts* opts, const moe_weights* gate_up,
                                      const moe_weights* gate, const moe_weights* up, const moe_weights* down,
                                      void* y, uint32_t flags, const moe_taps* taps, void* stream);
+
+/*
+ * The routing gate: experts and weights of every token from router logits, in
+ * the forms that moe_route (softmax over the selected experts) does not have.
+ *
+ *   s_e    = softmax(l)_e over all E experts (MOE_SCORE_SOFTMAX), or
+ *            1 / (1 + exp(-l_e)) (MOE_SCORE_SIGMOID)
+ *   key_e  = s_e + bias_e with a bias; without one the logits give the order
+ *   groups G > 1: the E experts form G groups of E/G consecutive experts; a
+ *            group is worth the sum of its group_best (1 or 2) best keys (of
+ *            scores, where it is 2), and the group_k best groups are kept, the
+ *            lower index first among equal ones.  (moe_route_opts.groups is
+ *            another rule: at most one expert per group.)
+ *   the k best keys of the kept groups are chosen, in key order, the lower
+ *            index first among equal keys
+ *   w_j    = scale * s_j, or with renorm scale * s_j / sum over the chosen s_r
+ *            (sigmoid: the sum plus 1e-20)
+ *
+ * The bias (load balancing without an auxiliary loss) only selects: the
+ * weights are formed from the scores, and no gradient reaches it.  Keys are
+ * compared as if formed in 64 bits; weights are fp32.
+ * A logit of -inf masks an expert: its score and its weight are 0 (also in a
+ * row that masks every expert) and its key is -inf whatever its bias, so the
+ * other experts of the kept groups come first.  A key of -inf adds nothing to
+ * its group's sum as the second best.  A NaN logit is the last choice of all;
+ * it makes softmax weights (renormalised: only if it is chosen) NaN.  Chosen
+ * indices are always distinct and within [0, E).
+ *
+ *   score      moe_score
+ *   bias       fp32 [E] on the device, or NULL
+ *   groups     0 or 1: none; 2..MOE_GATE_MAX_GROUPS, dividing E
+ *   group_k    groups kept, 1..groups, with group_k * (E / groups) >= k
+ *   group_best 1 or 2, at most E / groups
+ *   renorm     0 or 1
+ *   scale      finite
+ *   capacity   moe_layer_forward_gated only, as in moe_route_opts
+ * groups <= 1: group_k and group_best are ignored.  A NULL moe_gate_opts means
+ * {softmax, no bias, no groups, renorm 1, scale 1}: moe_route's static top-k.
+ * MOE_ERR_OPTION: a value out of range.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+#define MOE_GATE_MAX_GROUPS 64
+#define MOE_GATE_MAX_TOKENS (1 << 25)
+typedef struct {
+  int32_t score;
+  const float* bias;
+  int32_t groups;
+  int32_t group_k;
+  int32_t group_best;
+  int32_t renorm;
+  float scale;
+  int32_t capacity;
+} moe_gate_opts;
+
+/*
+ * The gate on logits [T, E] of type lt (MOE_F32, MOE_F16 or MOE_BF16), rows
+ * ld >= E elements apart.
+ *   k         1..min(E, 8); 1 <= E <= 256; 0 <= T <= MOE_GATE_MAX_TOKENS
+ *   topk_idx  int32 [T, k] out; topk_w fp32 [T, k] out
+ */
+moe_status moe_gate_from_logits(const void* logits, moe_dtype lt, int64_t ld, int32_t T, int32_t E, int32_t k,
+                                const moe_gate_opts* opts, int32_t* topk_idx, float* topk_w, void* stream);
+/*
+ * Router projection (as in moe_route) and the gate.  logits_out fp32 [T, E]
+ * may be NULL; ws then holds the logits: at least moe_gate_workspace_size(T, E)
+ * bytes, 16-byte aligned.
+ */
+size_t moe_gate_workspace_size(int32_t T, int32_t E);
+moe_status moe_gate(const void* x, moe_dtype dt, int32_t T, int32_t H, const void* router_w, int32_t E, int32_t k,
+                    const moe_gate_opts* opts, int32_t* topk_idx, float* topk_w, float* logits_out, void* ws,
+                    size_t ws_bytes, void* stream);
+/*
+ * The gate's gradient: grad_logits[t, e] = d (sum_s grad_w[t, s] * w[t, s]) /
+ * d logits[t, e] at fixed topk_idx, for the weights that the options (score,
+ * renorm, scale) define.
+ *   topk_idx     int32 [T, k], as the gate wrote it; an index outside [0, E)
+ *                has no part, equal indices in a row add up
+ *   grad_w       fp32 [T, k]; not looked at where the weight is 0
+ *   grad_logits  [T, E] out in the logits' type, rows ld_grad >= E elements
+ *                apart, every element of [T, E] written; must not overlap
+ *                the inputs
+ */
+moe_status moe_gate_backward(const void* logits, moe_dtype lt, int64_t ld, int32_t T, int32_t E, int32_t k,
+                             const moe_gate_opts* opts, const int32_t* topk_idx, const float* grad_w,
+                             void* grad_logits, int64_t ld_grad, void* stream);
+/*
+ * The whole layer with the gate in place of the static top-k: as
+ * moe_layer_forward_ex with moe_gate_opts.  Either router_w is given, or
+ * logits (fp32 [T, E], 4-byte aligned, e.g. a shared router's logits with
+ * per-request adapters added by moe_lora_add) with router_w NULL; both:
+ * MOE_ERR_OPTION.  Workspace: moe_layer_workspace_size.  The entropy tap is 0.
+ */
+moe_status moe_layer_forward_gated(const void* x, moe_dtype dt, int32_t T, int32_t H, const void* router_w,
+                                   const float* logits, int32_t E, int32_t k, const moe_gate_opts* opts,
+                                   const moe_weights* gate_up, const moe_weights* gate, const moe_weights* up,
+                                   const moe_weights* down, void* y, uint32_t flags, const moe_taps* taps, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a projection that they share
+ * (the router, or any projection next to the layer):
+ *
+ *   out[t, :] = base[t, :] + scale[a] * (x[t, :] . A_a^T) . B_a^T,  a = ids[t]
+ *
+ *   a      [L, R, K], b [L, N, R]: the L adapters of one rank R, in x's type
+ *          (16-byte aligned)
+ *   scale  fp32 [L], or NULL (1)
+ *   ranks  int32 [L], or NULL (R): the ranks in use.  Rows of A and columns of
+ *          B from ranks[a] on are not looked at; values are taken into [0, R]
+ *   K % 8 == 0, R % 8 == 0, 8 <= R <= MOE_LORA_MAX_RANK, N >= 1, L >= 1
+ */
+#define MOE_LORA_MAX_RANK 128
+typedef struct {
+  const void* a;
+  const void* b;
+  const float* scale;
+  const int32_t* ranks;
+  int32_t L;
+  int32_t R;
+  int32_t K;
+  int32_t N;
+} moe_lora;
+
+/*
+ *   x      [T, K] of type dt (MOE_F16 / MOE_BF16), rows ldx apart, ldx % 8 == 0,
+ *          16-byte aligned
+ *   ids    int32 [T]: the adapter of each token, in any order; outside [0, L):
+ *          none, out = base
+ *   base   [T, N] of type out_dt (dt or MOE_F32), rows ld_base apart
+ *   out    [T, N] likewise, rows ld_out apart.  out == base (with the same row
+ *          distance) adds in place and leaves tokens without an adapter
+ *          untouched; otherwise the two must not overlap
+ *   ws     at least moe_lora_workspace_size(...) bytes, 16-byte aligned
+ * Sums are fp32 and one rounding gives out.  0 <= T <= MOE_GATE_MAX_TOKENS.
+ */
+size_t moe_lora_workspace_size(int32_t T, int32_t K, int32_t N, int32_t L, int32_t R);
+moe_status moe_lora_add(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const moe_lora* lora, const int32_t* ids,
+                        const void* base, int64_t ld_base, void* out, int64_t ld_out, moe_dtype out_dt, void* ws,
+                        size_t ws_bytes, void* stream);
 
 /*
  * Health figures of per-expert activation counts (page "Qwen3.5-MoE与Qwen3-MoE

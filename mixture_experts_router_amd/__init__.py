@@ -5,7 +5,8 @@ kernels.  PyTorch provides device memory and the current stream.  The names
 mirror the C ABI in include/moe.h:
 
     route, topk_from_logits, layer_forward, fuse_gate_up,
-    layer_workspace_size, route_workspace_size
+    layer_workspace_size, route_workspace_size,
+    gate, gate_from_logits, gate_backward, layer_forward_gated, lora_add
 
 If the library is not built this module raises on first use; there is no
 fallback implementation.
@@ -22,7 +23,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_amd.so")
 
-MOE_F16, MOE_BF16 = 1, 2
+MOE_F16, MOE_BF16, MOE_F32 = 1, 2, 3
 MOE_K_ENTROPY = -1
 MOE_K_ENTROPY_CAP = 3
 FLAG_UNFUSED, FLAG_FORCE_GEMV, FLAG_FORCE_MFMA = 0x1, 0x2, 0x4
@@ -35,7 +36,9 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTS = ("moe_route_workspace_size", "moe_route", "moe_route_ex", "moe_topk_from_logits",
            "moe_topk_from_logits_ex", "moe_layer_workspace_size", "moe_layer_forward", "moe_layer_forward_ex",
-           "moe_layer_forward_noalloc",
+           "moe_layer_forward_noalloc", "moe_layer_forward_gated",
+           "moe_gate_workspace_size", "moe_gate", "moe_gate_from_logits", "moe_gate_backward",
+           "moe_lora_workspace_size", "moe_lora_add",
            "moe_expert_load_stats", "moe_fuse_gate_up", "moe_packed_sb_bytes", "moe_pack_sb", "moe_packed_q_bytes", "moe_pack_q", "moe_status_string",
            "moe_debug_set_events",
            "moe_debug_last_plan", "moe_debug_set_tuning", "moe_debug_stream_read")
@@ -61,6 +64,18 @@ FMT_AFFINE, FMT_NVFP4 = 0, 1
 class CRouteOpts(ctypes.Structure):
     _fields_ = [("health", ctypes.c_void_p), ("alpha", ctypes.c_float), ("groups", ctypes.c_int32),
                 ("capacity", ctypes.c_int32)]
+
+
+class CGateOpts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("bias", ctypes.c_void_p), ("groups", ctypes.c_int32),
+                ("group_k", ctypes.c_int32), ("group_best", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("capacity", ctypes.c_int32)]
+
+
+class CLora(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p), ("L", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("N", ctypes.c_int32)]
 
 
 class CTaps(ctypes.Structure):
@@ -102,6 +117,23 @@ def lib() -> ctypes.CDLL:
                                             ctypes.POINTER(CWeights), ctypes.POINTER(CWeights),
                                             ctypes.POINTER(CWeights), vp, u32, ctypes.POINTER(CTaps), vp]
     L.moe_layer_forward_noalloc.restype = i32
+    gopt = ctypes.POINTER(CGateOpts)
+    L.moe_gate_workspace_size.argtypes = [i32, i32]
+    L.moe_gate_workspace_size.restype = sz
+    L.moe_gate.argtypes = [vp, i32, i32, i32, vp, i32, i32, gopt, vp, vp, vp, vp, sz, vp]
+    L.moe_gate.restype = i32
+    L.moe_gate_from_logits.argtypes = [vp, i32, i64, i32, i32, i32, gopt, vp, vp, vp]
+    L.moe_gate_from_logits.restype = i32
+    L.moe_gate_backward.argtypes = [vp, i32, i64, i32, i32, i32, gopt, vp, vp, vp, i64, vp]
+    L.moe_gate_backward.restype = i32
+    L.moe_layer_forward_gated.argtypes = [vp, i32, i32, i32, vp, vp, i32, i32, gopt, ctypes.POINTER(CWeights),
+                                          ctypes.POINTER(CWeights), ctypes.POINTER(CWeights),
+                                          ctypes.POINTER(CWeights), vp, u32, ctypes.POINTER(CTaps), vp, sz, vp]
+    L.moe_layer_forward_gated.restype = i32
+    L.moe_lora_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    L.moe_lora_workspace_size.restype = sz
+    L.moe_lora_add.argtypes = [vp, i32, i64, i32, ctypes.POINTER(CLora), vp, vp, i64, vp, i64, i32, vp, sz, vp]
+    L.moe_lora_add.restype = i32
     L.moe_expert_load_stats.argtypes = [vp, i32, vp, vp, vp]
     L.moe_expert_load_stats.restype = i32
     L.moe_layer_workspace_size.argtypes = [i32, i32, i32, i32, i32, u32]
@@ -372,6 +404,269 @@ def layer_forward_noalloc(x: torch.Tensor, router_w: torch.Tensor, k: int, down:
                                          ctypes.byref(ctaps) if ctaps is not None else None, _stream(stream))
     _check(st, "moe_layer_forward_noalloc")
     return y
+
+
+# ------------------------------------------------------ gate and adapters --
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+_TYPES = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
+def _elsewhere(t: torch.Tensor, stream):
+    """The context in which a call on tensor `t` runs, or None where that is the
+    current device and stream already.  Under `stream`, what the call allocates
+    belongs to that stream."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU, got one on %s" % t.device)
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+        return torch.cuda.stream(stream)
+    if t.get_device() != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return None
+
+
+def _current(t: torch.Tensor) -> int:
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _operand(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dtype, shape):
+    """Address of a dense tensor of that type and shape on `like`'s device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be dense with shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != like.device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, like.device))
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(T, columns, elements between rows) of a matrix whose rows are dense."""
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions, got shape %s" % (name, tuple(t.shape)))
+    T, n = t.shape
+    ld, step = t.stride()
+    if step != 1 and n > 1:
+        raise ValueError("%s: the elements of a row must be adjacent" % name)
+    return T, n, ld if T > 1 else n
+
+
+def _dense_rows(t: torch.Tensor) -> torch.Tensor:
+    """`t`, or a dense copy where its rows are not dense or overlap."""
+    if t.dim() == 2 and t.stride(1) == 1 and (t.stride(0) >= t.shape[1] or t.shape[0] < 2):
+        return t
+    return t.contiguous()
+
+
+def _gate_opts(like: torch.Tensor, E: int, score: str, bias, groups: int, group_k: int, group_best: int, renorm: bool,
+               scale: float, capacity: int = 0) -> CGateOpts:
+    if score not in SCORES:
+        raise ValueError("score must be one of %s, got %r" % (sorted(SCORES), score))
+    return CGateOpts(SCORES[score], _operand(bias, "bias", like, torch.float32, (E,)), groups, group_k, group_best,
+                     1 if renorm else 0, scale, capacity)
+
+
+def _gate_type(logits: torch.Tensor) -> int:
+    code = _TYPES.get(logits.dtype)
+    if code is None:
+        raise TypeError("logits must be float32, float16 or bfloat16, got %s" % logits.dtype)
+    return code
+
+
+def _routing_out(like: torch.Tensor, T: int, k: int, out):
+    """The (idx, w) tensors of a gate call, new or the caller's."""
+    if out is None:
+        return (torch.empty((T, max(k, 0)), dtype=torch.int32, device=like.device),
+                torch.empty((T, max(k, 0)), dtype=torch.float32, device=like.device))
+    idx, w = out
+    _operand(idx, "out[0]", like, torch.int32, (T, k))
+    _operand(w, "out[1]", like, torch.float32, (T, k))
+    return idx, w
+
+
+def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                     groups: int = 0, group_k: int = 0, group_best: int = 1, renorm: bool = True, scale: float = 1.0,
+                     out=None, stream=None):
+    """The routing gate on logits [T, E] (float32, float16 or bfloat16): dict(idx
+    [T, k] int32, w [T, k] float32).  score "softmax" or "sigmoid"; bias [E]
+    float32 is added to the scores for the selection only; groups: only the
+    experts of the group_k best of `groups` groups can be chosen, a group being
+    worth the sum of its group_best best keys; renorm: the weights of a token
+    sum to `scale` (moe_gate_opts).  out: (idx, w) to write into."""
+    ctx = _elsewhere(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return gate_from_logits(logits, k, score=score, bias=bias, groups=groups, group_k=group_k,
+                                    group_best=group_best, renorm=renorm, scale=scale, out=out)
+    code = _gate_type(logits)
+    logits = _dense_rows(logits)
+    T, E, ld = _rows(logits, "logits")
+    o = _gate_opts(logits, E, score, bias, groups, group_k, group_best, renorm, scale)
+    idx, w = _routing_out(logits, T, k, out)
+    _check(lib().moe_gate_from_logits(logits.data_ptr(), code, ld, T, E, k, o, idx.data_ptr(), w.data_ptr(),
+                                      _current(logits)), "moe_gate_from_logits")
+    return dict(idx=idx, w=w)
+
+
+def gate(x: torch.Tensor, router_w: torch.Tensor, k: int, *, score: str = "softmax",
+         bias: Optional[torch.Tensor] = None, groups: int = 0, group_k: int = 0, group_best: int = 1,
+         renorm: bool = True, scale: float = 1.0, want_logits: bool = False, out=None, stream=None):
+    """Router projection of x [T, H] and the gate on its fp32 logits (options as
+    in gate_from_logits): dict(idx, w[, logits])."""
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return gate(x, router_w, k, score=score, bias=bias, groups=groups, group_k=group_k,
+                        group_best=group_best, renorm=renorm, scale=scale, want_logits=want_logits, out=out)
+    code = _dtype_code(x)
+    if x.dim() != 2 or router_w.dim() != 2:
+        raise ValueError("x and router_w must have two dimensions")
+    (T, H), E = x.shape, router_w.shape[0]
+    x = x.contiguous()
+    o = _gate_opts(x, E, score, bias, groups, group_k, group_best, renorm, scale)
+    pw = _operand(router_w, "router_w", x, x.dtype, (E, H))
+    idx, w = _routing_out(x, T, k, out)
+    logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
+    _check(lib().moe_gate(x.data_ptr(), code, T, H, pw, E, k, o, idx.data_ptr(), w.data_ptr(), logits.data_ptr(), None,
+                          0, _current(x)), "moe_gate")
+    r = dict(idx=idx, w=w)
+    if want_logits:
+        r["logits"] = logits
+    return r
+
+
+def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor, *, score: str = "softmax",
+                  renorm: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """The gradient [T, E] of the gate's weights with respect to the logits, in
+    their type: idx [T, k] int32 as the gate returned it, grad_w [T, k] float32,
+    score, renorm and scale as in the forward call (a bias and groups only
+    select: they change nothing here)."""
+    ctx = _elsewhere(logits, stream)
+    if ctx is not None:
+        with ctx:
+            return gate_backward(logits, idx, grad_w, score=score, renorm=renorm, scale=scale, out=out)
+    code = _gate_type(logits)
+    logits = _dense_rows(logits)
+    T, E, ld = _rows(logits, "logits")
+    if idx.dim() != 2:
+        raise ValueError("idx must have two dimensions")
+    k = idx.shape[1]
+    pi = _operand(idx, "idx", logits, torch.int32, (T, k))
+    pg = _operand(grad_w, "grad_w", logits, torch.float32, (T, k))
+    if out is None:
+        g, ldg = torch.empty((T, E), dtype=logits.dtype, device=logits.device), E
+    else:
+        g = out
+        if g.dtype != logits.dtype:
+            raise TypeError("out must be %s, got %s" % (logits.dtype, g.dtype))
+        if g.shape != logits.shape or g.device != logits.device:
+            raise ValueError("out must have the logits' shape and device")
+        _, _, ldg = _rows(g, "out")
+    o = _gate_opts(logits, E, score, None, 0, 0, 1, renorm, scale)
+    _check(lib().moe_gate_backward(logits.data_ptr(), code, ld, T, E, k, o, pi, pg, g.data_ptr(), ldg,
+                                   _current(logits)), "moe_gate_backward")
+    return g
+
+
+def layer_forward_gated(x: torch.Tensor, router_w: Optional[torch.Tensor], k: int, down: Weights,
+                        gate_up: Optional[Weights] = None, gate: Optional[Weights] = None,
+                        up: Optional[Weights] = None, flags: int = 0, taps: Optional[dict] = None,
+                        out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None, *,
+                        logits: Optional[torch.Tensor] = None, score: str = "softmax",
+                        bias: Optional[torch.Tensor] = None, groups: int = 0, group_k: int = 0, group_best: int = 1,
+                        renorm: bool = True, scale: float = 1.0, capacity: int = 0) -> torch.Tensor:
+    """layer_forward with the gate's routing (options as in gate_from_logits).
+    logits [T, E] float32, with router_w None: the caller's router logits."""
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return layer_forward_gated(x, router_w, k, down, gate_up, gate, up, flags, taps, out, workspace,
+                                       logits=logits, score=score, bias=bias, groups=groups, group_k=group_k,
+                                       group_best=group_best, renorm=renorm, scale=scale, capacity=capacity)
+    code = _dtype_code(x)
+    T, H = x.shape
+    E = down.E
+    _operand(x, "x", x, x.dtype, (T, H))
+    pw = _operand(router_w, "router_w", x, x.dtype, (E, H))
+    pl = _operand(logits, "logits", x, torch.float32, (T, E))
+    o = _gate_opts(x, E, score, bias, groups, group_k, group_best, renorm, scale, capacity)
+    y = torch.empty_like(x) if out is None else out
+    _operand(y, "out", x, x.dtype, (T, H))
+    need = layer_workspace_size(T, H, E, k, down.K, flags)
+    ws = workspace
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    ctaps = None
+    if taps:
+        ctaps = CTaps(*[(taps[n].data_ptr() if n in taps and taps[n] is not None else None) for n in TAP_NAMES])
+    ref = lambda w: w.c() if w is not None else None
+    _check(lib().moe_layer_forward_gated(x.data_ptr(), code, T, H, pw, pl, E, k, o, ref(gate_up), ref(gate), ref(up),
+                                         down.c(), y.data_ptr(), flags, ctaps, ws.data_ptr(), ws.numel(), _current(x)),
+           "moe_layer_forward_gated")
+    return y
+
+
+def lora_workspace_size(T: int, K: int, N: int, L: int, R: int) -> int:
+    return int(lib().moe_lora_workspace_size(T, K, N, L, R))
+
+
+def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *,
+             scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """base [T, N] + scale[i] * (x [T, K] a[i]^T) b[i]^T with i = ids[t] (moe_lora):
+    the low-rank adapters of many requests beside a projection they share, whose
+    output `base` is (x's type, or float32: e.g. router logits).  a [L, R, K]
+    and b [L, N, R] in x's type; ids [T] int32 in any order, outside [0, L) for a
+    token without an adapter; scale [L] float32; ranks [L] int32, the ranks in
+    use of adapters smaller than R.  out: written instead of a new tensor; pass
+    base itself to add in place.  workspace: uint8, lora_workspace_size bytes."""
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return lora_add(x, base, ids, a, b, scale=scale, ranks=ranks, out=out, workspace=workspace)
+    code = _dtype_code(x)
+    if base.dtype != x.dtype and base.dtype != torch.float32:
+        raise TypeError("base must be %s or float32, got %s" % (x.dtype, base.dtype))
+    if a.dim() != 3 or b.dim() != 3 or base.dim() != 2:
+        raise ValueError("a and b must have three dimensions, base two")
+    x = _dense_rows(x)
+    T, K, ldx = _rows(x, "x")
+    if ldx % 8 or x.data_ptr() % 16:
+        x, ldx = x.clone(memory_format=torch.contiguous_format), K
+    (L, R, _), N = a.shape, base.shape[1]
+    if base.shape[0] != T or base.device != x.device:
+        raise ValueError("base must have a row for each of x, on its device")
+    lora = CLora(_operand(a, "a", x, x.dtype, (L, R, K)), _operand(b, "b", x, x.dtype, (L, N, R)),
+                 _operand(scale, "scale", x, torch.float32, (L,)), _operand(ranks, "ranks", x, torch.int32, (L,)),
+                 L, R, K, N)
+    pids = _operand(ids, "ids", x, torch.int32, (T,))
+    if out is None:
+        base = _dense_rows(base)
+        out, ldo = torch.empty((T, N), dtype=base.dtype, device=x.device), N
+    else:
+        if out.dtype != base.dtype:
+            raise TypeError("out must be %s, got %s" % (base.dtype, out.dtype))
+        if out.shape != base.shape or out.device != x.device:
+            raise ValueError("out must have base's shape and device")
+        if out is not base:
+            base = _dense_rows(base)
+        _, _, ldo = _rows(out, "out")
+    _, _, ldb = _rows(base, "base")
+    need = lora_workspace_size(T, K, N, L, R)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    elif ws.device != x.device or not ws.is_contiguous():
+        raise ValueError("workspace must be dense and on x's device")
+    _check(lib().moe_lora_add(x.data_ptr(), code, ldx, T, lora, pids, base.data_ptr(), ldb, out.data_ptr(), ldo,
+                              _TYPES[base.dtype], ws.data_ptr(), ws.numel() * ws.element_size(), _current(x)),
+           "moe_lora_add")
+    return out
 
 
 def expert_load_stats(counts: torch.Tensor, stream=None):

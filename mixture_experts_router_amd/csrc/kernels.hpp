@@ -80,6 +80,42 @@ hipError_t launch_load_stats(const int32_t* counts, int E, int32_t* least_used, 
 hipError_t launch_topk(const float* logits, int T, int E, int k, int gs, int32_t* idx, float* w, int32_t* k_used,
                        float* entropy, float* scratch, hipStream_t st, int32_t* clear_word = nullptr);
 
+// ------------------------------------------------------------------ gate
+// score kinds and logit types (f16 / bf16: the activation codes)
+enum { GATE_SOFTMAX = 0, GATE_SIGMOID = 1 };
+enum { GATE_F32 = 3 };
+struct GateDev {
+  const float* bias = nullptr;  // fp32 [E], added to the scores for the selection only
+  int score = GATE_SOFTMAX;
+  int groups = 1;      // 1: none; else at most 64 groups of E / groups experts
+  int group_k = 0;     // groups kept
+  int group_best = 1;  // experts whose keys rank a group (1 or 2)
+  int renorm = 1;
+  float scale = 1.0f;
+};
+// experts and weights of every token from logits [T, E] (rows ld apart);
+// k_used, entropy (k and 0) and clear_word (0) as in launch_topk, optional
+hipError_t launch_gate(const void* logits, int lt, int64_t ld, int T, int E, int k, const GateDev& g, int32_t* idx,
+                       float* w, hipStream_t st, int32_t* k_used = nullptr, float* entropy = nullptr,
+                       int32_t* clear_word = nullptr);
+// out[t, e] = d (sum_s dw[t, s] w[t, s]) / d logits[t, e], in the logits' type (rows ldo apart)
+hipError_t launch_gate_backward(const void* logits, int lt, int64_t ld, int T, int E, int k, const GateDev& g,
+                                const int32_t* idx, const float* dw, void* out, int64_t ldo, hipStream_t st);
+
+// -------------------------------------------------- low-rank adapters
+// out[t] = base[t] + scale[a] * (x[t] A_a^T) B_a^T with a = ids[t]; see lora.hip
+struct LoraDev {
+  const void* a;         // [L, R, K]
+  const void* b;         // [L, N, R]
+  const float* scale;    // [L] or NULL
+  const int32_t* ranks;  // [L] or NULL
+  int L, R, K, N;
+};
+int64_t lora_partial_floats(int T, int K, int N, int L, int R);  // floats of workspace
+hipError_t launch_lora(const void* x, int act, int64_t ldx, int T, const LoraDev& ad, const int32_t* ids,
+                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, float* part,
+                       hipStream_t st);
+
 // ------------------------------------------------------------------ sort
 // k_used_dev may be NULL (then k_static is used); capacity > 0 lists only the
 // first `capacity` pairs of every expert (the rest get pos -1)

@@ -281,6 +281,51 @@ moe_status check_opts(const moe_route_opts* o, int E, int k, RouteOpt* out) {
   return MOE_OK;
 }
 
+// Gate options, checked (NULL: softmax over the selected experts, no bias, no
+// groups).  capacity is for the layer alone.
+moe_status check_gate_opts(const moe_gate_opts* o, int E, int k, bool layer, moe::GateDev* g, int* cap) {
+  *g = moe::GateDev{};
+  *cap = 0;
+  if (!o) return MOE_OK;
+  if (o->score != MOE_SCORE_SOFTMAX && o->score != MOE_SCORE_SIGMOID) return MOE_ERR_OPTION;
+  if (o->renorm != 0 && o->renorm != 1) return MOE_ERR_OPTION;
+  if (!std::isfinite(o->scale)) return MOE_ERR_OPTION;
+  if (o->bias && (reinterpret_cast<uintptr_t>(o->bias) & 3u) != 0) return MOE_ERR_ALIGN;
+  if (o->capacity < 0 || (o->capacity > 0 && !layer)) return MOE_ERR_OPTION;
+  if (o->groups < 0) return MOE_ERR_OPTION;
+  if (o->groups > 1) {
+    if (o->groups > MOE_GATE_MAX_GROUPS || E % o->groups != 0) return MOE_ERR_OPTION;
+    const int gs = E / o->groups;
+    if (o->group_k < 1 || o->group_k > o->groups || o->group_k * gs < k) return MOE_ERR_OPTION;
+    if (o->group_best < 1 || o->group_best > 2 || o->group_best > gs) return MOE_ERR_OPTION;
+    g->groups = o->groups;
+    g->group_k = o->group_k;
+    g->group_best = o->group_best;
+  }
+  g->score = o->score == MOE_SCORE_SIGMOID ? moe::GATE_SIGMOID : moe::GATE_SOFTMAX;
+  g->bias = o->bias;
+  g->renorm = o->renorm;
+  g->scale = o->scale;
+  *cap = o->capacity;
+  return MOE_OK;
+}
+
+bool half_type(moe_dtype dt) { return dt == MOE_F16 || dt == MOE_BF16; }
+
+bool aligned_to(const void* p, moe_dtype dt) {
+  return (reinterpret_cast<uintptr_t>(p) & (dt == MOE_F32 ? 3u : 1u)) == 0;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// sizes of a gate call on logits [T, E], rows ld apart
+moe_status check_gate(moe_dtype lt, int64_t ld, int T, int E, int k) {
+  if (lt != MOE_F32 && !half_type(lt)) return MOE_ERR_DTYPE;
+  if (T < 0 || T > MOE_GATE_MAX_TOKENS || E < 1 || E > MOE_MAX_EXPERTS || ld < E) return MOE_ERR_SHAPE;
+  if (k < 1 || k > MOE_MAX_K || k > E) return MOE_ERR_K;
+  return MOE_OK;
+}
+
 // the selection launches: static top-k, or the adaptive pass (two launches
 // with scratch for the per-token entropies, one without)
 // (clear_word: see launch_topk)
@@ -302,17 +347,35 @@ moe_status route_impl(const void* x, moe_dtype dt, int T, int H, const void* wr,
 
 moe_status scratch_ptr(void** out);
 
+// moe_layer_forward_gated: the gate's options, and the logits if the caller has them
+struct LayerGate {
+  const moe_gate_opts* opts;
+  const float* logits;
+};
+
 // use_scratch: the workspace is this device's file-scope scratch array (ws
 // and ws_bytes ignored); a call that needs more returns MOE_ERR_SCRATCH.
 moe_status forward_impl(const void* x, moe_dtype dt, int T, int H, const void* router_w, int E, int k,
                         const moe_route_opts* opts, const moe_weights* gate_up, const moe_weights* gate,
                         const moe_weights* up, const moe_weights* down, void* y, uint32_t flags,
-                        const moe_taps* taps, void* ws, size_t ws_bytes, hipStream_t st, bool use_scratch = false) {
+                        const moe_taps* taps, void* ws, size_t ws_bytes, hipStream_t st, bool use_scratch = false,
+                        const LayerGate* gate_by = nullptr) {
   // ---- validation (host only)
-  moe_status s = check_router(x, dt, T, H, router_w, E, k);
+  // logits given (or no token): the router weights play no part, and an
+  // aligned address that nothing reads stands in for them
+  const float* logits_in = gate_by ? gate_by->logits : nullptr;
+  const void* wr = gate_by && !router_w && (logits_in || T == 0) ? (const void*)kAlign : router_w;
+  moe_status s = check_router(x, dt, T, H, wr, E, k);
   if (s != MOE_OK) return s;
   RouteOpt ro;
   if ((s = check_opts(opts, E, k, &ro)) != MOE_OK) return s;
+  moe::GateDev gd;
+  if (gate_by) {
+    if (k < 1) return MOE_ERR_K;
+    if (logits_in && !aligned4(logits_in)) return MOE_ERR_ALIGN;
+    if ((s = check_gate(MOE_F32, E, T, E, k)) != MOE_OK) return s;
+    if ((s = check_gate_opts(gate_by->opts, E, k, true, &gd, &ro.cap)) != MOE_OK) return s;
+  }
   if ((!y && T != 0) || !down) return MOE_ERR_NULL;
   if (T != 0 && !aligned16(y)) return MOE_ERR_ALIGN;
   const int I = down->K;
@@ -389,12 +452,29 @@ moe_status forward_impl(const void* x, moe_dtype dt, int T, int H, const void* r
   const int k_static = k > 0 ? k : 0;
 
   plan_begin(st);
+  // the router (unless the logits are given) and the gate
+  auto gated = [&](int32_t* clear_word) -> moe_status {
+    const float* from = logits_in ? logits_in : logits;
+    if (!logits_in) {
+      HIP_TRY(moe::launch_router_logits(x, router_w, logits, T, H, E, act, nullptr, 0.0f, st));
+      plan_step("router_logits", st);
+    }
+    HIP_TRY(moe::launch_gate(from, moe::GATE_F32, E, T, E, k, gd, idx, wts, st, k_used, entropy, clear_word));
+    plan_step("gate", st);
+    if (logits_in && taps && taps->logits) HIP_TRY(moe::launch_copy_words(logits_in, logits, (int64_t)T * E, st));
+    return MOE_OK;
+  };
   if (gemv) {
-    // decode path: with static k the GEMV kernels select the experts from the
-    // logits themselves (no separate selection launch)
-    HIP_TRY(moe::launch_router_logits(x, router_w, logits, T, H, E, act, ro.health, ro.alpha, st));
-    plan_step("router_logits", st);
     moe::GemvRoute rt{logits, E, idx, wts, k_used, entropy, ro.gs};
+    if (gate_by) {
+      if ((s = gated(nullptr)) != MOE_OK) return s;
+      rt.logits = nullptr;
+    } else {
+      // decode path: with static k the GEMV kernels select the experts from the
+      // logits themselves (no separate selection launch)
+      HIP_TRY(moe::launch_router_logits(x, router_w, logits, T, H, E, act, ro.health, ro.alpha, st));
+      plan_step("router_logits", st);
+    }
     if (k <= 0) {
       moe_status s2 = select_impl(logits, T, E, k, ro.gs, idx, wts, k_used, entropy, (float*)(W + L.hent), st);
       if (s2 != MOE_OK) return s2;
@@ -432,9 +512,12 @@ moe_status forward_impl(const void* x, moe_dtype dt, int T, int H, const void* r
   } else {
     // the selection also clears the flag that the operand conversion raises
     // for scaled bf16 tokens
-    if ((s = route_impl(x, dt, T, H, router_w, E, k, ro, idx, wts, k_used, entropy, logits, (float*)(W + L.hent),
-                        st, any_scaled)) != MOE_OK)
-      return s;
+    if (gate_by)
+      s = gated(any_scaled);
+    else
+      s = route_impl(x, dt, T, H, router_w, E, k, ro, idx, wts, k_used, entropy, logits, (float*)(W + L.hent), st,
+                     any_scaled);
+    if (s != MOE_OK) return s;
     const int bm = moe::gemm_block_m((int)P, E);
     const int mt = moe::gemm_max_mtiles((int)P, E, bm);
     // the GEMM operand: fp16 activations, 8-element blocks in 4-bit unpack
@@ -670,6 +753,148 @@ moe_status moe_layer_forward_noalloc(const void* x, moe_dtype dt, int32_t T, int
   try {
     return forward_impl(x, dt, T, H, router_w, E, k, opts, gate_up, gate, up, down, y, flags, taps, nullptr, 0,
                         (hipStream_t)stream, true);
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+moe_status moe_layer_forward_gated(const void* x, moe_dtype dt, int32_t T, int32_t H, const void* router_w,
+                                   const float* logits, int32_t E, int32_t k, const moe_gate_opts* opts,
+                                   const moe_weights* gate_up, const moe_weights* gate, const moe_weights* up,
+                                   const moe_weights* down, void* y, uint32_t flags, const moe_taps* taps, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  try {
+    if (router_w && logits) return MOE_ERR_OPTION;
+    const LayerGate by{opts, logits};
+    return forward_impl(x, dt, T, H, router_w, E, k, nullptr, gate_up, gate, up, down, y, flags, taps, ws, ws_bytes,
+                        (hipStream_t)stream, false, &by);
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+size_t moe_gate_workspace_size(int32_t T, int32_t E) {
+  if (T < 0 || E < 1) return 0;
+  return align_up((size_t)T * (size_t)E * 4);
+}
+
+moe_status moe_gate(const void* x, moe_dtype dt, int32_t T, int32_t H, const void* router_w, int32_t E, int32_t k,
+                    const moe_gate_opts* opts, int32_t* topk_idx, float* topk_w, float* logits_out, void* ws,
+                    size_t ws_bytes, void* stream) {
+  try {
+    moe_status s = check_router(x, dt, T, H, router_w, E, k);
+    if (s != MOE_OK) return s;
+    if ((s = check_gate(MOE_F32, E, T, E, k)) != MOE_OK) return s;
+    moe::GateDev g;
+    int cap;
+    if ((s = check_gate_opts(opts, E, k, false, &g, &cap)) != MOE_OK) return s;
+    if (T == 0) return MOE_OK;
+    if (!topk_idx || !topk_w) return MOE_ERR_NULL;
+    if (!aligned4(topk_idx) || !aligned4(topk_w) || !aligned4(logits_out)) return MOE_ERR_ALIGN;
+    float* logits = logits_out;
+    if (!logits) {
+      if (!ws || ws_bytes < moe_gate_workspace_size(T, E)) return MOE_ERR_WORKSPACE;
+      if (!aligned16(ws)) return MOE_ERR_ALIGN;
+      logits = (float*)ws;
+    }
+    DevProps props;
+    if ((s = device_props(&props)) != MOE_OK) return s;
+    hipStream_t st = (hipStream_t)stream;
+    plan_begin(st);
+    HIP_TRY(moe::launch_router_logits(x, router_w, logits, T, H, E, (int)dt, nullptr, 0.0f, st));
+    plan_step("router_logits", st);
+    HIP_TRY(moe::launch_gate(logits, moe::GATE_F32, E, T, E, k, g, topk_idx, topk_w, st));
+    plan_step("gate", st);
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+moe_status moe_gate_from_logits(const void* logits, moe_dtype lt, int64_t ld, int32_t T, int32_t E, int32_t k,
+                                const moe_gate_opts* opts, int32_t* topk_idx, float* topk_w, void* stream) {
+  try {
+    moe_status s = check_gate(lt, ld, T, E, k);
+    if (s != MOE_OK) return s;
+    moe::GateDev g;
+    int cap;
+    if ((s = check_gate_opts(opts, E, k, false, &g, &cap)) != MOE_OK) return s;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !topk_w) return MOE_ERR_NULL;
+    if (!aligned_to(logits, lt) || !aligned4(topk_idx) || !aligned4(topk_w)) return MOE_ERR_ALIGN;
+    DevProps props;
+    if ((s = device_props(&props)) != MOE_OK) return s;
+    hipStream_t st = (hipStream_t)stream;
+    plan_begin(st);
+    HIP_TRY(moe::launch_gate(logits, (int)lt, ld, T, E, k, g, topk_idx, topk_w, st));
+    plan_step("gate", st);
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+moe_status moe_gate_backward(const void* logits, moe_dtype lt, int64_t ld, int32_t T, int32_t E, int32_t k,
+                             const moe_gate_opts* opts, const int32_t* topk_idx, const float* grad_w,
+                             void* grad_logits, int64_t ld_grad, void* stream) {
+  try {
+    moe_status s = check_gate(lt, ld, T, E, k);
+    if (s != MOE_OK) return s;
+    if (ld_grad < E) return MOE_ERR_SHAPE;
+    moe::GateDev g;
+    int cap;
+    if ((s = check_gate_opts(opts, E, k, false, &g, &cap)) != MOE_OK) return s;
+    if (T == 0) return MOE_OK;
+    if (!logits || !topk_idx || !grad_w || !grad_logits) return MOE_ERR_NULL;
+    if (!aligned_to(logits, lt) || !aligned_to(grad_logits, lt) || !aligned4(topk_idx) || !aligned4(grad_w))
+      return MOE_ERR_ALIGN;
+    DevProps props;
+    if ((s = device_props(&props)) != MOE_OK) return s;
+    hipStream_t st = (hipStream_t)stream;
+    plan_begin(st);
+    HIP_TRY(moe::launch_gate_backward(logits, (int)lt, ld, T, E, k, g, topk_idx, grad_w, grad_logits, ld_grad, st));
+    plan_step("gate_backward", st);
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+size_t moe_lora_workspace_size(int32_t T, int32_t K, int32_t N, int32_t L, int32_t R) {
+  if (T < 1 || K < 1 || N < 1 || L < 1 || R < 1) return 0;
+  return align_up((size_t)moe::lora_partial_floats(T, K, N, L, R) * 4);
+}
+
+moe_status moe_lora_add(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const moe_lora* lora, const int32_t* ids,
+                        const void* base, int64_t ld_base, void* out, int64_t ld_out, moe_dtype out_dt, void* ws,
+                        size_t ws_bytes, void* stream) {
+  try {
+    if (!lora || !lora->a || !lora->b) return MOE_ERR_NULL;
+    if (!half_type(dt) || (out_dt != dt && out_dt != MOE_F32)) return MOE_ERR_DTYPE;
+    const int64_t K = lora->K, N = lora->N, R = lora->R;
+    if (T < 0 || T > MOE_GATE_MAX_TOKENS || lora->L < 1 || K < 8 || K % 8 != 0 || N < 1 || R < 8 || R % 8 != 0 ||
+        R > MOE_LORA_MAX_RANK)
+      return MOE_ERR_SHAPE;
+    if (ldx < K || ldx % 8 != 0 || ld_base < N || ld_out < N) return MOE_ERR_SHAPE;
+    if (!aligned16(lora->a) || !aligned16(lora->b) || !aligned4(lora->scale) || !aligned4(lora->ranks))
+      return MOE_ERR_ALIGN;
+    if (T == 0) return MOE_OK;
+    if (!x || !ids || !base || !out) return MOE_ERR_NULL;
+    if (!aligned16(x) || !aligned4(ids) || !aligned_to(base, out_dt) || !aligned_to(out, out_dt)) return MOE_ERR_ALIGN;
+    if (base == out && ld_base != ld_out) return MOE_ERR_SHAPE;  // in place: the same rows
+    if (!ws || ws_bytes < moe_lora_workspace_size(T, lora->K, lora->N, lora->L, lora->R)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(ws)) return MOE_ERR_ALIGN;
+    DevProps props;
+    moe_status s = device_props(&props);
+    if (s != MOE_OK) return s;
+    hipStream_t st = (hipStream_t)stream;
+    plan_begin(st);
+    const moe::LoraDev ad{lora->a, lora->b, lora->scale, lora->ranks, lora->L, lora->R, lora->K, lora->N};
+    HIP_TRY(moe::launch_lora(x, (int)dt, ldx, T, ad, ids, base, ld_base, out, ld_out, out_dt == MOE_F32, (float*)ws,
+                             st));
+    plan_step("lora_shrink", st);
+    plan_step("lora_expand", st);
+    return MOE_OK;
   } catch (...) {
     return MOE_ERR_INTERNAL;
   }

@@ -1,0 +1,343 @@
+"""The routing gate and its gradient on the GPU against 64-bit numpy.
+
+Indices are compared exactly: the gate promises the order of keys formed in 64
+bits.  u = 2^-24.  Weights: expf, the division and the logistic are each within
+an ulp (2 u), the exponent's argument is rounded once (|d| u relative in the
+result, |d| <= 40 in these inputs), up to eight terms are summed and the scale
+multiplies, so a weight is within (2 * 40 + 32) u < 2^-17 of its value.
+Gradients: at most that many roundings on each term, so within 2^-16 of the
+same sums over absolute values, plus half a step of a 16-bit output.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_router_amd as moe
+from gate_ref64 import grad64, select64, weights64
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+W_TOL = 2.0 ** -17
+G_TOL = 2.0 ** -16
+
+
+def logits_of(seed, T, E, dtype="f32", spread=1.5):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(T, E, generator=g) * spread).to(TYPES[dtype])
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def check(l, k, bias=None, **kw):
+    """One call against the reference; `l` and `bias` on the CPU."""
+    r = moe.gate_from_logits(l.cuda(), k, bias=None if bias is None else bias.cuda(), **kw)
+    torch.cuda.synchronize()
+    idx, w = r["idx"].cpu().numpy(), f64(r["w"])
+    l64 = f64(l)
+    want = select64(l64, k, bias=None if bias is None else f64(bias), **kw)
+    bad = np.flatnonzero((idx != want).any(1))
+    assert bad.size == 0, (bad[:5], idx[bad[:3]], want[bad[:3]])
+    ww = weights64(l64, want, **kw)
+    assert np.array_equal(np.isnan(w), np.isnan(ww))
+    err = np.abs(np.nan_to_num(w) - np.nan_to_num(ww))
+    assert np.all(err <= W_TOL * np.abs(np.nan_to_num(ww)) + 1e-37), err.max()
+    return r
+
+
+@pytest.mark.parametrize("T", [1, 3, 4, 5, 257])
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 2), (7, 3), (63, 8), (64, 4), (65, 5), (127, 8), (130, 1), (160, 6),
+                                 (255, 8), (256, 8)])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_plain(T, E, k, score, renorm):
+    check(logits_of(T * 1000 + E, T, E), k, score=score, renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,group_k,group_best", [
+    (256, 8, 8, 4, 2), (256, 8, 8, 4, 1), (160, 6, 8, 3, 1), (160, 6, 8, 3, 2), (64, 4, 64, 4, 1), (64, 4, 32, 5, 2),
+    (128, 8, 2, 1, 2), (12, 3, 3, 1, 2), (250, 8, 50, 7, 2), (256, 8, 2, 2, 1), (6, 2, 3, 2, 1), (126, 5, 63, 5, 2)])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_groups_and_bias(score, E, k, groups, group_k, group_best, with_bias):
+    l = logits_of(E + groups, 133, E)
+    b = torch.randn(E, generator=torch.Generator().manual_seed(9)) * 0.1 if with_bias else None
+    check(l, k, bias=b, score=score, groups=groups, group_k=group_k, group_best=group_best, renorm=score == "sigmoid")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(64, 0), (96, 6), (256, 8), (99, 0)])
+def test_half_logits_are_full_of_ties(dtype, score, E, groups):
+    l = (logits_of(E, 300, E) * 4).round().div(4).to(TYPES[dtype])  # quarter steps: many equal logits
+    kw = dict(score=score, groups=groups, group_k=3, group_best=2) if groups else dict(score=score)
+    check(l, 8, **kw)
+    check(l, 8, bias=torch.zeros(E), **kw)
+    check(l, 8, bias=torch.randint(0, 3, (E,), generator=torch.Generator().manual_seed(1)).float() / 8, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [0, 8])
+def test_keys_closer_than_fp32_can_tell(score, groups):
+    """Biases that bring every key to one value, up to their own rounding (2^-25 at 0.5): fp64 decides every slot."""
+    E, T = 64, 40
+    row = logits_of(11, 1, E)
+    l64 = f64(row)
+    s = 1 / (1 + np.exp(-l64)) if score == "sigmoid" else np.exp(l64 - l64.max()) / np.exp(l64 - l64.max()).sum()
+    bias = torch.from_numpy((1.3 - s[0]).astype(np.float32))
+    keys = s[0] + f64(bias)
+    assert np.ptp(keys) < 1e-6 and len(np.unique(keys)) > E // 2
+    l = row.repeat(T, 1)
+    l[1::2] = logits_of(12, T // 2, E)  # every other row is an ordinary one
+    kw = dict(groups=8, group_k=4, group_best=2) if groups else {}
+    check(l, 8, bias=bias, score=score, **kw)
+
+
+def test_extreme_biases_and_logits():
+    E = 128
+    l = logits_of(2, 64, E, spread=30.0)
+    l[:, ::7] = 88.0
+    l[:, 1::9] = -120.0
+    for score in ("softmax", "sigmoid"):
+        b = torch.zeros(E)
+        b[5], b[6], b[90] = -torch.inf, torch.inf, 1e30
+        b[20:40] = torch.finfo(torch.float32).min
+        b[50:60] = 1e6
+        check(l, 8, bias=b, score=score)
+        check(l, 8, bias=b, score=score, groups=16, group_k=3, group_best=2)
+    check(l, 8, score="softmax", renorm=False)
+
+
+@pytest.mark.parametrize("E", [16, 100, 256])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_masked_rows(E, score, renorm):
+    """-inf masks an expert: one left, none left, fewer than k left; the type's lowest value is an ordinary logit."""
+    l = logits_of(4, 8, E)
+    l[0, :] = -torch.inf
+    l[1, :] = -torch.inf
+    l[1, E // 2] = 0.25
+    l[2, 3:] = -torch.inf
+    l[3, ::2] = -torch.inf
+    l[4, :] = torch.finfo(torch.float32).min
+    l[5, 1:] = torch.finfo(torch.float32).min
+    l[6, 4:] = -100.0
+    for b in (None, torch.linspace(0, 0.25, E)):
+        r = check(l, 5, bias=b, score=score, renorm=renorm)
+        w = r["w"].cpu()
+        assert torch.all(w[0] == 0) and torch.all(torch.isfinite(w))
+    if E == 256:
+        check(l, 5, score=score, renorm=renorm, groups=8, group_k=2, group_best=2)
+
+
+def test_nan_logits_come_last_and_indices_stay_valid():
+    l = logits_of(6, 6, 40)
+    l[0, 7] = torch.nan
+    l[1, :] = torch.nan
+    l[2, 3:] = torch.nan
+    l[3, ::2] = torch.nan
+    for kw in (dict(), dict(bias=torch.full((40,), 0.5)), dict(groups=8, group_k=2, group_best=2)):
+        for score in ("softmax", "sigmoid"):
+            r = moe.gate_from_logits(l.cuda(), 5, score=score, renorm=False,
+                                     **{**kw, "bias": kw["bias"].cuda() if "bias" in kw else None})
+            idx = r["idx"].cpu().numpy()
+            assert idx.min() >= 0 and idx.max() < 40
+            assert all(len(set(row)) == 5 for row in idx.tolist())
+            if "groups" not in kw and (score == "sigmoid" or "bias" not in kw):
+                assert 7 not in idx[0] and set(idx[2]) == {0, 1, 2, 3, 4} and all(e % 2 for e in idx[3])
+            if score == "sigmoid":
+                other = r["w"].cpu()[[0, 4, 5]]
+                assert "groups" in kw or torch.all(torch.isfinite(other))
+
+
+def test_strides_and_alignment():
+    wide = logits_of(8, 50, 300)
+    dev = wide.cuda()
+    for cols in (slice(0, 256), slice(1, 161), slice(3, 67), slice(44, 300)):
+        r = moe.gate_from_logits(dev[:, cols], 4, score="sigmoid")
+        want = select64(f64(wide[:, cols]), 4, "sigmoid")
+        assert np.array_equal(r["idx"].cpu().numpy(), want)
+    t = dev.t()[:128]  # columns first: copied
+    assert np.array_equal(moe.gate_from_logits(t, 3)["idx"].cpu().numpy(), select64(f64(wide.t()[:128][:, :]), 3))
+    e = dev[:1, :64].expand(5, 64)
+    assert np.array_equal(moe.gate_from_logits(e, 3)["idx"].cpu().numpy(), select64(f64(wide[:1, :64].expand(5, 64)), 3))
+    r = moe.gate_from_logits(dev[:0, :64], 3)
+    assert r["idx"].shape == (0, 3) and r["w"].shape == (0, 3)
+
+
+def test_gate_equals_route_where_they_meet():
+    """Softmax, renormalised, no bias, no groups: moe_topk_from_logits' static selection, bit for bit."""
+    for E in (8, 64, 100, 256):
+        l = logits_of(E, 500, E).cuda()
+        a, b = moe.gate_from_logits(l, 6), moe.topk_from_logits(l, 6)
+        assert torch.equal(a["idx"], b["idx"])
+        # the same terms, summed pairwise here and in slot order there: seven roundings and the division's
+        assert torch.all((a["w"] - b["w"]).abs() <= 16 * 2.0 ** -24 * b["w"])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,H,E", [(3, 512, 24), (200, 256, 256)])
+def test_projection_and_gate(dtype, T, H, E):
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, H, generator=g).to(TYPES[dtype]).cuda()
+    wr = (torch.randn(E, H, generator=g) / H ** 0.5).to(TYPES[dtype]).cuda()
+    r = moe.gate(x, wr, 4, score="sigmoid", scale=2.0, want_logits=True)
+    # H products exact in fp32, H sums: H u of the sum of absolute values
+    want = f64(x) @ f64(wr).T
+    assert np.all(np.abs(f64(r["logits"]) - want) <= H * 2.0 ** -24 * (np.abs(f64(x)) @ np.abs(f64(wr)).T))
+    again = moe.gate_from_logits(r["logits"], 4, score="sigmoid", scale=2.0)
+    assert torch.equal(r["idx"], again["idx"]) and torch.equal(r["w"], again["w"])
+    assert moe.last_plan() == ["gate"]
+
+
+# ------------------------------------------------------------- gradient
+
+
+def check_grad(l, idx, dw, **kw):
+    got = moe.gate_backward(l.cuda(), idx.cuda(), dw.cuda(), **kw)
+    torch.cuda.synchronize()
+    assert got.dtype == l.dtype
+    want, mag = grad64(f64(l), idx.numpy(), f64(dw), **kw)
+    eps = 0.0 if l.dtype == torch.float32 else torch.finfo(l.dtype).eps / 2
+    sub = 2.0 ** -25 if l.dtype == torch.float16 else 1e-38
+    err = np.abs(f64(got) - want)
+    assert np.all(err <= G_TOL * mag + eps * np.abs(want) + sub), (err - G_TOL * mag).max()
+    return got
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 4), (5, 7, 3), (17, 63, 8), (33, 65, 5), (64, 130, 1),
+                                   (100, 255, 8), (259, 256, 8), (16, 160, 6)])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_gradient(T, E, k, score, renorm, dtype):
+    l = logits_of(T + E, T, E, dtype)
+    idx = torch.from_numpy(select64(f64(l), k, score))
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(3))
+    check_grad(l, idx, dw, score=score, renorm=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_gradient_against_differences(score, renorm):
+    """(f(l + h) - f(l - h)) / 2h of the gate's own weights: off by h^2 / 6 times a third derivative of a few units
+    (h = 2^-6: 5e-4), and by the weights' 2^-17 rounding over h (2 * 4 * 2.5 * 2^-17 / 2^-5 < 5e-3)."""
+    T, E, k, h = 6, 20, 4, 2.0 ** -6
+    l = (logits_of(5, T, E) * 8).round() / 8 + torch.arange(E) * 2.0 ** -4 * 0.5
+    r = moe.gate_from_logits(l.cuda(), k, score=score, renorm=renorm, scale=2.5)
+    idx = r["idx"].cpu()
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(8)).clamp(-2, 2)
+    got = check_grad(l, idx, dw, score=score, renorm=renorm, scale=2.5).cpu()
+
+    def value(v):  # the weights of the same experts, whatever the order they are chosen in now
+        w = weights64(f64(v), idx.numpy(), score, renorm, 2.5)
+        q = moe.gate_from_logits(v.cuda(), k, score=score, renorm=renorm, scale=2.5)
+        same = torch.sort(q["idx"].cpu(), 1).values.equal(torch.sort(idx, 1).values)
+        if same:  # reorder the gate's weights to idx
+            pos = (q["idx"].cpu()[:, None, :] == idx[:, :, None]).int().argmax(2)
+            w = f64(q["w"].cpu().gather(1, pos))
+        return (w * f64(dw)).sum(1)
+
+    for e in range(E):
+        d = torch.zeros(T, E)
+        d[:, e] = h
+        want = (value(l + d) - value(l - d)) / (2 * h)
+        assert np.max(np.abs(f64(got[:, e]) - want)) < 6e-3
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_gradient_of_masked_repeated_and_foreign_indices(score, renorm):
+    T, E, k = 9, 50, 6
+    l = logits_of(3, T, E)
+    idx = torch.from_numpy(select64(f64(l), k, score))
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(4))
+    l[0, :] = -torch.inf  # nothing left
+    l[1, idx[1, 2].item()] = -torch.inf
+    dw[1, 2] = torch.nan  # the incoming gradient of a masked expert is not looked at
+    idx[2, 3] = -1
+    idx[3, 0], dw[3, 0] = E, torch.inf
+    idx[4, 1] = idx[4, 0]
+    idx[5, :] = idx[5, 0]
+    idx[6, :] = -1
+    idx[7, 5] = idx[7, 1]
+    idx[7, 3] = 1 << 30
+    ref_dw = dw.clone()
+    ref_dw[1, 2] = 0.0
+    got = moe.gate_backward(l.cuda(), idx.cuda(), dw.cuda(), score=score, renorm=renorm)
+    want, mag = grad64(f64(l), idx.numpy(), f64(ref_dw), score, renorm)
+    assert np.all(np.abs(f64(got) - want) <= G_TOL * mag + 1e-38)
+    assert torch.all(got[0] == 0) and torch.all(got[6] == 0)
+
+
+def test_gradient_strides_and_out():
+    T, k = 37, 4
+    for E, off, dtype in ((64, 0, "f32"), (64, 1, "f32"), (61, 2, "bf16"), (128, 3, "f16")):
+        wide = logits_of(E, T, E + 8, dtype)
+        l = wide[:, off:off + E]
+        idx = torch.from_numpy(select64(f64(l), k))
+        dw = torch.randn(T, k, generator=torch.Generator().manual_seed(5))
+        out = torch.full((T, E + 5), 7.0, dtype=TYPES[dtype], device="cuda")
+        for score, renorm in (("softmax", False), ("sigmoid", True)):
+            moe.gate_backward(wide.cuda()[:, off:off + E], idx.cuda(), dw.cuda(), score=score, renorm=renorm,
+                              out=out[:, 1:1 + E])
+            dense = moe.gate_backward(l.contiguous().cuda(), idx.cuda(), dw.cuda(), score=score, renorm=renorm)
+            assert torch.equal(out[:, 1:1 + E], dense)
+            assert torch.all(out[:, 0] == 7) and torch.all(out[:, 1 + E:] == 7)
+    assert moe.gate_backward(torch.zeros(0, 8).cuda(), torch.zeros(0, 2, dtype=torch.int32).cuda(),
+                             torch.zeros(0, 2).cuda()).shape == (0, 8)
+
+
+# ----------------------------------------------- streams, graphs, arguments
+
+
+def test_streams_and_graph_replays():
+    l = logits_of(21, 300, 256).cuda()
+    bias = (torch.randn(256, generator=torch.Generator().manual_seed(2)) * 0.1).cuda()
+    kw = dict(score="sigmoid", groups=8, group_k=4, group_best=2, scale=2.5)
+    dw = torch.randn(300, 8, generator=torch.Generator().manual_seed(3)).cuda()
+    want = moe.gate_from_logits(l, 8, bias=bias, **kw)
+    grad = moe.gate_backward(l, want["idx"], dw, score="sigmoid", scale=2.5)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    r = moe.gate_from_logits(l, 8, bias=bias, stream=side, **kw)
+    g2 = moe.gate_backward(l, r["idx"], dw, score="sigmoid", scale=2.5, stream=side)
+    side.synchronize()
+    assert torch.equal(r["idx"], want["idx"]) and torch.equal(r["w"], want["w"]) and torch.equal(g2, grad)
+
+    out = (torch.empty_like(want["idx"]), torch.empty_like(want["w"]))
+    go = torch.empty_like(grad)
+    src = l.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.gate_from_logits(src, 8, bias=bias, out=out, **kw)
+        moe.gate_backward(src, out[0], dw, score="sigmoid", scale=2.5, out=go)
+    for i in range(4):
+        new = logits_of(30 + i, 300, 256).cuda()
+        src.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        e = moe.gate_from_logits(new, 8, bias=bias, **kw)
+        assert torch.equal(out[0], e["idx"]) and torch.equal(out[1], e["w"])
+        assert torch.equal(go, moe.gate_backward(new, e["idx"], dw, score="sigmoid", scale=2.5))
+
+
+def test_argument_errors():
+    l = torch.zeros(4, 8, device="cuda")
+    i, d = torch.zeros(4, 2, dtype=torch.int32, device="cuda"), torch.zeros(4, 2, device="cuda")
+    for call, err in (
+        (lambda: moe.gate_from_logits(l.double(), 2), TypeError),
+        (lambda: moe.gate_from_logits(l[0], 2), ValueError),
+        (lambda: moe.gate_from_logits(l, 2, score="relu"), ValueError),
+        (lambda: moe.gate_from_logits(l, 2, bias=torch.zeros(8)), ValueError),
+        (lambda: moe.gate_from_logits(l, 2, bias=torch.zeros(7, device="cuda")), ValueError),
+        (lambda: moe.gate_from_logits(l, 2, bias=torch.zeros(8, device="cuda").half()), TypeError),
+        (lambda: moe.gate_from_logits(l, 9), moe.MoeError),
+        (lambda: moe.gate_from_logits(l, 0), moe.MoeError),
+        (lambda: moe.gate_from_logits(l, 2, groups=3, group_k=1), moe.MoeError),
+        (lambda: moe.gate_from_logits(l, 2, out=(i.long(), d)), TypeError),
+        (lambda: moe.gate_backward(l, i.long(), d), TypeError),
+        (lambda: moe.gate_backward(l, i[:3], d[:3]), ValueError),
+        (lambda: moe.gate_backward(l, i, d.half()), TypeError),
+        (lambda: moe.gate_backward(l, i, d, out=torch.zeros(4, 8, device="cuda").half()), TypeError),
+    ):
+        with pytest.raises(err):
+            call()
