@@ -50,29 +50,42 @@ __device__ __forceinline__ uint64_t key_of64(double v) {
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, ROWS, 0xF, false);
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, true);
 }
 
-constexpr int DPP_BCAST15 = 0x142;  // lane 15 of a row to the next row
-constexpr int DPP_BCAST31 = 0x143;  // lane 31 to lanes 32-63
-
-// maximum over the 64 lanes, in a scalar register
-__device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
+// maximum over the 16 lanes of a row, in every lane of it
+__device__ __forceinline__ uint32_t max16_u(uint32_t v) {
   v = max(v, dpp_u<DPP_QUAD_1032, 0xF>(v));
   v = max(v, dpp_u<DPP_QUAD_2301, 0xF>(v));
   v = max(v, dpp_u<DPP_ROW_HALF_MIRROR, 0xF>(v));
   v = max(v, dpp_u<DPP_ROW_MIRROR, 0xF>(v));
-  v = max(v, dpp_u<DPP_BCAST15, 0xA>(v));
-  v = max(v, dpp_u<DPP_BCAST31, 0xC>(v));
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  return v;
+}
+
+__device__ __forceinline__ void or16(uint32_t& v) {
+  v |= dpp_u<DPP_QUAD_1032, 0xF>(v);
+  v |= dpp_u<DPP_QUAD_2301, 0xF>(v);
+  v |= dpp_u<DPP_ROW_HALF_MIRROR, 0xF>(v);
+  v |= dpp_u<DPP_ROW_MIRROR, 0xF>(v);
+}
+
+// the next lane's value (0 past the row)
+__device__ __forceinline__ uint32_t dpp_next(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x101, 0xF, 0xF, true);
+}
+
+__device__ __forceinline__ uint64_t lane_read64(uint64_t v, int src) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(src << 2, (int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(src << 2, (int)(uint32_t)(v >> 32));
+  return (uint64_t)hi << 32 | lo;
 }
 
 // 64-bit maximum, then the lowest index that holds it (slow path only)
 __device__ __forceinline__ int wave_best64(uint64_t key, int index) {
 #pragma unroll 1
   for (int off = 1; off < WAVE; off <<= 1) {
-    const uint64_t ok = __shfl_xor(key, off);
-    const int oi = __shfl_xor(index, off);
+    const uint64_t ok = lane_read64(key, lane_id() ^ off);
+    const int oi = __builtin_amdgcn_ds_bpermute((lane_id() ^ off) << 2, index);
     const bool take = ok > key || (ok == key && oi < index);
     key = take ? ok : key;
     index = take ? oi : index;
@@ -82,7 +95,8 @@ __device__ __forceinline__ int wave_best64(uint64_t key, int index) {
 
 __device__ __forceinline__ double wave_sum64(double v) {
 #pragma unroll 1
-  for (int off = 1; off < WAVE; off <<= 1) v += __shfl_xor(v, off);
+  for (int off = 1; off < WAVE; off <<= 1)
+    v += __builtin_bit_cast(double, lane_read64(__builtin_bit_cast(uint64_t, v), lane_id() ^ off));
   return v;
 }
 
@@ -133,17 +147,158 @@ __device__ __forceinline__ float max8(float v) {
   return v;
 }
 
+__device__ __forceinline__ float sum16(float v) {
+  v = sum8(v);
+  return v + dpp_f<DPP_ROW_MIRROR>(v);
+}
+
+__device__ __forceinline__ float max16(float v) {
+  v = max8(v);
+  return fmaxf(v, dpp_f<DPP_ROW_MIRROR>(v));
+}
+
 __device__ __forceinline__ float sigmoid_f32(float l) { return 1.0f / (1.0f + expf(-l)); }
 
 constexpr float SIGMOID_EPS = 1e-20f;  // added to the selected scores' sum
 
 }  // namespace
 
+// ------------------------------------------------------ the exact order --
+//
+// One wave, one token: the k experts by keys in fp64, lane s returning slot
+// s's.  Taken only for tokens whose fp32 keys do not decide.  lds: one double
+// per expert.
+template <int VPL, int LT>
+__device__ __forceinline__ int exact_experts(const void* __restrict__ logits, int64_t ld, int64_t t, int E, int k,
+                                             const GateDev& g, double* __restrict__ lds) {
+  const int lane = lane_id(), e0 = lane * VPL;
+  double d[VPL];
+  float m = -INFINITY;
+  bool masked[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const float l = e0 + j < E ? load_logit<LT>(logits, t * ld + e0 + j) : -INFINITY;
+    masked[j] = l == -INFINITY;
+    m = fmaxf(m, l);
+    d[j] = (double)l;
+  }
+  if (g.score == GATE_SOFTMAX) {
+    m = wave_max(m);
+    double z = 0.0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      d[j] = masked[j] ? 0.0 : exp(d[j] - (double)m);
+      z += d[j];
+    }
+    z = wave_sum64(z);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) d[j] = d[j] / z;  // z = 0 only where all are masked
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) d[j] = 1.0 / (1.0 + exp(-d[j]));
+  }
+  uint64_t key[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    if (g.bias && e0 + j < E) d[j] = d[j] + (double)g.bias[e0 + j];
+    if (masked[j]) d[j] = -INFINITY;
+    key[j] = e0 + j < E ? key_of64(d[j]) : 0ull;
+  }
+  if (g.groups > 1) {
+    const int G = g.groups, gs = E / G;
+    wave_lds_fence();
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) lds[e0 + j] = d[j];
+    wave_lds_fence();
+    uint64_t worth = 0ull;  // of group `lane`; G <= 64
+    if (lane < G) {
+      uint64_t b1 = 0, b2 = 0;
+      int i1 = 0, i2 = 0;
+      for (int i = 0; i < gs; ++i) {
+        const uint64_t u = key_of64(lds[lane * gs + i]);
+        if (u > b1) {
+          b2 = b1, i2 = i1;
+          b1 = u, i1 = i;
+        } else if (u > b2) {
+          b2 = u, i2 = i;
+        }
+      }
+      double v = lds[lane * gs + i1];
+      const double second = lds[lane * gs + i2];
+      if (g.group_best == 2 && second != -INFINITY) v = v + second;
+      worth = key_of64(v);
+    }
+    uint64_t kept = 0;
+#pragma unroll 1
+    for (int s = 0; s < g.group_k; ++s) {
+      const int win = wave_best64(worth, lane);
+      kept |= 1ull << win;
+      if (lane == win) worth = 0ull;
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (e0 + j < E && !(kept >> ((e0 + j) / gs) & 1)) key[j] = 0ull;
+  }
+  int mine = 0;
+#pragma unroll 1
+  for (int s = 0; s < k; ++s) {
+    uint64_t bk = 0;
+    int bi = 64 * VPL;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (key[j] > bk) bk = key[j], bi = e0 + j;
+    const int e = wave_best64(bk, bi);
+    if (lane == s) mine = e;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (e0 + j == e) key[j] = 0ull;
+  }
+  return mine;
+}
+
+// ------------------------------------------------------ sorting networks --
+//
+// A key and its expert as one double in [1, 2): the 32 key bits, then 256 - e,
+// in the mantissa.  Larger key first, lower index first among equal keys is
+// then the order of the doubles, and a comparator is v_max_f64 + v_min_f64
+// (full rate, like fp32).
+__device__ __forceinline__ double pack_key(uint32_t key, int e) {
+  const uint32_t hi = __builtin_amdgcn_alignbit(0x3FFu, key, 12), lo = (key << 20) | (uint32_t)(256 - e) << 11;
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ void order2(double& a, double& b) {
+  const double hi = __builtin_fmax(a, b), lo = __builtin_fmin(a, b);
+  a = hi;
+  b = lo;
+}
+
+// descending; 5 and 19 comparators
+__device__ __forceinline__ void sort4(double* v) {
+  order2(v[0], v[1]), order2(v[2], v[3]), order2(v[0], v[2]), order2(v[1], v[3]), order2(v[1], v[2]);
+}
+
+__device__ __forceinline__ void sort8(double* v) {
+  sort4(v), sort4(v + 4);  // odd-even merge of the two halves
+  order2(v[0], v[4]), order2(v[1], v[5]), order2(v[2], v[6]), order2(v[3], v[7]);
+  order2(v[2], v[4]), order2(v[3], v[5]);
+  order2(v[1], v[2]), order2(v[3], v[4]), order2(v[5], v[6]);
+}
+
 // ----------------------------------------------------------- the gate ---
 //
-// One wave per token; lane i holds the VPL consecutive experts i*VPL ...
-// (VPL = 1, 2, 4 for up to 64, 128, 256 experts), so a row is one coalesced
-// load and each of the k rounds is six DPP maxima and a few ballots.
+// Sixteen lanes a token, four tokens a wave; lane i of a row holds the EPL
+// consecutive experts i*EPL ... (EPL = 4, 8, 16 for up to 64, 128, 256
+// experts).  Each lane sorts its keys once and keeps the best eight in LDS, so
+// each of the k rounds compares sixteen list heads (eight DPP steps for the key
+// and the lowest index) and one lane moves to its next, which is in registers
+// already while the one after it is read.
+//
+// Where scores order the experts, the fp32 keys decide unless two that matter
+// lie within the window of their error: two slots next to each other, the
+// last slot and the best key left out, or the border of the kept groups.  Such
+// a token (under 1% of ordinary ones) is selected again by exact_experts.
+// Equal logits with equal biases are exact ties and need no second look.
 //
 // Error bounds of the fp32 keys (u = 2^-24, products and sums rounded once,
 // v_exp_f32 and v_rcp_f32 within one ulp):
@@ -156,219 +311,311 @@ constexpr float SIGMOID_EPS = 1e-20f;  // added to the selected scores' sum
 //   the bias adds u |key|.
 // Two keys further apart than twice that keep their order; the windows below
 // (2^-20, or 2^-17 p_max, plus 2^-22 |key|) hold that with a margin.
-template <int VPL, int LT>
-__global__ __launch_bounds__(256) void gate_kernel(const void* __restrict__ logits, int64_t ld, int vec, int T, int E,
+constexpr int GATE_PITCH = 260;             // LDS words a token holds its keys in
+constexpr int GATE_WAVE_WORDS = 9 * 64 * 2;  // LDS words a wave: nine list entries a lane (the last is the end), four
+                                             // tokens' keys, or one double per expert of one token
+static_assert(GATE_WAVE_WORDS >= 4 * GATE_PITCH && GATE_WAVE_WORDS >= 2 * 256, "LDS of a wave");
+
+template <int EPL, int LT>
+__global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ logits, int64_t ld, int vec, int T, int E,
                                                    int k, GateDev g, int32_t* __restrict__ idx,
                                                    float* __restrict__ w, int32_t* __restrict__ k_used,
                                                    float* __restrict__ entropy, int32_t* __restrict__ clear_word) {
-  __shared__ uint32_t keys[4][64 * VPL];
-  __shared__ double lds[4][64 * VPL];
-  const int lane = lane_id(), wave = wave_id();
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  extern __shared__ __attribute__((aligned(16))) uint32_t gate_lds[];
+  constexpr int LL = EPL < 8 ? EPL : 8;  // a lane's list: at most MOE_MAX_K of its experts are chosen
+  const int lane = lane_id(), i16 = lane % 16, r = lane / 16;
+  uint32_t* const wlds = gate_lds + wave_id() * GATE_WAVE_WORDS;
+  const int64_t t0 = (int64_t)blockIdx.x * (blockDim.x / 16) + wave_id() * 4;
+  const int64_t t = t0 + r;
+  const bool tv = t < T;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     if (k_used) *k_used = k;
     if (entropy) *entropy = 0.0f;
     if (clear_word) *clear_word = 0;
   }
-  if (t >= T) return;
-  const int e0 = lane * VPL;
-  float l[VPL], b[VPL];
-  const int64_t at = t * ld + e0;
+  const int e0 = i16 * EPL;
+  float l[EPL], b[EPL];
+  const int64_t at = (tv ? t : 0) * ld + e0;
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) l[j] = b[j] = 0.0f;
-  if (vec) {  // E is a multiple of VPL: a lane's experts are all there or all missing
-    if (e0 < E) load_logits<LT, VPL>(logits, at, l);
+  for (int j = 0; j < EPL; ++j) {
+    l[j] = -INFINITY;
+    b[j] = 0.0f;
+  }
+  if (vec) {  // E is a multiple of four
+#pragma unroll
+    for (int j = 0; j < EPL; j += 4)
+      if (e0 + j < E) load_logits<LT, 4>(logits, at + j, l + j);
   } else {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
+    for (int j = 0; j < EPL; ++j)
       if (e0 + j < E) l[j] = load_logit<LT>(logits, at + j);
   }
   if (g.bias) {
+    if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(g.bias) & 15u) == 0) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (e0 + j < E) b[j] = g.bias[e0 + j];
+      for (int j = 0; j < EPL; j += 4)
+        if (e0 + j < E) load_logits<GATE_F32, 4>(g.bias, e0 + j, b + j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if (e0 + j < E) b[j] = g.bias[e0 + j];
+    }
   }
 
   // ---- keys
   const bool by_score = g.bias != nullptr || (g.groups > 1 && g.group_best == 2);
   const bool softmax = g.score == GATE_SOFTMAX;
-  float m_all = 0.0f, z_all = 1.0f;  // softmax over all experts
-  float ex[VPL];
+  float m_all = 0.0f, z_all = 1.0f, window = 0x1p-20f;  // softmax over all experts; sigmoid's window
+  bool unsure = false;
+  uint32_t key[EPL];
   if (softmax && (by_score || !g.renorm)) {
-    float m = -INFINITY;
+    float m = l[0];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (e0 + j < E) m = fmaxf(m, l[j]);
-    m_all = wave_max(m);
+    for (int j = 1; j < EPL; ++j) m = fmaxf(m, l[j]);
+    m_all = max16(m);
     if (m_all == -INFINITY) m_all = 0.0f;  // every expert masked: all terms are 0
-    float z = 0.0f;
+    float z = 0.0f, ex[EPL];
+    if (g.renorm) {  // the probabilities only order the experts
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      ex[j] = e0 + j < E ? expf(l[j] - m_all) : 0.0f;
-      z += ex[j];
+      for (int j = 0; j < EPL; ++j) z += ex[j] = __expf(l[j] - m_all);
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) z += ex[j] = expf(l[j] - m_all);
     }
-    z_all = wave_sum(z);
+    z_all = sum16(z);
     if (z_all == 0.0f) z_all = 1.0f;
-  }
-  uint32_t key[VPL];
-  float window = 0.0f;
-  if (by_score) {
-    const float rz = softmax ? __builtin_amdgcn_rcpf(z_all) : 1.0f;
-    window = softmax ? ldexp_f(rz, -17) : 0x1p-20f;
+    const float rz = __builtin_amdgcn_rcpf(z_all);
+    window = ldexp_f(rz, -17);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const float s = softmax ? ex[j] * rz : __builtin_amdgcn_rcpf(1.0f + __expf(-l[j]));
-      key[j] = key_of(l[j] == -INFINITY ? -INFINITY : s + b[j]);
+    for (int j = 0; j < EPL; ++j) b[j] = ex[j] * rz + b[j];
+  } else if (by_score) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) b[j] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[j])) + b[j];
+  }
+  if (by_score) {
+    // the score's sum is never -0 and its NaNs are left to the exact order, so
+    // these keys need no canonical form
+    float low = l[0], any = b[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) {
+      low = fminf(low, l[j]);
+      any += b[j];
+    }
+    unsure = any != any;
+    if (__ballot(low == -INFINITY)) {  // masked experts (or lanes without any)
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) b[j] = l[j] == -INFINITY ? -INFINITY : b[j];
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const uint32_t u = __builtin_bit_cast(uint32_t, b[j]);
+      key[j] = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = key_of(l[j]);
+    for (int j = 0; j < EPL; ++j) key[j] = key_of(l[j]);
   }
+  if (E != 16 * EPL || t0 + 4 > T) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j)
-    if (e0 + j >= E) key[j] = 0u;
+    for (int j = 0; j < EPL; ++j)
+      if (e0 + j >= E || !tv) key[j] = 0u;
+  }
 
-  // the keys in 64 bits (taken only where 32 bits do not decide)
-  auto keys64 = [&](double* d) __attribute__((always_inline)) {
-    if (softmax) {
-      double z = 0.0;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        d[j] = e0 + j < E ? exp((double)l[j] - (double)m_all) : 0.0;
-        z += d[j];
-      }
-      z = wave_sum64(z);
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) d[j] = d[j] / z + (double)b[j];  // z = 0 only where all are masked
-    } else {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) d[j] = 1.0 / (1.0 + exp(-(double)l[j])) + (double)b[j];
-    }
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (l[j] == -INFINITY) d[j] = -INFINITY;
-  };
-
-  // ---- groups: lane i < G ranks group i, G <= 64
-  if (g.groups > 1) {
-    const int G = g.groups, gs = E / G;
-    uint32_t* row = keys[wave];
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) row[e0 + j] = key[j];
-    wave_lds_fence();
-    uint32_t best = 0u, next = 0u;
-    if (lane < G) {
-      for (int i = 0; i < gs; ++i) {
-        const uint32_t u = row[lane * gs + i];
-        next = max(next, min(best, u));
-        best = max(best, u);
-      }
-    }
-    float value = value_of(best), err = 0.0f;
+  // ---- groups: a group's worth as a range [low, high] of keys, of which only
+  // the order counts: kept if fewer than group_k others can be above it,
+  // dropped if group_k others are
+  auto range = [&](uint32_t best, uint32_t next, uint32_t& low, uint32_t& high) __attribute__((always_inline)) {
+    low = high = best;
+    if (!by_score || best == 0u) return;
+    float v = value_of(best), err = window + 0x1p-22f * fabsf(v);
     if (g.group_best == 2) {
-      const float second = value_of(next), v2 = second == -INFINITY ? 0.0f : second;
-      err = 2.0f * window + 0x1p-22f * (fabsf(value) + fabsf(v2));
-      value = value + v2;
-    } else if (by_score) {
-      err = window + 0x1p-22f * fabsf(value);
-    }
-    // two sums whose ranges value +- err do not meet keep their order
-    const uint32_t top = lane < G ? key_of(value + err) : 0u;
-    const float low = value - err;
-    uint32_t gkey = lane < G ? key_of(value) : 0u;
-    uint64_t kept = 0;
-#pragma unroll 1
-    for (int s = 0; s < g.group_k; ++s) {
-      const uint32_t m = wave_max_key(gkey);
-      int win = (int)__builtin_ctzll(__ballot(gkey == m && gkey != 0u));
-      if (by_score) {
-        const uint32_t bar = key_of(readlane_f(low, win));
-        const uint64_t near = __ballot(gkey != 0u && max(top, gkey) >= bar);
-        if ((near & (near - 1)) != 0) {
-          double d[VPL];
-          keys64(d);
-          wave_lds_fence();
-#pragma unroll
-          for (int j = 0; j < VPL; ++j) lds[wave][e0 + j] = d[j];
-          wave_lds_fence();
-          double v = 0.0;
-          if (near >> lane & 1) {
-            uint64_t b1 = 0, b2 = 0;
-            int i1 = 0, i2 = 0;
-            for (int i = 0; i < gs; ++i) {
-              const uint64_t u = key_of64(lds[wave][lane * gs + i]);
-              if (u > b1) {
-                b2 = b1, i2 = i1;
-                b1 = u, i1 = i;
-              } else if (u > b2) {
-                b2 = u, i2 = i;
-              }
-            }
-            v = lds[wave][lane * gs + i1];
-            const double second = lds[wave][lane * gs + i2];
-            if (g.group_best == 2 && second != -INFINITY) v = v + second;
-          }
-          win = wave_best64(near >> lane & 1 ? key_of64(v) : 0ull, lane);
-        }
+      const float v2 = value_of(next);
+      if (v2 != -INFINITY) {
+        err = err + (window + 0x1p-22f * fabsf(v2));
+        v = v + v2;
       }
-      kept |= 1ull << win;
-      if (lane == win) gkey = 0u;
     }
-    // e / gs for e < 256: ceil(2^16 / gs) is exact enough for gs <= 256
+    const float lo = v - err, hi = v + err;
+    const bool sure = lo <= hi;  // NaN: anything is possible
+    low = sure ? key_of(lo) : 1u;
+    high = sure ? key_of(hi) : 0xFFFFFFFFu;
+  };
+  const int G = g.groups, gs = G > 1 ? E / G : 1;
+  const int lanes = gs / EPL;  // lanes a group, where a group is whole lanes
+  const bool whole = G > 1 && gs % EPL == 0 && (lanes & (lanes - 1)) == 0;
+  if (G > 1 && !whole) {
+    // any size: lanes take groups i16, i16 + 16, ... from LDS
+    uint32_t* const row = wlds + r * GATE_PITCH;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) row[e0 + j] = key[j];
+    wave_lds_fence();
+    uint32_t low[4], high[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int gg = i16 + 16 * q;
+      low[q] = high[q] = 0u;
+      if (gg < G) {
+        uint32_t best = 0u, next = 0u;
+        for (int i = 0; i < gs; ++i) {
+          const uint32_t u = row[gg * gs + i];
+          next = max(next, min(best, u));
+          best = max(best, u);
+        }
+        range(best, next, low[q], high[q]);
+      }
+    }
+    wave_lds_fence();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i16 + 16 * q < G) {
+        row[2 * (i16 + 16 * q)] = low[q];
+        row[2 * (i16 + 16 * q) + 1] = high[q];
+      }
+    wave_lds_fence();
+    uint64_t kept = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int gg = i16 + 16 * q;
+      if (gg < G) {
+        int may = 0, must = 0;
+        for (int h = 0; h < G; ++h) {
+          const uint32_t hl = row[2 * h], hh = row[2 * h + 1];
+          may += (int)(h != gg) & ((int)(hh > low[q]) | ((int)(hh == low[q]) & ((int)by_score | (int)(h < gg))));
+          must += (int)(hl > high[q]);
+        }
+        if (may < g.group_k) kept |= 1ull << gg;
+        else if (by_score && must < g.group_k) unsure = true;
+      }
+    }
+    uint32_t k0 = (uint32_t)kept, k1 = (uint32_t)(kept >> 32);
+    or16(k0);
+    or16(k1);
+    kept = (uint64_t)k1 << 32 | k0;
+    // e / gs for e < 256 and gs <= 128
     const uint32_t inv = (65536u + gs - 1) / gs;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (e0 + j < E && !(kept >> (((uint32_t)(e0 + j) * inv) >> 16) & 1)) key[j] = 0u;
+    for (int j = 0; j < EPL; ++j)
+      if (!(kept >> (((uint32_t)(e0 + j) * inv) >> 16 & 63u) & 1)) key[j] = 0u;
   }
 
-  // ---- the k best keys; lane s keeps the expert of slot s
-  int mine = 0;
-#pragma unroll 1
-  for (int s = 0; s < k; ++s) {
-    uint32_t lm = key[0];
+  // ---- each lane's experts in order
+  double list[EPL];
 #pragma unroll
-    for (int j = 1; j < VPL; ++j) lm = max(lm, key[j]);
-    const uint32_t m = wave_max_key(lm);
-    int e = 64 * VPL;
+  for (int j = 0; j < EPL; ++j) list[j] = pack_key(key[j], e0 + j);
+  if constexpr (EPL == 4) {
+    sort4(list);
+  } else {
+    sort8(list);
+    if constexpr (EPL == 16) {  // the best eight of two sorted eights
+      sort8(list + 8);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const uint64_t hit = __ballot(key[j] == m);
-      const int c = hit ? (int)__builtin_ctzll(hit) * VPL + j : 64 * VPL;
-      e = min(e, c);
+      for (int j = 0; j < 8; ++j) list[j] = __builtin_fmax(list[j], list[15 - j]);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((j & d) == 0) order2(list[j], list[j + d]);
     }
-    if (by_score) {
-      const float v = value_of(m);
-      const uint32_t bar = key_of(v - (window + 0x1p-22f * fabsf(v)));
-      int near = 0;
+  }
+  auto key_in = [](double d) { return (uint32_t)(__builtin_bit_cast(uint64_t, d) >> 20); };
+  auto expert_in = [](double d) { return (uint32_t)__builtin_bit_cast(uint64_t, d) >> 11 & 511u; };  // 256 - e
+
+  bool dropped = false;
+  if (whole) {
+    uint32_t best = key_in(list[0]), next = key_in(list[1]);
+    auto join = [&](uint32_t ob, uint32_t on) __attribute__((always_inline)) {
+      next = max(min(best, ob), max(next, on));
+      best = max(best, ob);
+    };
+    if (lanes > 1) join(dpp_u<DPP_QUAD_1032, 0xF>(best), dpp_u<DPP_QUAD_1032, 0xF>(next));
+    if (lanes > 2) join(dpp_u<DPP_QUAD_2301, 0xF>(best), dpp_u<DPP_QUAD_2301, 0xF>(next));
+    if (lanes > 4) join(dpp_u<DPP_ROW_HALF_MIRROR, 0xF>(best), dpp_u<DPP_ROW_HALF_MIRROR, 0xF>(next));
+    uint32_t low, high;
+    range(best, next, low, high);
+    int may = 0, must = 0;
+    auto rival = [&](int n, uint32_t hl, uint32_t hh) __attribute__((always_inline)) {
+      // without ranges the lower group wins a tie: n lanes back is lower unless it wrapped
+      may += (int)(hh > low) | ((int)(hh == low) & ((int)by_score | (int)(n <= i16)));
+      must += (int)(hl > high);
+    };
+    // the other groups of the row, one turn of `lanes` at a time (lanes without
+    // experts hold 0, below every key)
+#define MOE_GATE_TURN(n) \
+  if (((n) & (lanes - 1)) == 0) rival(n, dpp_u<0x120 + (n), 0xF>(low), dpp_u<0x120 + (n), 0xF>(high))
+    MOE_GATE_TURN(1);
+    MOE_GATE_TURN(2);
+    MOE_GATE_TURN(3);
+    MOE_GATE_TURN(4);
+    MOE_GATE_TURN(5);
+    MOE_GATE_TURN(6);
+    MOE_GATE_TURN(7);
+    MOE_GATE_TURN(8);
+    MOE_GATE_TURN(9);
+    MOE_GATE_TURN(10);
+    MOE_GATE_TURN(11);
+    MOE_GATE_TURN(12);
+    MOE_GATE_TURN(13);
+    MOE_GATE_TURN(14);
+    MOE_GATE_TURN(15);
+#undef MOE_GATE_TURN
+    unsure |= by_score && may >= g.group_k && must < g.group_k && best != 0u;
+    dropped = may >= g.group_k;
+  }
+
+  // ---- the k best keys, and with scores the best one left out: lane s keeps slot s
+  uint32_t mine = 0u;
+  int me = 0;
+  const int last = by_score ? k : k - 1;
+  u32x2* const entry = (u32x2*)wlds + lane;  // entry j of this lane at entry[64 * j]
+  wave_lds_fence();
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) near += (int)__popcll(__ballot(key[j] != 0u && key[j] >= bar));
-      if (near != 1) {
-        double d[VPL];
-        keys64(d);
-        uint64_t bk = 0;
-        int bi = 64 * VPL;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) {
-          const uint64_t u = key[j] != 0u && key[j] >= bar ? key_of64(d[j]) : 0ull;
-          if (u > bk) bk = u, bi = e0 + j;
-        }
-        e = wave_best64(bk, bi);
+  for (int j = 1; j < LL; ++j) entry[64 * j] = u32x2{dropped ? 0u : key_in(list[j]), expert_in(list[j])};
+  entry[64 * LL] = u32x2{0u, 0u};
+  wave_lds_fence();
+  uint32_t hk = dropped ? 0u : key_in(list[0]), hc = expert_in(list[0]);
+  const bool more = EPL > LL && !dropped && key_in(list[LL - 1]) != 0u;  // the lane may hold more keys than its list
+  int next = 64;
+#pragma unroll 1
+  for (int s = 0; s <= last; ++s) {
+    const u32x2 after = entry[next];
+    const uint32_t m = max16_u(hk);
+    const uint32_t c = max16_u(hk == m ? hc : 0u);  // the lowest index: the largest 256 - e
+    if (i16 == s) {
+      mine = m;
+      me = 256 - (int)c;
+    }
+    const bool taken = hc == c;  // an expert is in one list
+    hk = taken ? after.x : hk;
+    hc = taken ? after.y : hc;
+    next = min(next + (taken ? 64 : 0), 64 * LL);
+  }
+  unsure |= more && hk == 0u;  // eight chosen from one lane: its ninth was not looked at
+
+  const bool held = tv && i16 <= last && mine != 0u;
+  float ls = held ? load_logit<LT>(logits, t * ld + me) : 0.0f;
+  if (by_score) {
+    const float bs = held && g.bias ? g.bias[me] : 0.0f;
+    const float v = value_of(mine), nv = value_of(dpp_next(mine));
+    const float nl = __builtin_bit_cast(float, dpp_next(__builtin_bit_cast(uint32_t, ls)));
+    const float nb = __builtin_bit_cast(float, dpp_next(__builtin_bit_cast(uint32_t, bs)));
+    const bool rival = i16 < k && dpp_next(mine) != 0u;
+    const bool apart = v - nv > window + 0x1p-22f * fabsf(v);  // false for NaN and infinities
+    const bool tie = i16 + 1 < k && ls == nl && (bs == nb || ls == -INFINITY);
+    uint64_t again = __ballot(tv && ((rival && !apart && !tie) || unsure));
+    while (again) {
+      const int rr = (int)__builtin_ctzll(again) / 16;
+      again &= ~(0xFFFFull << (16 * rr));
+      const int e = exact_experts<EPL / 4, LT>(logits, ld, t0 + rr, E, k, g, (double*)wlds);
+      const int mv = __builtin_amdgcn_ds_bpermute(i16 << 2, e);
+      if (r == rr && i16 < k) {
+        me = mv;
+        ls = load_logit<LT>(logits, t * ld + me);
       }
     }
-    if (lane == s) mine = e;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (e0 + j == e) key[j] = 0u;
   }
 
-  // ---- weights, slot s in lane s (lanes k..7 add nothing)
-  float ls = 0.0f;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const float v = lane_read_f(l[j], mine / VPL);
-    if (mine % VPL == j) ls = v;
-  }
-  const bool on = lane < k;
+  // ---- weights of slot i16 (lanes k..15 add nothing)
+  const bool on = tv && i16 < k;
   const bool masked = ls == -INFINITY;  // a masked expert has weight 0, also where all are masked
   float wt;
   if (softmax) {
@@ -385,8 +632,8 @@ __global__ __launch_bounds__(256) void gate_kernel(const void* __restrict__ logi
     wt = g.renorm ? s1 / (sum8(s1) + SIGMOID_EPS) : s1;
   }
   if (on) {
-    idx[t * k + lane] = mine;
-    w[t * k + lane] = g.scale * wt;
+    idx[t * k + i16] = me;
+    w[t * k + i16] = g.scale * wt;
   }
 }
 
@@ -451,18 +698,14 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restri
     if (tv) {
       for (int x = i16; x < E; x += 16) m = fmaxf(m, load_logit<LT>(logits, t * ld + x));
     }
-    m = fmaxf(m, dpp_f<DPP_QUAD_1032>(m));
-    m = fmaxf(m, dpp_f<DPP_QUAD_2301>(m));
-    m = fmaxf(m, dpp_f<DPP_ROW_HALF_MIRROR>(m));
-    m = fmaxf(m, dpp_f<DPP_ROW_MIRROR>(m));
+    m = max16(m);
     if (tv) {
       for (int x = i16; x < E; x += 16) {
         const float v = load_logit<LT>(logits, t * ld + x);
         z += v == -INFINITY ? 0.0f : expf(v - m);
       }
     }
-    z = sum8(z);
-    z += dpp_f<DPP_ROW_MIRROR>(z);
+    z = sum16(z);
     const float p = ls == -INFINITY ? 0.0f : expf(ls - m) / z;
     dot = sum8(p != 0.0f ? gv * p : 0.0f);
     val = gv;
@@ -528,16 +771,18 @@ int lt_bytes(int lt) { return lt == GATE_F32 ? 4 : 2; }
 
 hipError_t launch_gate(const void* logits, int lt, int64_t ld, int T, int E, int k, const GateDev& g, int32_t* idx,
                        float* w, hipStream_t st, int32_t* k_used, float* entropy, int32_t* clear_word) {
-  const int vpl = E <= 64 ? 1 : E <= 128 ? 2 : 4;
-  // one load per lane where a row starts aligned to a lane's piece
-  const int vec = E % vpl == 0 && ld % vpl == 0 && (reinterpret_cast<uintptr_t>(logits) % (vpl * lt_bytes(lt))) == 0;
-  const unsigned grid = (unsigned)(((int64_t)T + 3) / 4);
+  // four logits a load where rows start aligned to that
+  const int vec = E % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) % (4 * lt_bytes(lt))) == 0;
+  const int waves = T <= 4096 ? 1 : 4;  // few tokens: a wave to a CU
+  const unsigned grid = (unsigned)(((int64_t)T + 4 * waves - 1) / (4 * waves));
+  const uint32_t lds = waves * GATE_WAVE_WORDS * 4;
   auto go = [&](auto kern) {
-    return launch_kernel(kern, grid, 256, 0, st, logits, ld, vec, T, E, k, g, idx, w, k_used, entropy, clear_word);
+    return launch_kernel(kern, grid, 64 * waves, lds, st, logits, ld, vec, T, E, k, g, idx, w, k_used, entropy,
+                         clear_word);
   };
   auto pick = [&](auto lc) {
     constexpr int LT = decltype(lc)::value;
-    return vpl == 1 ? go(gate_kernel<1, LT>) : vpl == 2 ? go(gate_kernel<2, LT>) : go(gate_kernel<4, LT>);
+    return E <= 64 ? go(gate_kernel<4, LT>) : E <= 128 ? go(gate_kernel<8, LT>) : go(gate_kernel<16, LT>);
   };
   if (lt == GATE_F32) return pick(std::integral_constant<int, GATE_F32>{});
   if (lt == ACT_BF16) return pick(std::integral_constant<int, ACT_BF16>{});
