@@ -466,9 +466,11 @@ moe_status moe_layer_forward_gated(const void* x, moe_dtype dt, int32_t T, int32
  *   scale  fp32 [L], or NULL (1)
  *   ranks  int32 [L], or NULL (R): the ranks in use.  Rows of A and columns of
  *          B from ranks[a] on are not looked at; values are taken into [0, R]
- *   K % 8 == 0, R % 8 == 0, 8 <= R <= MOE_LORA_MAX_RANK, N >= 1, L >= 1
+ *   K % 8 == 0, R % 8 == 0, 8 <= R <= MOE_LORA_MAX_RANK, N >= 1, L >= 1, K
+ *   and N at most MOE_LORA_MAX_COLUMNS
  */
 #define MOE_LORA_MAX_RANK 128
+#define MOE_LORA_MAX_COLUMNS (1 << 22)
 typedef struct {
   const void* a;
   const void* b;
@@ -489,13 +491,12 @@ typedef struct {
  *   out    [T, N] likewise, rows ld_out apart.  out == base (with the same row
  *          distance) adds in place and leaves tokens without an adapter
  *          untouched; otherwise the two must not overlap
- *   ws     at least moe_lora_workspace_size(...) bytes, 16-byte aligned
- * Sums are fp32 and one rounding gives out.  0 <= T <= MOE_GATE_MAX_TOKENS.
+ * ldx and ld_base at most MOE_LORA_MAX_COLUMNS.  Sums are fp32 and one rounding
+ * gives out.  0 <= T <= MOE_GATE_MAX_TOKENS.  One launch, no workspace.
  */
-size_t moe_lora_workspace_size(int32_t T, int32_t K, int32_t N, int32_t L, int32_t R);
 moe_status moe_lora_add(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const moe_lora* lora, const int32_t* ids,
-                        const void* base, int64_t ld_base, void* out, int64_t ld_out, moe_dtype out_dt, void* ws,
-                        size_t ws_bytes, void* stream);
+                        const void* base, int64_t ld_base, void* out, int64_t ld_out, moe_dtype out_dt,
+                        void* stream);
 
 /*
  * Health figures of per-expert activation counts (page "Qwen3.5-MoE与Qwen3-MoE

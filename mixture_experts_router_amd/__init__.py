@@ -38,7 +38,7 @@ EXPORTS = ("moe_route_workspace_size", "moe_route", "moe_route_ex", "moe_topk_fr
            "moe_topk_from_logits_ex", "moe_layer_workspace_size", "moe_layer_forward", "moe_layer_forward_ex",
            "moe_layer_forward_noalloc", "moe_layer_forward_gated",
            "moe_gate_workspace_size", "moe_gate", "moe_gate_from_logits", "moe_gate_backward",
-           "moe_lora_workspace_size", "moe_lora_add",
+           "moe_lora_add",
            "moe_expert_load_stats", "moe_fuse_gate_up", "moe_packed_sb_bytes", "moe_pack_sb", "moe_packed_q_bytes", "moe_pack_q", "moe_status_string",
            "moe_debug_set_events",
            "moe_debug_last_plan", "moe_debug_set_tuning", "moe_debug_stream_read")
@@ -130,9 +130,7 @@ def lib() -> ctypes.CDLL:
                                           ctypes.POINTER(CWeights), ctypes.POINTER(CWeights),
                                           ctypes.POINTER(CWeights), vp, u32, ctypes.POINTER(CTaps), vp, sz, vp]
     L.moe_layer_forward_gated.restype = i32
-    L.moe_lora_workspace_size.argtypes = [i32, i32, i32, i32, i32]
-    L.moe_lora_workspace_size.restype = sz
-    L.moe_lora_add.argtypes = [vp, i32, i64, i32, ctypes.POINTER(CLora), vp, vp, i64, vp, i64, i32, vp, sz, vp]
+    L.moe_lora_add.argtypes = [vp, i32, i64, i32, ctypes.POINTER(CLora), vp, vp, i64, vp, i64, i32, vp]
     L.moe_lora_add.restype = i32
     L.moe_expert_load_stats.argtypes = [vp, i32, vp, vp, vp]
     L.moe_expert_load_stats.restype = i32
@@ -416,14 +414,15 @@ def _elsewhere(t: torch.Tensor, stream):
     """The context in which a call on tensor `t` runs, or None where that is the
     current device and stream already.  Under `stream`, what the call allocates
     belongs to that stream."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on the GPU, got one on %s" % t.device)
     if stream is not None:
         if stream.device != t.device:
             raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
         return torch.cuda.stream(stream)
-    if t.get_device() != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
+    if dev != torch.cuda.current_device():
+        return torch.cuda.device(dev)
     return None
 
 
@@ -431,22 +430,21 @@ def _elsewhere(t: torch.Tensor, stream):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _current(t: torch.Tensor) -> int:
+def _current(dev: int) -> int:
     if _raw_stream is not None:
-        return _raw_stream(t.get_device())
-    return torch.cuda.current_stream(t.device).cuda_stream
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _operand(t: Optional[torch.Tensor], name: str, like: torch.Tensor, dtype, shape):
-    """Address of a dense tensor of that type and shape on `like`'s device (None: NULL)."""
+def _operand(t: Optional[torch.Tensor], name: str, dev: int, dtype, shape):
+    """Address of a dense tensor of that type and shape on GPU `dev` (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be dense with shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != like.device:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, like.device))
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        raise ValueError("%s must be dense on GPU %d with shape %s, got shape %s on %s" %
+                         (name, dev, tuple(shape), tuple(t.shape), t.device))
     return t.data_ptr()
 
 
@@ -468,11 +466,12 @@ def _dense_rows(t: torch.Tensor) -> torch.Tensor:
     return t.contiguous()
 
 
-def _gate_opts(like: torch.Tensor, E: int, score: str, bias, groups: int, group_k: int, group_best: int, renorm: bool,
+def _gate_opts(dev: int, E: int, score: str, bias, groups: int, group_k: int, group_best: int, renorm: bool,
                scale: float, capacity: int = 0) -> CGateOpts:
-    if score not in SCORES:
+    kind = SCORES.get(score)
+    if kind is None:
         raise ValueError("score must be one of %s, got %r" % (sorted(SCORES), score))
-    return CGateOpts(SCORES[score], _operand(bias, "bias", like, torch.float32, (E,)), groups, group_k, group_best,
+    return CGateOpts(kind, _operand(bias, "bias", dev, torch.float32, (E,)), groups, group_k, group_best,
                      1 if renorm else 0, scale, capacity)
 
 
@@ -486,11 +485,12 @@ def _gate_type(logits: torch.Tensor) -> int:
 def _routing_out(like: torch.Tensor, T: int, k: int, out):
     """The (idx, w) tensors of a gate call, new or the caller's."""
     if out is None:
-        return (torch.empty((T, max(k, 0)), dtype=torch.int32, device=like.device),
-                torch.empty((T, max(k, 0)), dtype=torch.float32, device=like.device))
+        shape = (T, max(k, 0))
+        return like.new_empty(shape, dtype=torch.int32), like.new_empty(shape, dtype=torch.float32)
     idx, w = out
-    _operand(idx, "out[0]", like, torch.int32, (T, k))
-    _operand(w, "out[1]", like, torch.float32, (T, k))
+    dev = like.get_device()
+    _operand(idx, "out[0]", dev, torch.int32, (T, k))
+    _operand(w, "out[1]", dev, torch.float32, (T, k))
     return idx, w
 
 
@@ -511,10 +511,11 @@ def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bi
     code = _gate_type(logits)
     logits = _dense_rows(logits)
     T, E, ld = _rows(logits, "logits")
-    o = _gate_opts(logits, E, score, bias, groups, group_k, group_best, renorm, scale)
+    dev = logits.get_device()
+    o = _gate_opts(dev, E, score, bias, groups, group_k, group_best, renorm, scale)
     idx, w = _routing_out(logits, T, k, out)
     _check(lib().moe_gate_from_logits(logits.data_ptr(), code, ld, T, E, k, o, idx.data_ptr(), w.data_ptr(),
-                                      _current(logits)), "moe_gate_from_logits")
+                                      _current(dev)), "moe_gate_from_logits")
     return dict(idx=idx, w=w)
 
 
@@ -533,12 +534,13 @@ def gate(x: torch.Tensor, router_w: torch.Tensor, k: int, *, score: str = "softm
         raise ValueError("x and router_w must have two dimensions")
     (T, H), E = x.shape, router_w.shape[0]
     x = x.contiguous()
-    o = _gate_opts(x, E, score, bias, groups, group_k, group_best, renorm, scale)
-    pw = _operand(router_w, "router_w", x, x.dtype, (E, H))
+    dev = x.get_device()
+    o = _gate_opts(dev, E, score, bias, groups, group_k, group_best, renorm, scale)
+    pw = _operand(router_w, "router_w", dev, x.dtype, (E, H))
     idx, w = _routing_out(x, T, k, out)
     logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
     _check(lib().moe_gate(x.data_ptr(), code, T, H, pw, E, k, o, idx.data_ptr(), w.data_ptr(), logits.data_ptr(), None,
-                          0, _current(x)), "moe_gate")
+                          0, _current(dev)), "moe_gate")
     r = dict(idx=idx, w=w)
     if want_logits:
         r["logits"] = logits
@@ -562,10 +564,11 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
     if idx.dim() != 2:
         raise ValueError("idx must have two dimensions")
     k = idx.shape[1]
-    pi = _operand(idx, "idx", logits, torch.int32, (T, k))
-    pg = _operand(grad_w, "grad_w", logits, torch.float32, (T, k))
+    dev = logits.get_device()
+    pi = _operand(idx, "idx", dev, torch.int32, (T, k))
+    pg = _operand(grad_w, "grad_w", dev, torch.float32, (T, k))
     if out is None:
-        g, ldg = torch.empty((T, E), dtype=logits.dtype, device=logits.device), E
+        g, ldg = logits.new_empty((T, E)), E
     else:
         g = out
         if g.dtype != logits.dtype:
@@ -573,9 +576,9 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
         if g.shape != logits.shape or g.device != logits.device:
             raise ValueError("out must have the logits' shape and device")
         _, _, ldg = _rows(g, "out")
-    o = _gate_opts(logits, E, score, None, 0, 0, 1, renorm, scale)
-    _check(lib().moe_gate_backward(logits.data_ptr(), code, ld, T, E, k, o, pi, pg, g.data_ptr(), ldg,
-                                   _current(logits)), "moe_gate_backward")
+    o = _gate_opts(dev, E, score, None, 0, 0, 1, renorm, scale)
+    _check(lib().moe_gate_backward(logits.data_ptr(), code, ld, T, E, k, o, pi, pg, g.data_ptr(), ldg, _current(dev)),
+           "moe_gate_backward")
     return g
 
 
@@ -597,12 +600,13 @@ def layer_forward_gated(x: torch.Tensor, router_w: Optional[torch.Tensor], k: in
     code = _dtype_code(x)
     T, H = x.shape
     E = down.E
-    _operand(x, "x", x, x.dtype, (T, H))
-    pw = _operand(router_w, "router_w", x, x.dtype, (E, H))
-    pl = _operand(logits, "logits", x, torch.float32, (T, E))
-    o = _gate_opts(x, E, score, bias, groups, group_k, group_best, renorm, scale, capacity)
+    dev = x.get_device()
+    _operand(x, "x", dev, x.dtype, (T, H))
+    pw = _operand(router_w, "router_w", dev, x.dtype, (E, H))
+    pl = _operand(logits, "logits", dev, torch.float32, (T, E))
+    o = _gate_opts(dev, E, score, bias, groups, group_k, group_best, renorm, scale, capacity)
     y = torch.empty_like(x) if out is None else out
-    _operand(y, "out", x, x.dtype, (T, H))
+    _operand(y, "out", dev, x.dtype, (T, H))
     need = layer_workspace_size(T, H, E, k, down.K, flags)
     ws = workspace
     if ws is None or ws.numel() < need:
@@ -612,66 +616,57 @@ def layer_forward_gated(x: torch.Tensor, router_w: Optional[torch.Tensor], k: in
         ctaps = CTaps(*[(taps[n].data_ptr() if n in taps and taps[n] is not None else None) for n in TAP_NAMES])
     ref = lambda w: w.c() if w is not None else None
     _check(lib().moe_layer_forward_gated(x.data_ptr(), code, T, H, pw, pl, E, k, o, ref(gate_up), ref(gate), ref(up),
-                                         down.c(), y.data_ptr(), flags, ctaps, ws.data_ptr(), ws.numel(), _current(x)),
+                                         down.c(), y.data_ptr(), flags, ctaps, ws.data_ptr(), ws.numel(), _current(dev)),
            "moe_layer_forward_gated")
     return y
 
 
-def lora_workspace_size(T: int, K: int, N: int, L: int, R: int) -> int:
-    return int(lib().moe_lora_workspace_size(T, K, N, L, R))
-
-
 def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Tensor, b: torch.Tensor, *,
              scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
-             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """base [T, N] + scale[i] * (x [T, K] a[i]^T) b[i]^T with i = ids[t] (moe_lora):
     the low-rank adapters of many requests beside a projection they share, whose
     output `base` is (x's type, or float32: e.g. router logits).  a [L, R, K]
     and b [L, N, R] in x's type; ids [T] int32 in any order, outside [0, L) for a
     token without an adapter; scale [L] float32; ranks [L] int32, the ranks in
     use of adapters smaller than R.  out: written instead of a new tensor; pass
-    base itself to add in place.  workspace: uint8, lora_workspace_size bytes."""
+    base itself to add in place."""
     ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
-            return lora_add(x, base, ids, a, b, scale=scale, ranks=ranks, out=out, workspace=workspace)
+            return lora_add(x, base, ids, a, b, scale=scale, ranks=ranks, out=out)
+    dtype, odt = x.dtype, base.dtype
     code = _dtype_code(x)
-    if base.dtype != x.dtype and base.dtype != torch.float32:
-        raise TypeError("base must be %s or float32, got %s" % (x.dtype, base.dtype))
+    if odt is not dtype and odt is not torch.float32:
+        raise TypeError("base must be %s or float32, got %s" % (dtype, odt))
     if a.dim() != 3 or b.dim() != 3 or base.dim() != 2:
         raise ValueError("a and b must have three dimensions, base two")
     x = _dense_rows(x)
     T, K, ldx = _rows(x, "x")
     if ldx % 8 or x.data_ptr() % 16:
         x, ldx = x.clone(memory_format=torch.contiguous_format), K
+    dev = x.get_device()
     (L, R, _), N = a.shape, base.shape[1]
-    if base.shape[0] != T or base.device != x.device:
+    if base.shape[0] != T or base.get_device() != dev:
         raise ValueError("base must have a row for each of x, on its device")
-    lora = CLora(_operand(a, "a", x, x.dtype, (L, R, K)), _operand(b, "b", x, x.dtype, (L, N, R)),
-                 _operand(scale, "scale", x, torch.float32, (L,)), _operand(ranks, "ranks", x, torch.int32, (L,)),
+    lora = CLora(_operand(a, "a", dev, dtype, (L, R, K)), _operand(b, "b", dev, dtype, (L, N, R)),
+                 _operand(scale, "scale", dev, torch.float32, (L,)), _operand(ranks, "ranks", dev, torch.int32, (L,)),
                  L, R, K, N)
-    pids = _operand(ids, "ids", x, torch.int32, (T,))
+    pids = _operand(ids, "ids", dev, torch.int32, (T,))
     if out is None:
         base = _dense_rows(base)
-        out, ldo = torch.empty((T, N), dtype=base.dtype, device=x.device), N
+        out, ldo = base.new_empty((T, N)), N
     else:
-        if out.dtype != base.dtype:
-            raise TypeError("out must be %s, got %s" % (base.dtype, out.dtype))
-        if out.shape != base.shape or out.device != x.device:
+        if out.dtype is not odt:
+            raise TypeError("out must be %s, got %s" % (odt, out.dtype))
+        if out.shape != base.shape or out.get_device() != dev:
             raise ValueError("out must have base's shape and device")
         if out is not base:
             base = _dense_rows(base)
         _, _, ldo = _rows(out, "out")
     _, _, ldb = _rows(base, "base")
-    need = lora_workspace_size(T, K, N, L, R)
-    ws = workspace
-    if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-    elif ws.device != x.device or not ws.is_contiguous():
-        raise ValueError("workspace must be dense and on x's device")
     _check(lib().moe_lora_add(x.data_ptr(), code, ldx, T, lora, pids, base.data_ptr(), ldb, out.data_ptr(), ldo,
-                              _TYPES[base.dtype], ws.data_ptr(), ws.numel() * ws.element_size(), _current(x)),
-           "moe_lora_add")
+                              _TYPES[odt], _current(dev)), "moe_lora_add")
     return out
 
 

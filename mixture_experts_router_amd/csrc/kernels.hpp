@@ -111,10 +111,8 @@ struct LoraDev {
   const int32_t* ranks;  // [L] or NULL
   int L, R, K, N;
 };
-int64_t lora_partial_floats(int T, int K, int N, int L, int R);  // floats of workspace
 hipError_t launch_lora(const void* x, int act, int64_t ldx, int T, const LoraDev& ad, const int32_t* ids,
-                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, float* part,
-                       hipStream_t st);
+                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, hipStream_t st);
 
 // ------------------------------------------------------------------ sort
 // k_used_dev may be NULL (then k_static is used); capacity > 0 lists only the

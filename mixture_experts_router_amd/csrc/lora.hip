@@ -2,14 +2,11 @@
 //
 //   out[t] = base[t] + scale_a * (x[t] A_a^T) B_a^T,   a = ids[t]
 //
-// with A_a [R, K] and B_a [N, R] of adapter a.  Two launches: v = x A^T into
-// fp32 partial sums, then base + scale v B^T.  Both look at chunks of 64
-// consecutive tokens: every wave reads the chunk's 64 ids (one a lane), walks
-// its distinct adapters with ballots and works on the tokens of one adapter
-// at a time on the matrix cores, so neither sorted ids nor a sorting launch
-// are needed, each adapter is read once a chunk, and runs of one request fill
-// the tiles.  Workgroup (chunk, j, s) takes the j-th, (j + J)-th ... distinct
-// adapter and the s-th part of the reduced (or written) columns.
+// with A_a [R, K] and B_a [N, R] of adapter a, in one launch.  Every wave of a
+// workgroup reads the 64 ids of its chunk of consecutive tokens (one a lane),
+// walks the chunk's distinct adapters with ballots and takes its turn at their
+// tiles: up to 16 tokens of one adapter on the matrix cores.  So ids come in
+// any order, without a sorting launch, and runs of one request fill the tiles.
 //
 // Rounding: x A^T has exact products and fp32 sums, which stay in fp32.  For
 // the second product v goes to the matrix cores as two 16-bit parts (hi + lo:
@@ -30,6 +27,16 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int CHUNK = 64;  // tokens a workgroup looks at: one id a lane
+
+// Loads whose place may not exist go through a descriptor's range check, which
+// gives zeros: no branch, and 32-bit offsets.  FAR lies beyond every
+// descriptor here (the sizes stay below 2^31 bytes) and still does with any
+// offset within one added.
+constexpr uint32_t FAR = 0x80000000u;
+
+__device__ __forceinline__ u32x4 buf_load16(rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+}
 
 template <int ACT>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -62,126 +69,18 @@ __device__ __forceinline__ int adapter_rank(const int32_t* __restrict__ ranks, i
   return ranks ? min(max(ranks[a], 0), R) : R;
 }
 
-// ------------------------------------------------------------- x A^T ----
-//
-// D = A x^T: rows are ranks, columns tokens, so a lane ends with four
-// consecutive ranks of one token.  The four waves take consecutive parts of
-// the workgroup's columns and are added through LDS in wave order; lane group
-// g = lane / 16 of a 64-column block reads columns 16 g .. 16 g + 15 (32
-// contiguous bytes) of its row, the same order in both operands.
-template <int ACT, int RT>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx,
-                                                          const uint16_t* __restrict__ am,
-                                                          const int32_t* __restrict__ ids,
-                                                          const int32_t* __restrict__ ranks, float* __restrict__ part,
-                                                          int T, int L, int R, int K) {
-  constexpr int NT = RT == 8 ? 2 : 4;  // token tiles a pass
-  constexpr int UB = RT <= 2 ? 2 : 1;  // 64-column blocks in flight
-  __shared__ f32x4 red[2][RT * NT][WAVE];
-  const int lane = lane_id(), wave = wave_id();
-  const int l16 = lane % 16, g = lane / 16;
-  const int64_t t0 = (int64_t)blockIdx.x * CHUNK;
-  const int id = chunk_id(ids, t0, T, L);
-  const int nb = (K + 63) / 64, W = gridDim.z * 4, slot = blockIdx.z * 4 + wave;
-  const int b0 = (int)((int64_t)nb * slot / W), b1 = (int)((int64_t)nb * (slot + 1) / W);
-  uint64_t left = __ballot(id >= 0);
-  for (int n = 0; left != 0; ++n) {
-    const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
-    const uint64_t mine = __ballot(id == a);
-    left &= ~mine;
-    if (n % (int)gridDim.y != (int)blockIdx.y) continue;
-    const int m = (int)__popcll(mine);
-    const int nth = nth_lane(mine);
-    const int rank = adapter_rank(ranks, a, R);
-    const uint16_t* arow = am + ((int64_t)a * R + l16) * K + 16 * g;
-    for (int i0 = 0; i0 * 16 < m; i0 += NT) {
-      f32x4 acc[RT][NT];
-      const uint16_t* xrow[NT];
-      int tok[NT];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int p = (i0 + i) * 16 + l16;
-        tok[i] = __builtin_amdgcn_ds_bpermute((p < m ? p : 0) << 2, nth);
-        if (p >= m) tok[i] = -1;
-        xrow[i] = x + (t0 + max(tok[i], 0)) * ldx + 16 * g;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      }
-      const int nt = min(NT, (m - i0 * 16 + 15) / 16);
-      for (int b = b0; b < b1; b += UB) {
-        u32x4 av[UB][2][RT], xv[UB][2][NT];
-#pragma unroll
-        for (int u = 0; u < UB; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = (b + u) * 64 + 8 * h;
-            const bool in = b + u < b1 && c + 16 * g < K;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              xv[u][h][i] = u32x4{0u, 0u, 0u, 0u};
-              if (i < nt && in && tok[i] >= 0) xv[u][h][i] = load16(xrow[i] + c);
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-              av[u][h][r] = u32x4{0u, 0u, 0u, 0u};
-              if (in && r * 16 + l16 < rank) av[u][h][r] = load16(arow + (int64_t)r * 16 * K + c);
-            }
-          }
-#pragma unroll
-        for (int u = 0; u < UB; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-              if (i < nt) {
-#pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r][i] = mfma16<ACT>(av[u][h][r], xv[u][h][i], acc[r][i]);
-              }
-      }
-      // (w0 + w2) + (w1 + w3)
-      __syncthreads();
-      if (wave >= 2) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (i < nt) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r) red[wave - 2][r * NT + i][lane] = acc[r][i];
-          }
-      }
-      __syncthreads();
-      if (wave < 2) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (i < nt) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r) acc[r][i] = acc[r][i] + red[wave][r * NT + i][lane];
-          }
-      }
-      __syncthreads();
-      if (wave == 1) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (i < nt) {
-#pragma unroll
-            for (int r = 0; r < RT; ++r) red[0][r * NT + i][lane] = acc[r][i];
-          }
-      }
-      __syncthreads();
-      if (wave == 0) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          if (i < nt && tok[i] >= 0) {
-            float* to = part + ((int64_t)blockIdx.z * T + t0 + tok[i]) * R;
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-              if (r * 16 + 4 * g < R) *(f32x4*)(to + r * 16 + 4 * g) = acc[r][i] + red[0][r * NT + i][lane];
-          }
-      }
-    }
+// ------------------------------------------------- base + scale v B^T ---
+
+// two fp32 as two 16-bit values, round to nearest even (the hardware's conversions)
+template <int ACT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (ACT == ACT_BF16) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+  } else {
+    return __builtin_bit_cast(uint32_t, f16x2{(f16)a, (f16)b});
   }
 }
-
-// ------------------------------------------------- base + scale v B^T ---
 
 // splits v (finite or not) into NP 16-bit parts, each the rounding of what
 // the earlier ones leave
@@ -189,255 +88,491 @@ template <int ACT, int NP>
 __device__ __forceinline__ void split_parts(float v, uint16_t* o) {
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    o[i] = f32_to_act_bits(v, ACT);
+    o[i] = (uint16_t)pack2<ACT>(v, 0.0f);
     const float f = act_to_f32(o[i], ACT);
     v = fabsf(f) < INFINITY ? v - f : 0.0f;  // inf and NaN are the first part alone
   }
 }
 
-// RS: 32-rank steps of the reduction; 0 stands for up to 16 ranks, where one
-// matrix instruction takes the first two parts side by side
-template <int ACT, bool F32, int RS>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restrict__ part, int S,
-                                                          const uint16_t* __restrict__ bm,
-                                                          const float* __restrict__ scale,
-                                                          const int32_t* __restrict__ ids,
-                                                          const int32_t* __restrict__ ranks, const void* base,
-                                                          int64_t ldb, void* out, int64_t ldo, int T, int L, int R,
-                                                          int N, int vec) {
-  constexpr int NP = F32 && ACT == ACT_BF16 ? 3 : 2;
-  constexpr int RP = RS == 0 ? 16 : RS * 32;
-  constexpr int STEPS = RS == 0 ? 1 : RS;
-  __shared__ __attribute__((aligned(16))) uint16_t vs[NP][CHUNK][RP + 8];
-  __shared__ int exps[CHUNK];
-  const int lane = lane_id(), wave = wave_id();
-  const int l16 = lane % 16, g = lane / 16;
-  const int64_t t0 = (int64_t)blockIdx.x * CHUNK;
-  const int id = chunk_id(ids, t0, T, L);
-  const int nb = (N + 31) / 32;
-  const int b0 = (int)((int64_t)nb * blockIdx.z / gridDim.z), b1 = (int)((int64_t)nb * (blockIdx.z + 1) / gridDim.z);
-  uint64_t left = __ballot(id >= -1);
-  for (int n = 0; left != 0; ++n) {
-    const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
-    const uint64_t mine = __ballot(id == a);
-    left &= ~mine;
-    if (n % (int)gridDim.y != (int)blockIdx.y) continue;
-    const int m = (int)__popcll(mine);
-    const int nth = nth_lane(mine);
-    if (a < 0) {
-      // no adapter: out is base, moved only if the two are not one buffer
-      if (out == base) continue;
-      const int c0 = b0 * 32, c1 = min(N, b1 * 32);
-      for (int p = wave; p < m; p += 4) {
-        const int64_t t = t0 + __builtin_amdgcn_readlane(nth, p);
-        for (int c = c0 + lane; c < c1; c += WAVE) {
-          if constexpr (F32) ((float*)out)[t * ldo + c] = ((const float*)base)[t * ldb + c];
-          else ((uint16_t*)out)[t * ldo + c] = ((const uint16_t*)base)[t * ldb + c];
-        }
+// order of one wave's LDS accesses (its LDS instructions execute in order)
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// 4 x 4 transpose of 16-byte pieces between the four lanes of a quad and four
+// registers: lane q's piece j becomes lane j's piece q.  A tile's rows are
+// loaded with four consecutive lanes on 64 contiguous bytes of a row (load j:
+// row 4 (lane / 4 % 4) + j), which the L1 serves more than twice as fast as
+// sixteen rows a sixteen lanes (16.0 against 7.3 TB/s from L2), and this makes
+// lane l hold row l % 16 as the matrix instructions want it.
+// Two exchanges, of lane bit 0 with register bit 0 and of bit 1 with bit 1: each
+// register is one v_cndmask whose other operand comes through a quad
+// permutation (the compiler makes two instructions of it).  a, b, c, d are the
+// words of v[0] .. v[3].  s_nop 1 at both ends: a DPP operand and a matrix
+// instruction's may be read two wait states after the vector instruction that
+// wrote them; inside, at least two instructions lie between.
+__device__ __forceinline__ void quad_transpose(u32x4 (&v)[4]) {
+  uint32_t a0 = v[0][0], a1 = v[0][1], a2 = v[0][2], a3 = v[0][3], b0 = v[1][0], b1 = v[1][1], b2 = v[1][2],
+           b3 = v[1][3], c0 = v[2][0], c1 = v[2][1], c2 = v[2][2], c3 = v[2][3], d0 = v[3][0], d1 = v[3][1],
+           d2 = v[3][2], d3 = v[3][3], t0, t1, t2, t3, u0, u1, u2, u3;
+  asm("s_nop 1\n\t"
+      "s_mov_b32 vcc_lo, 0x55555555\n\ts_mov_b32 vcc_hi, 0x55555555\n\t"
+      "v_cndmask_b32_dpp %[t0], %[b0], %[a0], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[u0], %[d0], %[c0], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[t1], %[b1], %[a1], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[u1], %[d1], %[c1], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[t2], %[b2], %[a2], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[u2], %[d2], %[c2], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[t3], %[b3], %[a3], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[u3], %[d3], %[c3], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "s_mov_b32 vcc_lo, 0xaaaaaaaa\n\ts_mov_b32 vcc_hi, 0xaaaaaaaa\n\t"
+      "v_cndmask_b32_dpp %[b0], %[a0], %[b0], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[d0], %[c0], %[d0], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[b1], %[a1], %[b1], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[d1], %[c1], %[d1], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[b2], %[a2], %[b2], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[d2], %[c2], %[d2], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[b3], %[a3], %[b3], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[d3], %[c3], %[d3], vcc quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+      "s_mov_b32 vcc_lo, 0x33333333\n\ts_mov_b32 vcc_hi, 0x33333333\n\t"
+      "v_cndmask_b32_dpp %[a0], %[u0], %[t0], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[a1], %[u1], %[t1], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[a2], %[u2], %[t2], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[a3], %[u3], %[t3], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "s_mov_b32 vcc_lo, 0xcccccccc\n\ts_mov_b32 vcc_hi, 0xcccccccc\n\t"
+      "v_cndmask_b32_dpp %[c0], %[t0], %[u0], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[c1], %[t1], %[u1], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[c2], %[t2], %[u2], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[c3], %[t3], %[u3], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "s_mov_b32 vcc_lo, 0x33333333\n\ts_mov_b32 vcc_hi, 0x33333333\n\t"
+      "v_cndmask_b32_dpp %[t0], %[d0], %[b0], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[t1], %[d1], %[b1], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[t2], %[d2], %[b2], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[t3], %[d3], %[b3], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "s_mov_b32 vcc_lo, 0xcccccccc\n\ts_mov_b32 vcc_hi, 0xcccccccc\n\t"
+      "v_cndmask_b32_dpp %[d0], %[b0], %[d0], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[d1], %[b1], %[d1], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[d2], %[b2], %[d2], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "v_cndmask_b32_dpp %[d3], %[b3], %[d3], vcc quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1"
+      : [a0] "+&v"(a0), [a1] "+&v"(a1), [a2] "+&v"(a2), [a3] "+&v"(a3),
+        [b0] "+&v"(b0), [b1] "+&v"(b1), [b2] "+&v"(b2), [b3] "+&v"(b3),
+        [c0] "+&v"(c0), [c1] "+&v"(c1), [c2] "+&v"(c2), [c3] "+&v"(c3),
+        [d0] "+&v"(d0), [d1] "+&v"(d1), [d2] "+&v"(d2), [d3] "+&v"(d3),
+        [t0] "=&v"(t0), [t1] "=&v"(t1), [t2] "=&v"(t2), [t3] "=&v"(t3), [u0] "=&v"(u0), [u1] "=&v"(u1), [u2] "=&v"(u2), [u3] "=&v"(u3)
+      :
+      : "vcc");
+  v[0] = u32x4{a0, a1, a2, a3};
+  v[1] = u32x4{t0, t1, t2, t3};
+  v[2] = u32x4{c0, c1, c2, c3};
+  v[3] = u32x4{d0, d1, d2, d3};
+}
+
+// columns c0 .. c1 - 1 of the chunk's tokens nth[p0 .. p0 + cnt): out = base, a row a wave
+template <bool F32>
+__device__ __forceinline__ void copy_rows(const void* base, int64_t ldb, void* out, int64_t ldo, int64_t t0, int nth,
+                                          int p0, int cnt, int c0, int c1, int vec) {
+  constexpr int PER = F32 ? 4 : 8;
+  const int lane = lane_id();
+  for (int p = wave_id(); p < cnt; p += (int)blockDim.x / WAVE) {
+    const int64_t t = t0 + __builtin_amdgcn_readlane(nth, p0 + p);
+    int c = c0;
+    if (vec) {
+      for (c += lane * PER; c + PER <= c1; c += WAVE * PER) {
+        if constexpr (F32) *(u32x4*)((float*)out + t * ldo + c) = load16((const float*)base + t * ldb + c);
+        else *(u32x4*)((uint16_t*)out + t * ldo + c) = load16((const uint16_t*)base + t * ldb + c);
       }
-      continue;
+      c = c0 + max(c1 - c0, 0) / PER * PER;
     }
-    const int rank = adapter_rank(ranks, a, R);
-    __syncthreads();  // the previous adapter's parts are read
-    {
-      const float sc = scale ? scale[a] : 1.0f;
-      const int row = threadIdx.x / 16, i16 = threadIdx.x % 16;
-      for (int p0 = 0; p0 < m; p0 += 16) {
-        const int p = p0 + row;
-        const int tok = __builtin_amdgcn_ds_bpermute((p < m ? p : 0) << 2, nth);
-        const float* from = part + (t0 + tok) * R;
-        float v[RP / 16];
-        float top = 0.0f;
-#pragma unroll
-        for (int q = 0; q < RP / 16; ++q) {
-          const int r = i16 + 16 * q;
-          v[q] = 0.0f;
-          if (r < rank) {
-            for (int s = 0; s < S; ++s) v[q] += from[(int64_t)s * T * R + r];
-            v[q] *= sc;
-          }
-          top = fmaxf(top, fabsf(v[q]));
-        }
-        int e = 0;
-        if constexpr (ACT == ACT_F16) {
-          top = fmaxf(top, dpp_f<DPP_QUAD_1032>(top));
-          top = fmaxf(top, dpp_f<DPP_QUAD_2301>(top));
-          top = fmaxf(top, dpp_f<DPP_ROW_HALF_MIRROR>(top));
-          top = fmaxf(top, dpp_f<DPP_ROW_MIRROR>(top));
-          if (top > 0.0f && top < INFINITY) e = __builtin_amdgcn_frexp_expf(top) - 14;
-        }
-        if (p < m) {
-          if (i16 == 0) exps[p] = e;
-#pragma unroll
-          for (int q = 0; q < RP / 16; ++q) {
-            uint16_t o[NP];
-            split_parts<ACT, NP>(ACT == ACT_F16 ? ldexp_f(v[q], -e) : v[q], o);
-#pragma unroll
-            for (int i = 0; i < NP; ++i) vs[i][p][i16 + 16 * q] = o[i];
-          }
-        }
-      }
-    }
-    __syncthreads();
-    const int nt = (m + 15) / 16;
-    for (int b = b0 + wave; b < b1; b += 4) {
-      // D = B v^T: tile u's row i is column 8 (i / 4) + 4 u + i % 4 of the 32,
-      // so a lane ends with eight consecutive columns of one token
-      const int n0 = b * 32;
-      u32x4 bv[STEPS][2];
-#pragma unroll
-      for (int q = 0; q < STEPS; ++q)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int nr = n0 + l16 / 4 * 8 + 4 * u + l16 % 4;
-          const int r0 = RS == 0 ? g % 2 * 8 : 32 * q + 8 * g;
-          u32x4 w = u32x4{0u, 0u, 0u, 0u};
-          if (nr < N && r0 < rank) {
-            w = load16(bm + ((int64_t)a * N + nr) * R + r0);
-            if (r0 + 8 > rank) {  // columns past the rank may hold anything
-#pragma unroll
-              for (int h = 0; h < 4; ++h)
-                w[h] &= (r0 + 2 * h < rank ? 0xFFFFu : 0u) | (r0 + 2 * h + 1 < rank ? 0xFFFF0000u : 0u);
-            }
-          }
-          bv[q][u] = w;
-        }
-      for (int i = 0; i < nt; ++i) {
-        const int p = min(i * 16 + l16, m - 1);
-        const int64_t t = t0 + __builtin_amdgcn_ds_bpermute(p << 2, nth);
-        const int c = n0 + 8 * g;
-        const bool live = i * 16 + l16 < m;
-        const bool whole = vec && c + 8 <= N;
-        u32x4 o0 = u32x4{0u, 0u, 0u, 0u}, o1 = o0;
-        if (live && whole) {
-          if constexpr (F32) {
-            o0 = load16((const float*)base + t * ldb + c);
-            o1 = load16((const float*)base + t * ldb + c + 4);
-          } else {
-            o0 = load16((const uint16_t*)base + t * ldb + c);
-          }
-        }
-        f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-        for (int q = 0; q < STEPS; ++q) {
-          if constexpr (RS == 0) {
-            const u32x4 v01 = *(const u32x4*)&vs[g / 2][p][g % 2 * 8];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) acc[u] = mfma16<ACT>(bv[0][u], v01, acc[u]);
-            if constexpr (NP == 3) {
-              const u32x4 v2 = g < 2 ? *(const u32x4*)&vs[NP - 1][p][g * 8] : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-              for (int u = 0; u < 2; ++u) acc[u] = mfma16<ACT>(bv[0][u], v2, acc[u]);
-            }
-          } else {
-#pragma unroll
-            for (int h = NP - 1; h >= 0; --h) {  // small parts first
-              const u32x4 v = *(const u32x4*)&vs[h][p][32 * q + 8 * g];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) acc[u] = mfma16<ACT>(bv[q][u], v, acc[u]);
-            }
-          }
-        }
-        float d[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = acc[j / 4][j % 4];
-        if constexpr (ACT == ACT_F16) {
-          const int e = exps[p];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = ldexp_f(d[j], e);
-        }
-        if (live) {
-          if (whole) {
-            if constexpr (F32) {
-              f32x4 y0 = __builtin_bit_cast(f32x4, o0), y1 = __builtin_bit_cast(f32x4, o1);
-  #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                y0[j] = y0[j] + d[j];
-                y1[j] = y1[j] + d[j + 4];
-              }
-              *(f32x4*)((float*)out + t * ldo + c) = y0;
-              *(f32x4*)((float*)out + t * ldo + c + 4) = y1;
-            } else {
-              u32x4 y;
-  #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                y[j] = (uint32_t)f32_to_act_bits(act_to_f32(o0[j] & 0xFFFFu, ACT) + d[2 * j], ACT) |
-                       (uint32_t)f32_to_act_bits(act_to_f32(o0[j] >> 16, ACT) + d[2 * j + 1], ACT) << 16;
-              *(u32x4*)((uint16_t*)out + t * ldo + c) = y;
-            }
-          } else {
-  #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (c + j < N) {
-                if constexpr (F32)
-                  ((float*)out)[t * ldo + c + j] = ((const float*)base)[t * ldb + c + j] + d[j];
-                else
-                  ((uint16_t*)out)[t * ldo + c + j] =
-                      f32_to_act_bits(act_to_f32(((const uint16_t*)base)[t * ldb + c + j], ACT) + d[j], ACT);
-              }
-          }
-        }
-      }
+    for (c += lane; c < c1; c += WAVE) {
+      if constexpr (F32) ((float*)out)[t * ldo + c] = ((const float*)base)[t * ldb + c];
+      else ((uint16_t*)out)[t * ldo + c] = ((const uint16_t*)base)[t * ldb + c];
     }
   }
 }
 
-struct LoraGrid {
-  int chunks, J, S, NS;
+// the chunk's rows of a matrix of n columns of es bytes
+__device__ __forceinline__ rsrc_t chunk_rows(const void* p, int es, int64_t t0, int64_t ld, int T, int n) {
+  const int rows = (int)min((int64_t)CHUNK, T - t0);
+  return make_rsrc((const uint8_t*)p + t0 * ld * es, (uint32_t)(((rows - 1) * ld + n) * es));
+}
+
+// the parts of token p's v as operands: RT = 1 (up to 16 ranks) puts the first
+// two side by side in one instruction's 32 columns
+template <int RT, int NP, int STEPS, int ROWS, int PITCH>
+__device__ __forceinline__ void load_parts(const uint16_t (&vs)[NP][ROWS][PITCH], int p, u32x4 (&vv)[NP][STEPS]) {
+  const int g = lane_id() / 16;
+#pragma unroll
+  for (int h = 0; h < NP; ++h)
+#pragma unroll
+    for (int q = 0; q < STEPS; ++q) {
+      if constexpr (RT == 1)
+        vv[h][q] = h == 0 ? *(const u32x4*)&vs[g / 2][p][g % 2 * 8]
+                          : (h == 2 && g < 2 ? *(const u32x4*)&vs[NP - 1][p][g * 8] : u32x4{0u, 0u, 0u, 0u});
+      else
+        vv[h][q] = *(const u32x4*)&vs[h][p][32 * q + 8 * g];
+    }
+}
+
+// Columns n0 .. n0 + 31 of 16 tokens (token l16 of lane group g): D = B v^T,
+// where tile u's row i is column 8 (i / 4) + 4 u + i % 4 of the 32, so a lane
+// ends with eight consecutive columns of one token.  RT = 1: up to 16 ranks,
+// where one matrix instruction takes the first two parts of v side by side.
+// Loads and use are apart, so a wave has the next blocks' loads in flight.
+template <int RT>
+struct BRows {  // this lane's 16-byte pieces of 32 rows of B: RT of them, 32 / RT rows apart
+  static constexpr int PR = 2 * RT, STEP = WAVE / PR;  // pieces a row, rows a load
+  static constexpr int BP = RT * 32 + 16;  // bytes between rows in LDS: 16 consecutive rows start in different banks
+  rsrc_t b;
+  uint32_t from, row_bytes;
+  int to;
+  bool ragged;
+
+  __device__ __forceinline__ BRows(const uint16_t* bm, int a, int N, int R, int rank) {
+    const int row = lane_id() / PR, piece = lane_id() % PR;
+    b = make_rsrc(bm + (int64_t)a * N * R, (uint32_t)N * R * 2);
+    row_bytes = R * 2;
+    from = piece * 8 < rank ? row * row_bytes + piece * 16 : FAR;
+    to = row * BP + piece * 16;
+    ragged = rank % 8 != 0;
+  }
+  // the rows of columns 32 blk ...; from b1 on zeros that read nothing (2^30
+  // lies beyond B, and past FAR)
+  __device__ __forceinline__ void load(u32x4 (&raw)[RT], int blk, int b1) const {
+    const uint32_t off = from + (blk < b1 ? (uint32_t)(blk * 32) * row_bytes : 0x40000000u);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) raw[i] = buf_load16(b, off + (uint32_t)(i * STEP) * row_bytes);
+  }
 };
 
-// Adapters walked side by side (J) and splits of the reduced (S) and written
-// (NS) columns, from the sizes alone: the ids are on the device.
-LoraGrid lora_grid(int T, int K, int N, int L, int R) {
-  LoraGrid r;
-  r.chunks = (int)(((int64_t)T + CHUNK - 1) / CHUNK);
-  r.J = std::max(1, std::min(std::min(T, CHUNK), std::min(L, 512 / r.chunks)));
-  const int nbk = (K + 63) / 64, nbn = (N + 31) / 32;
-  const int work = r.chunks * std::min(r.J, 16);
-  r.S = std::max(1, std::min(std::min(16, nbk / 4), 1024 / work));
-  r.NS = std::max(1, std::min(std::min(32, nbn / 4), 2048 / work));
-  return r;
+// the loaded rows through LDS, from which every lane takes its own row's pieces
+template <int RT, int STEPS = RT == 1 ? 1 : RT / 2>
+__device__ __forceinline__ void take_rows(const u32x4 (&raw)[RT], const BRows<RT>& rows, int rank, uint8_t* lds,
+                                          u32x4 (&bv)[STEPS][2]) {
+  const int l16 = lane_id() % 16, g = lane_id() / 16;
+  wave_order();  // the block before is read
+#pragma unroll
+  for (int i = 0; i < RT; ++i) *(u32x4*)(lds + rows.to + i * BRows<RT>::STEP * BRows<RT>::BP) = raw[i];
+  wave_order();
+#pragma unroll
+  for (int q = 0; q < STEPS; ++q)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      bv[q][u] = *(const u32x4*)(lds + (l16 / 4 * 8 + 4 * u + l16 % 4) * BRows<RT>::BP +
+                                 (RT == 1 ? g % 2 * 16 : 64 * q + 16 * g));
+  if (rows.ragged) {
+    // columns past the rank may hold anything (whole pieces of them are zeros)
+    asm volatile("");  // a branch: these masks are not worth computing otherwise
+#pragma unroll
+    for (int q = 0; q < STEPS; ++q)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int r = (RT == 1 ? g % 2 * 8 : 32 * q + 8 * g) + 2 * h;
+        const uint32_t mask = (r < rank ? 0xFFFFu : 0u) | (r + 1 < rank ? 0xFFFF0000u : 0u);
+        bv[q][0][h] &= mask;
+        bv[q][1][h] &= mask;
+      }
+  }
+}
+
+// v B^T of the block's 32 columns: this lane's eight columns of its token
+template <int ACT, int RT, int NP, int STEPS = RT == 1 ? 1 : RT / 2>
+__device__ __forceinline__ void block_product(const u32x4 (&bv)[STEPS][2], const u32x4 (&vv)[NP][STEPS], int e,
+                                              float (&d)[8]) {
+  f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+  for (int q = 0; q < STEPS; ++q)
+#pragma unroll
+    for (int h = NP - 1; h >= 0; --h) {  // small parts first
+      if (RT == 1 && h == 1) continue;   // beside the first part
+#pragma unroll
+      for (int u = 0; u < 2; ++u) acc[u] = mfma16<ACT>(bv[q][u], vv[h][q], acc[u]);
+    }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) d[j] = ACT == ACT_F16 ? ldexp_f(acc[j / 4][j % 4], e) : acc[j / 4][j % 4];
+}
+
+// out = base + d for eight whole columns.  Non-temporal: in a long batch the
+// written rows otherwise push out the ones still to be read (4096 tokens, 4096
+// columns, rank 64: 51 against 67 us; rank 16: 34 against 46).
+template <int ACT, bool F32>
+__device__ __forceinline__ void add_store(const u32x4 (&o)[F32 ? 2 : 1], const float (&d)[8], void* out, int64_t io) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f32x4 y = __builtin_bit_cast(f32x4, o[h]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = y[j] + d[4 * h + j];
+      __builtin_nontemporal_store(y, (f32x4*)((float*)out + io + 4 * h));
+    }
+  } else {
+    u32x4 y;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      y[j] = pack2<ACT>(act_to_f32(o[0][j] & 0xFFFFu, ACT) + d[2 * j], act_to_f32(o[0][j] >> 16, ACT) + d[2 * j + 1]);
+    __builtin_nontemporal_store(y, (u32x4*)((uint16_t*)out + io));
+  }
+}
+
+// ----------------------------------------------------------- the kernel --
+//
+// Both products of a tile (up to 16 tokens of one adapter) in one workgroup
+// of eight waves: the waves take consecutive parts of K and are added through
+// LDS in wave order, the tokens' sums are split into the parts the matrix
+// cores take, and the waves share the output's columns.  Workgroup
+// (chunk, q, z) takes every Q-th of the chunk's tiles and the z-th part of the
+// output's columns, repeating the first product for each part.
+constexpr int FW = 8;  // waves
+
+template <int ACT, bool F32, int RT>
+__global__ __launch_bounds__(64 * FW) void lora_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+                                                       const uint16_t* __restrict__ am,
+                                                       const uint16_t* __restrict__ bm,
+                                                       const float* __restrict__ scale,
+                                                       const int32_t* __restrict__ ids,
+                                                       const int32_t* __restrict__ ranks, const void* base,
+                                                       int64_t ldb, void* out, int64_t ldo, int T, int L, int R, int K,
+                                                       int N, int vec) {
+  constexpr int NP = F32 && ACT == ACT_BF16 ? 3 : 2;
+  constexpr int STEPS = RT == 1 ? 1 : RT / 2;  // 32-rank steps of the second product
+  constexpr int RP = RT * 16, TILE = 16;
+  constexpr int RB = RT < 4 ? RT : RT == 8 ? 2 : 4;  // rank tiles loaded, and summed over the waves, together
+  constexpr int H = RT / RB;
+  // loads in flight a wave: items of the first product, and of the second
+  // base's blocks (from HBM) and B's (from L2).  Sixteen waves a CU (128
+  // registers) overlap two workgroups.
+  constexpr int DEEP = RT == 4 ? 1 : 2;
+  constexpr int TURN = DEEP < H ? H : DEEP;
+  constexpr int AHEAD = F32 ? 2 : 4, BAHEAD = RT == 8 ? 1 : 2;
+  constexpr int OV = F32 ? 2 : 1;
+  constexpr int VR = (RP + WAVE - 1) / WAVE;
+  union Shared {
+    f32x4 red[FW][RB][WAVE];
+    uint8_t b[FW][32 * BRows<RT>::BP];
+  };
+  __shared__ __attribute__((aligned(16))) Shared sh;
+  __shared__ float vsum[TILE][RP + 4];
+  __shared__ __attribute__((aligned(16))) uint16_t vs[NP][TILE][RP + 8];
+  __shared__ int exps[TILE];
+  const int lane = lane_id(), wave = wave_id();
+  const int l16 = lane % 16, g = lane / 16;
+  const int64_t t0 = (int64_t)blockIdx.x * CHUNK;
+  const int id = chunk_id(ids, t0, T, L);
+  const int kb = (K + 127) / 128, k0 = kb * wave / FW, k1 = kb * (wave + 1) / FW;
+  const int nb = (N + 31) / 32;
+  const int per = (nb + (int)gridDim.z - 1) / (int)gridDim.z;
+  const int b0 = min(nb, (int)blockIdx.z * per), b1 = min(nb, b0 + per);
+  const rsrc_t rx = chunk_rows(x, 2, t0, ldx, T, K);
+  const rsrc_t rb = chunk_rows(base, F32 ? 4 : 2, t0, ldb, T, N);
+  uint64_t left = __ballot(id >= -1);
+  int seen = 0, turn = blockIdx.y;  // tiles walked past, and the next one of this workgroup
+  while (left != 0) {
+    const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
+    const uint64_t mine = __ballot(id == a);
+    left &= ~mine;
+    const int m = (int)__popcll(mine);
+    const int tiles = (m + TILE - 1) / TILE;
+    if (turn >= seen + tiles) {
+      seen += tiles;
+      continue;
+    }
+    const int nth = nth_lane(mine);
+    for (; turn < seen + tiles; turn += gridDim.y) {
+      const int p0 = (turn - seen) * TILE, cnt = min(TILE, m - p0);
+      if (a < 0) {
+        // no adapter: out is base, moved only if the two are not one buffer
+        if (out != base) copy_rows<F32>(base, ldb, out, ldo, t0, nth, p0, cnt, b0 * 32, min(N, b1 * 32), vec);
+        continue;
+      }
+      const int rank = adapter_rank(ranks, a, R);
+      // sizes the compiler must not know from here on: it would keep every
+      // product of them in registers over the loop, and spill
+      asm volatile("" : "+s"(K), "+s"(N), "+s"(R));
+
+      // ---- x A^T over this wave's columns.  A: load j is this lane's piece of
+      // row lrow + j of a 16-row tile, eight columns from lcol of a 128-column
+      // block, and the quad transpose makes it columns 32 g + 8 j of row l16.
+      // x, read once, comes in that place.
+      const bool have = l16 < cnt;
+      const int tok = __builtin_amdgcn_ds_bpermute((p0 + (have ? l16 : 0)) << 2, nth);
+      const int64_t t = t0 + tok;
+      const uint32_t xoff = have ? (uint32_t)tok * (uint32_t)ldx * 2 + g * 64 : FAR;
+      const uint32_t at = have && vec ? (uint32_t)tok * (uint32_t)ldb * (F32 ? 4 : 2) + g * (F32 ? 32 : 16) : FAR;
+      f32x4 acc[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      const rsrc_t ra = make_rsrc(am + (int64_t)a * R * K, (uint32_t)rank * K * 2);  // rows up to the rank
+      const int lrow = lane / 4 % 4 * 4, lcol = g * 32 + lane % 4 * 8;
+      const uint32_t aoff = (uint32_t)(lrow * K + lcol) * 2;
+      struct Item {
+        u32x4 x[4], a[RB][4];
+      } it[DEEP];
+      const int items = (k1 - k0) * H;
+      auto load = [&](Item& t, int i, int r0) __attribute__((always_inline)) {  // r0 = i % H * RB
+        const int c = (k0 + i / H) * 128;
+        const int end = i < items ? K : 0;  // past the last item: zeros, unread
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t.x[j] = buf_load16(rx, c + g * 32 + 8 * j < end ? xoff + (c + 8 * j) * 2 : FAR);
+        const uint32_t off = c + lcol < end ? aoff + c * 2 : FAR;
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t.a[r][j] = buf_load16(ra, off + (uint32_t)(((r0 + r) * 16 + j) * K) * 2);
+      };
+#pragma unroll
+      for (int h = 0; h < DEEP; ++h) load(it[h], h, h % H * RB);
+#pragma unroll 1
+      for (int i = 0; i < items; i += TURN) {
+#pragma unroll
+        for (int h = 0; h < TURN; ++h) {
+          Item& now = it[h % DEEP];
+#pragma unroll
+          for (int r = 0; r < RB; ++r) {
+            quad_transpose(now.a[r]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[h % H * RB + r] = mfma16<ACT>(now.a[r][j], now.x[j], acc[h % H * RB + r]);
+          }
+          load(now, i + h + DEEP, (h + DEEP) % H * RB);
+        }
+      }
+
+      // ---- the second product's first loads, which do not wait for the sums
+      const BRows<RT> rows(bm, a, N, R, rank);
+      u32x4 braw[BAHEAD][RT], o[AHEAD][OV];
+      auto load_o = [&](u32x4 (&v)[OV], int blk) __attribute__((always_inline)) {
+        const uint32_t off = blk < b1 && blk * 32 + 8 * g + 8 <= N ? at + (uint32_t)(blk * 32) * (F32 ? 4 : 2) : FAR;
+#pragma unroll
+        for (int h = 0; h < OV; ++h) v[h] = buf_load16(rb, off + 16 * h);
+      };
+#pragma unroll
+      for (int h = 0; h < BAHEAD; ++h) rows.load(braw[h], b0 + wave + FW * h, b1);
+#pragma unroll
+      for (int h = 0; h < AHEAD; ++h) load_o(o[h], b0 + wave + FW * h);
+
+      // ---- the waves' sums, token by token as 16-bit parts
+#pragma unroll
+      for (int r0 = 0; r0 < RT; r0 += RB) {
+        __syncthreads();  // the last tile's B rows, or the sums before these, are read
+#pragma unroll
+        for (int r = 0; r < RB; ++r) sh.red[wave][r][lane] = acc[r0 + r];
+        __syncthreads();
+        for (int i = threadIdx.x; i < RB * 256; i += 64 * FW) {
+          float v = 0.0f;
+#pragma unroll
+          for (int w = 0; w < FW; ++w) v += ((const float*)sh.red[w])[i];
+          vsum[i / 4 % 16][(r0 + i / 256) * 16 + i % 256 / 64 * 4 + i % 4] = v;
+        }
+      }
+      __syncthreads();
+      const float sc = scale ? scale[a] : 1.0f;
+      for (int p = wave; p < TILE; p += FW) {
+        float v[VR], top = 0.0f;
+#pragma unroll
+        for (int q = 0; q < VR; ++q) {
+          const int r = lane + WAVE * q;
+          v[q] = r < RP ? vsum[p][r] * sc : 0.0f;
+          top = fmaxf(top, fabsf(v[q]));
+        }
+        int e = 0;
+        if constexpr (ACT == ACT_F16) {
+          top = wave_max(top);
+          if (top > 0.0f && top < INFINITY) e = __builtin_amdgcn_frexp_expf(top) - 14;
+          if (lane == 0) exps[p] = e;
+        }
+#pragma unroll
+        for (int q = 0; q < VR; ++q) {
+          const int r = lane + WAVE * q;
+          uint16_t parts[NP];
+          split_parts<ACT, NP>(ACT == ACT_F16 ? ldexp_f(v[q], -e) : v[q], parts);
+          if (r < RP) {
+#pragma unroll
+            for (int h = 0; h < NP; ++h) vs[h][p][r] = parts[h];
+          }
+        }
+      }
+      __syncthreads();
+
+      // ---- base + v B^T: this wave's every FW-th block of 32 columns
+      u32x4 vv[NP][STEPS];
+      load_parts<RT>(vs, l16, vv);
+      const int e = ACT == ACT_F16 ? exps[l16] : 0;
+      const int whole = vec ? min(b1, N / 32) : b0;  // blocks of 32 columns that can be moved in 16 bytes
+      int b = b0 + wave;
+#pragma unroll 1
+      for (; b < whole; b += FW * AHEAD) {
+#pragma unroll
+        for (int h = 0; h < AHEAD; ++h) {
+          const int now = b + FW * h;
+          if (now < whole) {
+            u32x4 bv[STEPS][2];
+            take_rows<RT>(braw[h % BAHEAD], rows, rank, sh.b[wave], bv);
+            rows.load(braw[h % BAHEAD], now + FW * BAHEAD, b1);
+            float d[8];
+            block_product<ACT, RT, NP>(bv, vv, e, d);
+            if (have) add_store<ACT, F32>(o[h], d, out, t * ldo + now * 32 + 8 * g);
+            load_o(o[h], now + FW * AHEAD);
+          }
+        }
+      }
+      // the others, element by element
+      b = b0 + wave + (max(whole - b0 - wave, 0) + FW - 1) / FW * FW;
+#pragma unroll 1
+      for (; b < b1; b += FW) {
+        u32x4 bv[STEPS][2];
+        rows.load(braw[0], b, b1);
+        take_rows<RT>(braw[0], rows, rank, sh.b[wave], bv);
+        float d[8];
+        block_product<ACT, RT, NP>(bv, vv, e, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int c = b * 32 + 8 * g + j;
+          if (have && c < N) {
+            if constexpr (F32)
+              ((float*)out)[t * ldo + c] = ((const float*)base)[t * ldb + c] + d[j];
+            else
+              ((uint16_t*)out)[t * ldo + c] =
+                  (uint16_t)pack2<ACT>(act_to_f32(((const uint16_t*)base)[t * ldb + c], ACT) + d[j], 0.0f);
+          }
+        }
+      }
+    }
+    seen += tiles;
+  }
 }
 
 }  // namespace
 
-int64_t lora_partial_floats(int T, int K, int N, int L, int R) {
-  return (int64_t)lora_grid(T, K, N, L, R).S * T * R;
-}
-
 hipError_t launch_lora(const void* x, int act, int64_t ldx, int T, const LoraDev& ad, const int32_t* ids,
-                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, float* part,
-                       hipStream_t st) {
-  const LoraGrid lg = lora_grid(T, ad.K, ad.N, ad.L, ad.R);
+                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, hipStream_t st) {
   const int per = out_f32 ? 4 : 8;  // elements of 16 bytes
   const int vec = ldb % per == 0 && ldo % per == 0 &&
                   ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-  const dim3 gs(lg.chunks, lg.J, lg.S), ge(lg.chunks, lg.J, lg.NS);
-  auto shrink = [&](auto kern) {
-    return launch_kernel(kern, gs, 256, 0, st, (const uint16_t*)x, ldx, (const uint16_t*)ad.a, ids, ad.ranks, part, T,
-                         ad.L, ad.R, ad.K);
+  const int chunks = (int)(((int64_t)T + CHUNK - 1) / CHUNK);
+  // About 256 workgroups side by side, from the sizes alone (the ids are on the
+  // device).  Few tokens cannot fill the chip with tiles: the output's columns
+  // are split, at the price of repeating x A^T (K = N = 4096: one token, rank
+  // 16: 8.3 us in eight parts, 12.7 in one; 64 tokens of 48 adapters, rank 32:
+  // 15.2 in four, 22.7 in one; 512 tokens of 48 adapters: 52 in two, 41 in one).
+  const int parts = T <= 16 ? 8 : T <= 128 ? 4 : T <= 256 ? 2 : 1;
+  const int Q = std::max(1, std::min(std::min(T, CHUNK), 256 / chunks));
+  const dim3 grid(chunks, Q, std::max(1, std::min(parts, (ad.N + 31) / 32 / FW)));
+  auto go = [&](auto kern) {
+    return launch_kernel(kern, grid, 64 * FW, 0, st, (const uint16_t*)x, ldx, (const uint16_t*)ad.a,
+                         (const uint16_t*)ad.b, ad.scale, ids, ad.ranks, base, ldb, out, ldo, T, ad.L, ad.R, ad.K, ad.N,
+                         vec);
   };
-  auto expand = [&](auto kern) {
-    return launch_kernel(kern, ge, 256, 0, st, (const float*)part, lg.S, (const uint16_t*)ad.b, ad.scale, ids,
-                         ad.ranks, base, ldb, out, ldo, T, ad.L, ad.R, ad.N, vec);
-  };
-  auto run = [&](auto ac) {
+  auto rank = [&](auto ac, auto fc) {
     constexpr int A = decltype(ac)::value;
-    hipError_t e = ad.R <= 16   ? shrink(lora_shrink_kernel<A, 1>)
-                   : ad.R <= 32 ? shrink(lora_shrink_kernel<A, 2>)
-                   : ad.R <= 64 ? shrink(lora_shrink_kernel<A, 4>)
-                                : shrink(lora_shrink_kernel<A, 8>);
-    if (e != hipSuccess) return e;
-    auto go = [&](auto fc) {
-      constexpr bool F = decltype(fc)::value;
-      return ad.R <= 16   ? expand(lora_expand_kernel<A, F, 0>)
-             : ad.R <= 32 ? expand(lora_expand_kernel<A, F, 1>)
-             : ad.R <= 64 ? expand(lora_expand_kernel<A, F, 2>)
-                          : expand(lora_expand_kernel<A, F, 4>);
-    };
-    return out_f32 ? go(std::true_type{}) : go(std::false_type{});
+    constexpr bool F = decltype(fc)::value;
+    return ad.R <= 16   ? go(lora_kernel<A, F, 1>)
+           : ad.R <= 32 ? go(lora_kernel<A, F, 2>)
+           : ad.R <= 64 ? go(lora_kernel<A, F, 4>)
+                        : go(lora_kernel<A, F, 8>);
   };
-  return act == ACT_BF16 ? run(std::integral_constant<int, ACT_BF16>{}) : run(std::integral_constant<int, ACT_F16>{});
+  auto type = [&](auto ac) { return out_f32 ? rank(ac, std::true_type{}) : rank(ac, std::false_type{}); };
+  return act == ACT_BF16 ? type(std::integral_constant<int, ACT_BF16>{}) : type(std::integral_constant<int, ACT_F16>{});
 }
 
 }  // namespace moe

@@ -860,14 +860,9 @@ moe_status moe_gate_backward(const void* logits, moe_dtype lt, int64_t ld, int32
   }
 }
 
-size_t moe_lora_workspace_size(int32_t T, int32_t K, int32_t N, int32_t L, int32_t R) {
-  if (T < 1 || K < 1 || N < 1 || L < 1 || R < 1) return 0;
-  return align_up((size_t)moe::lora_partial_floats(T, K, N, L, R) * 4);
-}
-
 moe_status moe_lora_add(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const moe_lora* lora, const int32_t* ids,
-                        const void* base, int64_t ld_base, void* out, int64_t ld_out, moe_dtype out_dt, void* ws,
-                        size_t ws_bytes, void* stream) {
+                        const void* base, int64_t ld_base, void* out, int64_t ld_out, moe_dtype out_dt,
+                        void* stream) {
   try {
     if (!lora || !lora->a || !lora->b) return MOE_ERR_NULL;
     if (!half_type(dt) || (out_dt != dt && out_dt != MOE_F32)) return MOE_ERR_DTYPE;
@@ -876,24 +871,24 @@ moe_status moe_lora_add(const void* x, moe_dtype dt, int64_t ldx, int32_t T, con
         R > MOE_LORA_MAX_RANK)
       return MOE_ERR_SHAPE;
     if (ldx < K || ldx % 8 != 0 || ld_base < N || ld_out < N) return MOE_ERR_SHAPE;
+    // 32-bit offsets within an adapter and within 64 tokens' rows
+    if (K > MOE_LORA_MAX_COLUMNS || N > MOE_LORA_MAX_COLUMNS || ldx > MOE_LORA_MAX_COLUMNS ||
+        ld_base > MOE_LORA_MAX_COLUMNS)
+      return MOE_ERR_SHAPE;
     if (!aligned16(lora->a) || !aligned16(lora->b) || !aligned4(lora->scale) || !aligned4(lora->ranks))
       return MOE_ERR_ALIGN;
     if (T == 0) return MOE_OK;
     if (!x || !ids || !base || !out) return MOE_ERR_NULL;
     if (!aligned16(x) || !aligned4(ids) || !aligned_to(base, out_dt) || !aligned_to(out, out_dt)) return MOE_ERR_ALIGN;
     if (base == out && ld_base != ld_out) return MOE_ERR_SHAPE;  // in place: the same rows
-    if (!ws || ws_bytes < moe_lora_workspace_size(T, lora->K, lora->N, lora->L, lora->R)) return MOE_ERR_WORKSPACE;
-    if (!aligned16(ws)) return MOE_ERR_ALIGN;
     DevProps props;
     moe_status s = device_props(&props);
     if (s != MOE_OK) return s;
     hipStream_t st = (hipStream_t)stream;
     plan_begin(st);
     const moe::LoraDev ad{lora->a, lora->b, lora->scale, lora->ranks, lora->L, lora->R, lora->K, lora->N};
-    HIP_TRY(moe::launch_lora(x, (int)dt, ldx, T, ad, ids, base, ld_base, out, ld_out, out_dt == MOE_F32, (float*)ws,
-                             st));
-    plan_step("lora_shrink", st);
-    plan_step("lora_expand", st);
+    HIP_TRY(moe::launch_lora(x, (int)dt, ldx, T, ad, ids, base, ld_base, out, ld_out, out_dt == MOE_F32, st));
+    plan_step("lora", st);
     return MOE_OK;
   } catch (...) {
     return MOE_ERR_INTERNAL;

@@ -120,11 +120,10 @@ def test_gated_layer_refusals():
 
 
 def lora(x=P, dt=1, ldx=None, T=4, a=P, b=P, scale=None, ranks=None, L=3, R=16, K=64, N=48, ids=P, base=P, ldb=None,
-         out=P + (1 << 16), ldo=None, odt=1, ws=P, nbytes=None):
+         out=P + (1 << 16), ldo=None, odt=1):
     lib = moe.lib()
-    n = lib.moe_lora_workspace_size(T, K, N, L, R) if nbytes is None else nbytes
     return moe.STATUS[lib.moe_lora_add(x, dt, K if ldx is None else ldx, T, moe.CLora(a, b, scale, ranks, L, R, K, N),
-                                       ids, base, N if ldb is None else ldb, out, N if ldo is None else ldo, odt, ws, n,
+                                       ids, base, N if ldb is None else ldb, out, N if ldo is None else ldo, odt,
                                        None)]
 
 
@@ -139,18 +138,16 @@ def lora(x=P, dt=1, ldx=None, T=4, a=P, b=P, scale=None, ranks=None, L=3, R=16, 
     (dict(out=P, ldo=56), "MOE_ERR_SHAPE"), (dict(x=P + 8), "MOE_ERR_ALIGN"), (dict(a=P + 8), "MOE_ERR_ALIGN"),
     (dict(b=P + 2), "MOE_ERR_ALIGN"), (dict(scale=P + 2), "MOE_ERR_ALIGN"), (dict(ranks=P + 1), "MOE_ERR_ALIGN"),
     (dict(ids=P + 2), "MOE_ERR_ALIGN"), (dict(base=P + 1), "MOE_ERR_ALIGN"), (dict(out=P + 1), "MOE_ERR_ALIGN"),
-    (dict(odt=3, out=P + 2), "MOE_ERR_ALIGN"), (dict(ws=None), "MOE_ERR_WORKSPACE"),
-    (dict(nbytes=16), "MOE_ERR_WORKSPACE"), (dict(ws=P + 8), "MOE_ERR_ALIGN"),
+    (dict(odt=3, out=P + 2), "MOE_ERR_ALIGN"), (dict(ldx=(1 << 22) + 8), "MOE_ERR_SHAPE"),
+    (dict(ldb=(1 << 22) + 1), "MOE_ERR_SHAPE"), (dict(K=(1 << 22) + 8), "MOE_ERR_SHAPE"),
+    (dict(N=(1 << 22) + 8), "MOE_ERR_SHAPE"), (dict(T=(1 << 25) + 1), "MOE_ERR_SHAPE"),
 ])
 def test_lora_refusals(kw, status):
     assert lora(**kw) == status
 
 
-def test_lora_zero_tokens_and_workspace():
-    assert lora(T=0, x=None, ids=None, base=None, out=None, ws=None, nbytes=0) == "MOE_OK"
-    assert moe.lora_workspace_size(0, 64, 64, 1, 8) == 0
-    for T, K, N, L, R in ((1, 8, 1, 1, 8), (64, 4096, 4096, 48, 32), (70000, 4096, 64, 3, 128)):
-        assert moe.lora_workspace_size(T, K, N, L, R) >= T * R * 4
+def test_lora_zero_tokens():
+    assert lora(T=0, x=None, ids=None, base=None, out=None) == "MOE_OK"
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="the device check passes on a GPU")

@@ -177,22 +177,20 @@ def test_streams_and_graph_replays():
     torch.cuda.synchronize()
     sides = [torch.cuda.Stream() for _ in range(2)]
     got = []
-    for s in sides:  # two calls at once, a workspace each
+    for s in sides:  # two calls at once
         s.wait_stream(torch.cuda.current_stream())
         got.append(moe.lora_add(**d, stream=s))
     for s in sides:
         s.synchronize()
     assert all(torch.equal(g, want) for g in got)
     out = torch.empty_like(want)
-    ws = torch.empty(moe.lora_workspace_size(96, 512, 256, 8, 32), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        moe.lora_add(**d, out=out, workspace=ws)
+        moe.lora_add(**d, out=out)
     for i in range(4):
         n = make(50 + i, 96, 512, 256, 8, 32)
         d["x"].copy_(n["x"])
         d["ids"].copy_(n["ids"])
-        ws.random_(0, 255)  # nothing is kept in the workspace from call to call
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, moe.lora_add(**d))
@@ -206,7 +204,6 @@ def test_argument_errors():
         (dict(ids=c["ids"][:5]), ValueError), (dict(ids=c["ids"].cpu()), ValueError), (dict(base=c["base"][:5]), ValueError),
         (dict(scale=torch.zeros(2, device="cuda")), ValueError), (dict(ranks=torch.zeros(3, device="cuda")), TypeError),
         (dict(out=c["base"].float()), TypeError), (dict(out=c["base"][:, :31]), ValueError),
-        (dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), moe.MoeError),
         (dict(a=c["a"][:, :4], b=c["b"][:, :, :4]), ValueError),
         (dict(a=c["a"][:, :4].contiguous(), b=c["b"][:, :, :4].contiguous()), moe.MoeError),
     ):
