@@ -411,23 +411,27 @@ _TYPES = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F
 
 
 def _elsewhere(t: torch.Tensor, stream):
-    """The context in which a call on tensor `t` runs, or None where that is the
-    current device and stream already.  Under `stream`, what the call allocates
-    belongs to that stream."""
+    """The context for a call that is not on tensor `t`'s GPU or not on `stream`
+    yet.  Under `stream`, what the call allocates belongs to that stream."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensors must be on the GPU, got one on %s" % t.device)
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
-        return torch.cuda.stream(stream)
-    if dev != torch.cuda.current_device():
+    if stream is None:
         return torch.cuda.device(dev)
-    return None
+    if stream.device != t.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+    return torch.cuda.stream(stream)
 
 
-# the current stream's handle without a Stream object (2 us less a call)
+# the current device and stream's handle without Python objects (2 us less a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(t: torch.Tensor, stream) -> bool:
+    """Whether `t` is on the current GPU and no other stream is asked for."""
+    dev = t.get_device()
+    return stream is None and dev >= 0 and dev == _raw_device()
 
 
 def _current(dev: int) -> int:
@@ -449,21 +453,30 @@ def _operand(t: Optional[torch.Tensor], name: str, dev: int, dtype, shape):
 
 
 def _rows(t: torch.Tensor, name: str):
-    """(T, columns, elements between rows) of a matrix whose rows are dense."""
+    """(t, T, columns, elements between rows) of a matrix whose rows are dense and
+    do not overlap: `t` itself or, if it is none, a copy."""
     if t.dim() != 2:
         raise ValueError("%s must have two dimensions, got shape %s" % (name, tuple(t.shape)))
     T, n = t.shape
     ld, step = t.stride()
-    if step != 1 and n > 1:
-        raise ValueError("%s: the elements of a row must be adjacent" % name)
-    return T, n, ld if T > 1 else n
+    if step == 1 and (ld >= n or T < 2):
+        return t, T, n, ld if T > 1 else n
+    return t.contiguous(), T, n, n
 
 
-def _dense_rows(t: torch.Tensor) -> torch.Tensor:
-    """`t`, or a dense copy where its rows are not dense or overlap."""
-    if t.dim() == 2 and t.stride(1) == 1 and (t.stride(0) >= t.shape[1] or t.shape[0] < 2):
-        return t
-    return t.contiguous()
+def _out_rows(t: torch.Tensor, name: str, dev: int, dtype, shape) -> int:
+    """Elements between the dense rows of the caller's output."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape or t.get_device() != dev:
+        raise ValueError("%s must have shape %s on GPU %d, got %s on %s" %
+                         (name, tuple(shape), dev, tuple(t.shape), t.device))
+    ld, step = t.stride()
+    if shape[0] < 2:
+        ld = shape[1]
+    if (step != 1 and shape[1] > 1) or ld < shape[1]:
+        raise ValueError("%s: rows must be dense and apart" % name)
+    return ld
 
 
 def _gate_opts(dev: int, E: int, score: str, bias, groups: int, group_k: int, group_best: int, renorm: bool,
@@ -503,14 +516,12 @@ def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bi
     experts of the group_k best of `groups` groups can be chosen, a group being
     worth the sum of its group_best best keys; renorm: the weights of a token
     sum to `scale` (moe_gate_opts).  out: (idx, w) to write into."""
-    ctx = _elsewhere(logits, stream)
-    if ctx is not None:
-        with ctx:
+    if not _here(logits, stream):
+        with _elsewhere(logits, stream):
             return gate_from_logits(logits, k, score=score, bias=bias, groups=groups, group_k=group_k,
                                     group_best=group_best, renorm=renorm, scale=scale, out=out)
     code = _gate_type(logits)
-    logits = _dense_rows(logits)
-    T, E, ld = _rows(logits, "logits")
+    logits, T, E, ld = _rows(logits, "logits")
     dev = logits.get_device()
     o = _gate_opts(dev, E, score, bias, groups, group_k, group_best, renorm, scale)
     idx, w = _routing_out(logits, T, k, out)
@@ -524,9 +535,8 @@ def gate(x: torch.Tensor, router_w: torch.Tensor, k: int, *, score: str = "softm
          renorm: bool = True, scale: float = 1.0, want_logits: bool = False, out=None, stream=None):
     """Router projection of x [T, H] and the gate on its fp32 logits (options as
     in gate_from_logits): dict(idx, w[, logits])."""
-    ctx = _elsewhere(x, stream)
-    if ctx is not None:
-        with ctx:
+    if not _here(x, stream):
+        with _elsewhere(x, stream):
             return gate(x, router_w, k, score=score, bias=bias, groups=groups, group_k=group_k,
                         group_best=group_best, renorm=renorm, scale=scale, want_logits=want_logits, out=out)
     code = _dtype_code(x)
@@ -554,13 +564,11 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
     their type: idx [T, k] int32 as the gate returned it, grad_w [T, k] float32,
     score, renorm and scale as in the forward call (a bias and groups only
     select: they change nothing here)."""
-    ctx = _elsewhere(logits, stream)
-    if ctx is not None:
-        with ctx:
+    if not _here(logits, stream):
+        with _elsewhere(logits, stream):
             return gate_backward(logits, idx, grad_w, score=score, renorm=renorm, scale=scale, out=out)
     code = _gate_type(logits)
-    logits = _dense_rows(logits)
-    T, E, ld = _rows(logits, "logits")
+    logits, T, E, ld = _rows(logits, "logits")
     if idx.dim() != 2:
         raise ValueError("idx must have two dimensions")
     k = idx.shape[1]
@@ -570,12 +578,7 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
     if out is None:
         g, ldg = logits.new_empty((T, E)), E
     else:
-        g = out
-        if g.dtype != logits.dtype:
-            raise TypeError("out must be %s, got %s" % (logits.dtype, g.dtype))
-        if g.shape != logits.shape or g.device != logits.device:
-            raise ValueError("out must have the logits' shape and device")
-        _, _, ldg = _rows(g, "out")
+        g, ldg = out, _out_rows(out, "out", dev, logits.dtype, (T, E))
     o = _gate_opts(dev, E, score, None, 0, 0, 1, renorm, scale)
     _check(lib().moe_gate_backward(logits.data_ptr(), code, ld, T, E, k, o, pi, pg, g.data_ptr(), ldg, _current(dev)),
            "moe_gate_backward")
@@ -591,9 +594,8 @@ def layer_forward_gated(x: torch.Tensor, router_w: Optional[torch.Tensor], k: in
                         renorm: bool = True, scale: float = 1.0, capacity: int = 0) -> torch.Tensor:
     """layer_forward with the gate's routing (options as in gate_from_logits).
     logits [T, E] float32, with router_w None: the caller's router logits."""
-    ctx = _elsewhere(x, stream)
-    if ctx is not None:
-        with ctx:
+    if not _here(x, stream):
+        with _elsewhere(x, stream):
             return layer_forward_gated(x, router_w, k, down, gate_up, gate, up, flags, taps, out, workspace,
                                        logits=logits, score=score, bias=bias, groups=groups, group_k=group_k,
                                        group_best=group_best, renorm=renorm, scale=scale, capacity=capacity)
@@ -631,9 +633,8 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
     token without an adapter; scale [L] float32; ranks [L] int32, the ranks in
     use of adapters smaller than R.  out: written instead of a new tensor; pass
     base itself to add in place."""
-    ctx = _elsewhere(x, stream)
-    if ctx is not None:
-        with ctx:
+    if not _here(x, stream):
+        with _elsewhere(x, stream):
             return lora_add(x, base, ids, a, b, scale=scale, ranks=ranks, out=out)
     dtype, odt = x.dtype, base.dtype
     code = _dtype_code(x)
@@ -641,8 +642,7 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
         raise TypeError("base must be %s or float32, got %s" % (dtype, odt))
     if a.dim() != 3 or b.dim() != 3 or base.dim() != 2:
         raise ValueError("a and b must have three dimensions, base two")
-    x = _dense_rows(x)
-    T, K, ldx = _rows(x, "x")
+    x, T, K, ldx = _rows(x, "x")
     if ldx % 8 or x.data_ptr() % 16:
         x, ldx = x.clone(memory_format=torch.contiguous_format), K
     dev = x.get_device()
@@ -654,17 +654,14 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
                  L, R, K, N)
     pids = _operand(ids, "ids", dev, torch.int32, (T,))
     if out is None:
-        base = _dense_rows(base)
+        base, _, _, ldb = _rows(base, "base")
         out, ldo = base.new_empty((T, N)), N
     else:
-        if out.dtype is not odt:
-            raise TypeError("out must be %s, got %s" % (odt, out.dtype))
-        if out.shape != base.shape or out.get_device() != dev:
-            raise ValueError("out must have base's shape and device")
-        if out is not base:
-            base = _dense_rows(base)
-        _, _, ldo = _rows(out, "out")
-    _, _, ldb = _rows(base, "base")
+        ldo = _out_rows(out, "out", dev, odt, (T, N))
+        if out is base:
+            ldb = ldo
+        else:
+            base, _, _, ldb = _rows(base, "base")
     _check(lib().moe_lora_add(x.data_ptr(), code, ldx, T, lora, pids, base.data_ptr(), ldb, out.data_ptr(), ldo,
                               _TYPES[odt], _current(dev)), "moe_lora_add")
     return out

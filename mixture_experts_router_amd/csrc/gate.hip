@@ -258,12 +258,12 @@ __device__ __forceinline__ int exact_experts(const void* __restrict__ logits, in
 
 // ------------------------------------------------------ sorting networks --
 //
-// A key and its expert as one double in [1, 2): the 32 key bits, then 256 - e,
-// in the mantissa.  Larger key first, lower index first among equal keys is
-// then the order of the doubles, and a comparator is v_max_f64 + v_min_f64
-// (full rate, like fp32).
-__device__ __forceinline__ double pack_key(uint32_t key, int e) {
-  const uint32_t hi = __builtin_amdgcn_alignbit(0x3FFu, key, 12), lo = (key << 20) | (uint32_t)(256 - e) << 11;
+// A key and its place j < 16 in the lane as one double in [1, 2): the 32 key
+// bits, then 15 - j, in the mantissa.  Larger key first, lower index first
+// among equal keys is then the order of the doubles, and a comparator is
+// v_max_f64 + v_min_f64 (full rate, like fp32).
+__device__ __forceinline__ double pack_key(uint32_t key, int j) {
+  const uint32_t hi = __builtin_amdgcn_alignbit(0x3FFu, key, 12), lo = (key << 20) | (uint32_t)(15 - j);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
@@ -316,7 +316,7 @@ constexpr int GATE_WAVE_WORDS = 9 * 64 * 2;  // LDS words a wave: nine list entr
                                              // tokens' keys, or one double per expert of one token
 static_assert(GATE_WAVE_WORDS >= 4 * GATE_PITCH && GATE_WAVE_WORDS >= 2 * 256, "LDS of a wave");
 
-template <int EPL, int LT>
+template <int EPL, int LT, bool by_score>
 __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ logits, int64_t ld, int vec, int T, int E,
                                                    int k, GateDev g, int32_t* __restrict__ idx,
                                                    float* __restrict__ w, int32_t* __restrict__ k_used,
@@ -363,7 +363,6 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
   }
 
   // ---- keys
-  const bool by_score = g.bias != nullptr || (g.groups > 1 && g.group_best == 2);
   const bool softmax = g.score == GATE_SOFTMAX;
   float m_all = 0.0f, z_all = 1.0f, window = 0x1p-20f;  // softmax over all experts; sigmoid's window
   bool unsure = false;
@@ -480,8 +479,9 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
         int may = 0, must = 0;
         for (int h = 0; h < G; ++h) {
           const uint32_t hl = row[2 * h], hh = row[2 * h + 1];
-          may += (int)(h != gg) & ((int)(hh > low[q]) | ((int)(hh == low[q]) & ((int)by_score | (int)(h < gg))));
-          must += (int)(hl > high[q]);
+          may += by_score ? (int)(hh >= low[q]) & (int)(h != gg)
+                          : (int)(hh > low[q]) | ((int)(hh == low[q]) & (int)(h < gg));
+          must += by_score ? (int)(hl > high[q]) : 0;
         }
         if (may < g.group_k) kept |= 1ull << gg;
         else if (by_score && must < g.group_k) unsure = true;
@@ -501,7 +501,7 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
   // ---- each lane's experts in order
   double list[EPL];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) list[j] = pack_key(key[j], e0 + j);
+  for (int j = 0; j < EPL; ++j) list[j] = pack_key(key[j], j);
   if constexpr (EPL == 4) {
     sort4(list);
   } else {
@@ -518,7 +518,9 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
     }
   }
   auto key_in = [](double d) { return (uint32_t)(__builtin_bit_cast(uint64_t, d) >> 20); };
-  auto expert_in = [](double d) { return (uint32_t)__builtin_bit_cast(uint64_t, d) >> 11 & 511u; };  // 256 - e
+  auto expert_in = [e0](double d) {  // 256 - e = 256 - e0 - j
+    return ((uint32_t)__builtin_bit_cast(uint64_t, d) & 15u) + (uint32_t)(241 - e0);
+  };
 
   bool dropped = false;
   if (whole) {
@@ -535,8 +537,8 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
     int may = 0, must = 0;
     auto rival = [&](int n, uint32_t hl, uint32_t hh) __attribute__((always_inline)) {
       // without ranges the lower group wins a tie: n lanes back is lower unless it wrapped
-      may += (int)(hh > low) | ((int)(hh == low) & ((int)by_score | (int)(n <= i16)));
-      must += (int)(hl > high);
+      may += by_score ? (int)(hh >= low) : (int)(hh > low) | ((int)(hh == low) & (int)(n <= i16));
+      must += by_score ? (int)(hl > high) : 0;
     };
     // the other groups of the row, one turn of `lanes` at a time (lanes without
     // experts hold 0, below every key)
@@ -647,8 +649,10 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
 //   softmax       dl_j = p_j (g_j - sum_r g_r p_r), p over the selected when
 //                 renormalised (0 elsewhere), else over all experts
 // The selected gradients are scattered into an LDS row that is written out
-// whole, so the kernel is bound by the [T, E] gradient's bytes.  Only the
-// dense form reads every logit.  1 - s is formed as 1 / (1 + exp(l)).
+// whole, so the kernel is bound by the [T, E] gradient's bytes (65536 x 256
+// fp32, 67 MB: 18 us, 3.7 TB/s written beside the selected logits' lines; 25 us
+// with stores that stay in the caches).  Only the dense form reads every logit.
+// 1 - s is formed as 1 / (1 + exp(l)).
 template <int LT>
 __global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restrict__ logits, int64_t ld, int T, int E,
                                                             int k, int score, int renorm, float scale,
@@ -746,12 +750,12 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restri
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = grad(v[j], x + j);
       if constexpr (LT == GATE_F32) {
-        *(f32x4*)((float*)out + t * ldo + x) = v;
+        __builtin_nontemporal_store(v, (f32x4*)((float*)out + t * ldo + x));
       } else {
         u32x2 o;
         o.x = (uint32_t)f32_to_act_bits(v.x, LT) | (uint32_t)f32_to_act_bits(v.y, LT) << 16;
         o.y = (uint32_t)f32_to_act_bits(v.z, LT) | (uint32_t)f32_to_act_bits(v.w, LT) << 16;
-        *(u32x2*)((uint16_t*)out + t * ldo + x) = o;
+        __builtin_nontemporal_store(o, (u32x2*)((uint16_t*)out + t * ldo + x));
       }
     }
   } else {
@@ -780,10 +784,14 @@ hipError_t launch_gate(const void* logits, int lt, int64_t ld, int T, int E, int
     return launch_kernel(kern, grid, 64 * waves, lds, st, logits, ld, vec, T, E, k, g, idx, w, k_used, entropy,
                          clear_word);
   };
-  auto pick = [&](auto lc) {
+  // a bias, or groups ranked by two experts, order by scores; else the logits do
+  const bool by_score = g.bias != nullptr || (g.groups > 1 && g.group_best == 2);
+  auto size = [&](auto lc, auto sc) {
     constexpr int LT = decltype(lc)::value;
-    return E <= 64 ? go(gate_kernel<4, LT>) : E <= 128 ? go(gate_kernel<8, LT>) : go(gate_kernel<16, LT>);
+    constexpr bool S = decltype(sc)::value;
+    return E <= 64 ? go(gate_kernel<4, LT, S>) : E <= 128 ? go(gate_kernel<8, LT, S>) : go(gate_kernel<16, LT, S>);
   };
+  auto pick = [&](auto lc) { return by_score ? size(lc, std::true_type{}) : size(lc, std::false_type{}); };
   if (lt == GATE_F32) return pick(std::integral_constant<int, GATE_F32>{});
   if (lt == ACT_BF16) return pick(std::integral_constant<int, ACT_BF16>{});
   return pick(std::integral_constant<int, ACT_F16>{});
