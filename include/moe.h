@@ -490,7 +490,7 @@ typedef struct {
  *   base   [T, N] of type out_dt (dt or MOE_F32), rows ld_base apart
  *   out    [T, N] likewise, rows ld_out apart.  out == base (with the same row
  *          distance) adds in place and leaves tokens without an adapter
- *          untouched; otherwise the two must not overlap
+ *          untouched; otherwise the two must not overlap.  out never overlaps x
  * ldx and ld_base at most MOE_LORA_MAX_COLUMNS.  Sums are fp32 and one rounding
  * gives out.  0 <= T <= MOE_GATE_MAX_TOKENS.  One launch, no workspace.
  */

@@ -80,17 +80,21 @@ __device__ __forceinline__ uint64_t lane_read64(uint64_t v, int src) {
   return (uint64_t)hi << 32 | lo;
 }
 
-// 64-bit maximum, then the lowest index that holds it (slow path only)
+// maximum over the 64 lanes, in a scalar register
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
+  v = max16_u(v);
+  const uint32_t r0 = __builtin_amdgcn_readlane(v, 0), r1 = __builtin_amdgcn_readlane(v, 16);
+  const uint32_t r2 = __builtin_amdgcn_readlane(v, 32), r3 = __builtin_amdgcn_readlane(v, 48);
+  return max(max(r0, r1), max(r2, r3));
+}
+
+// the index of the largest 64-bit key, of equal ones the first lane's (indices
+// grow with the lane): the high words' maximum, then the low words' among those
 __device__ __forceinline__ int wave_best64(uint64_t key, int index) {
-#pragma unroll 1
-  for (int off = 1; off < WAVE; off <<= 1) {
-    const uint64_t ok = lane_read64(key, lane_id() ^ off);
-    const int oi = __builtin_amdgcn_ds_bpermute((lane_id() ^ off) << 2, index);
-    const bool take = ok > key || (ok == key && oi < index);
-    key = take ? ok : key;
-    index = take ? oi : index;
-  }
-  return __builtin_amdgcn_readfirstlane(index);
+  const uint32_t hi = (uint32_t)(key >> 32), lo = (uint32_t)key;
+  const uint32_t m1 = wave_max_key(hi);
+  const uint32_t m0 = wave_max_key(hi == m1 ? lo : 0u);
+  return __builtin_amdgcn_readlane(index, (int)__builtin_ctzll(__ballot(hi == m1 && lo == m0)));
 }
 
 __device__ __forceinline__ double wave_sum64(double v) {
@@ -214,6 +218,7 @@ __device__ __forceinline__ int exact_experts(const void* __restrict__ logits, in
     if (lane < G) {
       uint64_t b1 = 0, b2 = 0;
       int i1 = 0, i2 = 0;
+#pragma unroll 4
       for (int i = 0; i < gs; ++i) {
         const uint64_t u = key_of64(lds[lane * gs + i]);
         if (u > b1) {
@@ -301,16 +306,19 @@ __device__ __forceinline__ void sort8(double* v) {
 // Equal logits with equal biases are exact ties and need no second look.
 //
 // Error bounds of the fp32 keys (u = 2^-24, products and sums rounded once,
-// v_exp_f32 and v_rcp_f32 within one ulp):
-//   sigmoid: the exponential is off by (2|l| + 2) u relative, which reaches s
-//     times s (1 - s), and s (1 - s) |l| <= 0.224; the sum 1 + e adds u s, the
-//     reciprocal 2 u s: less than 4 u = 2^-22 in all.
-//   softmax: p is off by less than 40 u p_max: (3|d| + 2) u on each term
-//     (p |d| <= 0.37 p_max), and in the sum the same weighted by p, at most
-//     3 u (ln 256) + 2 u, and ten roundings.
+// v_exp_f32 and v_rcp_f32 within one ulp, 2 u):
+//   sigmoid: exp(-l) is off by (1.33 |l| + 2) u relative (the rounded product
+//     with the rounded log2 e, then the exponential), which reaches s times
+//     s (1 - s), and s (1 - s) |l| <= 0.224: 0.8 u; the sum 1 + e adds u s, the
+//     reciprocal 2 u s: less than 4 u in all.
+//   softmax: a term is off by (2.33 |d| + 2) u (the difference d is rounded
+//     too), and p |d| <= 0.37 p_max; the sum by the same weighted with p, at
+//     most 2.33 u ln 256 + 2 u, and 19 roundings; the reciprocal and the product
+//     3 u: less than 40 u p_max.
 //   the bias adds u |key|.
-// Two keys further apart than twice that keep their order; the windows below
-// (2^-20, or 2^-17 p_max, plus 2^-22 |key|) hold that with a margin.
+// KEY_ERR, SOFTMAX_ERR p_max and KEY_ROUND |key| are these with a margin.  Two
+// keys further apart than the sum of their errors keep their order.
+constexpr float KEY_ERR = 0x1.1p-22f, SOFTMAX_ERR = 0x1.48p-19f, KEY_ROUND = 0x1.1p-24f;
 constexpr int GATE_PITCH = 260;             // LDS words a token holds its keys in
 constexpr int GATE_WAVE_WORDS = 9 * 64 * 2;  // LDS words a wave: nine list entries a lane (the last is the end), four
                                              // tokens' keys, or one double per expert of one token
@@ -364,7 +372,7 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
 
   // ---- keys
   const bool softmax = g.score == GATE_SOFTMAX;
-  float m_all = 0.0f, z_all = 1.0f, window = 0x1p-20f;  // softmax over all experts; sigmoid's window
+  float m_all = 0.0f, z_all = 1.0f, key_err = KEY_ERR;  // softmax over all experts; sigmoid's error
   bool unsure = false;
   uint32_t key[EPL];
   if (softmax && (by_score || !g.renorm)) {
@@ -384,7 +392,7 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
     z_all = sum16(z);
     if (z_all == 0.0f) z_all = 1.0f;
     const float rz = __builtin_amdgcn_rcpf(z_all);
-    window = ldexp_f(rz, -17);
+    key_err = SOFTMAX_ERR * rz;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) b[j] = ex[j] * rz + b[j];
   } else if (by_score) {
@@ -426,14 +434,16 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
   auto range = [&](uint32_t best, uint32_t next, uint32_t& low, uint32_t& high) __attribute__((always_inline)) {
     low = high = best;
     if (!by_score || best == 0u) return;
-    float v = value_of(best), err = window + 0x1p-22f * fabsf(v);
+    float v = value_of(best), err = key_err + KEY_ROUND * fabsf(v);
     if (g.group_best == 2) {
       const float v2 = value_of(next);
       if (v2 != -INFINITY) {
-        err = err + (window + 0x1p-22f * fabsf(v2));
+        err = err + (key_err + KEY_ROUND * fabsf(v2));
         v = v + v2;
+        err = err + KEY_ROUND * fabsf(v);
       }
     }
+    err = err + 4.0f * KEY_ROUND * fabsf(v);  // the roundings of the range's own ends
     const float lo = v - err, hi = v + err;
     const bool sure = lo <= hi;  // NaN: anything is possible
     low = sure ? key_of(lo) : 1u;
@@ -601,7 +611,7 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
     const float nl = __builtin_bit_cast(float, dpp_next(__builtin_bit_cast(uint32_t, ls)));
     const float nb = __builtin_bit_cast(float, dpp_next(__builtin_bit_cast(uint32_t, bs)));
     const bool rival = i16 < k && dpp_next(mine) != 0u;
-    const bool apart = v - nv > window + 0x1p-22f * fabsf(v);  // false for NaN and infinities
+    const bool apart = v - nv > 2.0f * (key_err + KEY_ROUND * fabsf(v));  // false for NaN and infinities
     const bool tie = i16 + 1 < k && ls == nl && (bs == nb || ls == -INFINITY);
     uint64_t again = __ballot(tv && ((rival && !apart && !tie) || unsure));
     while (again) {
