@@ -472,7 +472,7 @@ __global__ __launch_bounds__(64 * FW) void lora_kernel(const uint16_t* __restric
 #pragma unroll
         for (int q = 0; q < VR; ++q) {
           const int r = lane + WAVE * q;
-          v[q] = r < RP ? vsum[p][r] * sc : 0.0f;
+          v[q] = r < rank ? vsum[p][r] * sc : 0.0f;  // past the rank zero, also where x is not finite
           top = fmaxf(top, fabsf(v[q]));
         }
         int e = 0;

@@ -119,6 +119,24 @@ def test_nan_in_one_row_stays_there():
     assert torch.equal(got[keep], want[keep])
 
 
+@pytest.mark.parametrize("R", [8, 16, 24, 40, 128])
+@pytest.mark.parametrize("dtype,out", [("bf16", "same"), ("f16", "same"), ("bf16", "f32"), ("f16", "f32")])
+def test_infinities_are_not_spread_by_unused_ranks(R, dtype, out):
+    """With positive adapters an infinite x gives an infinite row, whatever the tile's unused ranks hold; an adapter of
+    rank 0 adds nothing to it, and nothing of an infinite scale."""
+    c = make(8, 20, 72, 40, 3, R, dtype, out)
+    c["a"], c["b"] = c["a"].abs() + 0.125, c["b"].abs() + 0.125
+    c["ids"] = torch.arange(20, dtype=torch.int32) % 3
+    c["x"][3, 5], c["x"][7, 71], c["x"][5, 0] = torch.inf, -torch.inf, torch.inf
+    got = call(c, ranks=torch.tensor([R, R - 3, 0], dtype=torch.int32), scale=torch.tensor([1.0, 2.0, torch.inf])).cpu()
+    assert torch.all(got[3] == torch.inf) and torch.all(got[7] == -torch.inf)
+    none = c["ids"] == 2
+    assert torch.equal(got[none], c["base"][none])
+    rest = ~none
+    rest[[3, 7]] = False
+    assert torch.all(torch.isfinite(got[rest]))
+
+
 @pytest.mark.parametrize("power", [-30, 14])
 def test_fp16_values_beyond_its_range(power):
     """x A^T outside fp16's range (and far below it) still reaches the fp32 output."""
