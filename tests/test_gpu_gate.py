@@ -341,3 +341,101 @@ def test_argument_errors():
     ):
         with pytest.raises(err):
             call()
+
+
+# ----------------------------------------------- far offsets, long calls, near ties
+
+
+def test_rows_past_32_bit_offsets():
+    """70 rows 2^26 elements apart: byte offsets to 2^33 (fp16) of logits and of the gradient."""
+    T, E, ld = 70, 64, 1 << 26
+    l = logits_of(31, T, E, "f16")
+    far = torch.empty(T * ld, dtype=torch.float16, device="cuda").view(T, ld)[:, 5:5 + E]
+    far.copy_(l)
+    kw = dict(score="sigmoid", groups=8, group_k=4, group_best=2)
+    r = moe.gate_from_logits(far, 6, **kw)
+    assert np.array_equal(r["idx"].cpu().numpy(), select64(f64(l), 6, **kw))
+    dw = torch.randn(T, 6, generator=torch.Generator().manual_seed(1)).cuda()
+    for renorm in (True, False):
+        want = moe.gate_backward(l.cuda(), r["idx"], dw, renorm=renorm)
+        assert torch.equal(moe.gate_backward(far, r["idx"], dw, renorm=renorm), want)
+    moe.gate_backward(l.cuda(), r["idx"], dw, out=far)  # softmax over the selected: logits are read elsewhere
+    assert torch.equal(far, moe.gate_backward(l.cuda(), r["idx"], dw))
+
+
+def test_a_million_tokens_with_one_block_repeated():
+    """65 copies of 16384 rows in one call: each of them gets what the rows get alone."""
+    n, times, E = 1 << 14, 65, 256
+    l = logits_of(41, n, E, "bf16").cuda()
+    kw = dict(score="sigmoid", groups=8, group_k=4, group_best=2)
+    one = moe.gate_from_logits(l, 8, **kw)
+    many = moe.gate_from_logits(l.repeat(times, 1), 8, **kw)
+    assert torch.all(many["idx"].view(times, n, 8) == one["idx"]) and torch.all(many["w"].view(times, n, 8) == one["w"])
+    dw = torch.randn(n, 8, generator=torch.Generator().manual_seed(2)).cuda()
+    g = moe.gate_backward(l, one["idx"], dw, score="sigmoid")
+    assert torch.all(moe.gate_backward(l.repeat(times, 1), many["idx"], dw.repeat(times, 1), score="sigmoid")
+                     .view(times, n, E) == g)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [7, 8])
+@pytest.mark.parametrize("first", [32, 37])
+def test_every_winner_among_neighbours(score, k, first):
+    """Twelve consecutive experts far above the others, with keys that fp32 cannot tell apart: more of one lane's
+    experts than its list holds, in and across two lanes (sixteen experts a lane)."""
+    E, T = 256, 24
+    l = logits_of(51, T, E)
+    l[:, first:first + 12] = l[:1, :12] * 0.1
+    s = 1 / (1 + np.exp(-f64(l))) if score == "sigmoid" else np.exp(f64(l)) / np.exp(f64(l)).sum(1, keepdims=True)
+    for t in (0, T - 1):
+        bias = torch.zeros(E)
+        bias[first:first + 12] = torch.from_numpy((3.0 - s[t, first:first + 12]).astype(np.float32))
+        check(l, k, bias=bias, score=score)
+        check(l, k, bias=bias, score=score, groups=4, group_k=2, group_best=2)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_options(seed):
+    """Sizes, groups, masks, biases and types drawn at random, every index exact."""
+    rng = np.random.default_rng(seed)
+    for _ in range(25):
+        G = int(rng.integers(1, 17))
+        gs = int(rng.integers(1, 256 // G + 1))
+        E = G * gs
+        k = int(rng.integers(1, min(8, E) + 1))
+        kw = dict(score=["softmax", "sigmoid"][int(rng.integers(2))], renorm=bool(rng.integers(2)))
+        if G > 1:
+            low = -(-k // gs)
+            kw.update(groups=G, group_k=int(rng.integers(low, G + 1)), group_best=int(rng.integers(1, min(2, gs) + 1)))
+        l = logits_of(int(rng.integers(1 << 30)), int(rng.integers(1, 60)), E, ["f32", "f16", "bf16"][int(rng.integers(3))],
+                      float(rng.choice([0.01, 1.0, 6.0])))
+        if rng.integers(2):
+            l[torch.rand(l.shape, generator=torch.Generator().manual_seed(seed)) < 0.4] = -torch.inf
+        bias = torch.randn(E, generator=torch.Generator().manual_seed(seed)) * float(rng.choice([1e-6, 0.05, 2.0]))
+        r = check(l, k, bias=bias if rng.integers(2) else None, **kw)
+        dw = torch.randn(l.shape[0], k, generator=torch.Generator().manual_seed(seed))
+        check_grad(l, r["idx"].cpu(), dw, score=kw["score"], renorm=kw["renorm"], scale=0.5)
+
+
+def test_two_graphs_and_eager_calls_interleaved():
+    """Graphs that write their own outputs share nothing else: replayed in turn on two streams, with eager calls between."""
+    kw = dict(score="sigmoid", groups=8, group_k=4, group_best=2)
+    src = [logits_of(60 + i, 200, 256).cuda() for i in range(2)]
+    outs = [(torch.empty(200, 8, dtype=torch.int32, device="cuda"), torch.empty(200, 8, device="cuda")) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            moe.gate_from_logits(src[i], 8, out=outs[i], **kw)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for turn in range(3):
+        for i in range(2):
+            src[i].copy_(logits_of(70 + 2 * turn + i, 200, 256))
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        moe.gate_from_logits(src[0], 8, **kw)
+        torch.cuda.synchronize()
+        for i in range(2):
+            want = moe.gate_from_logits(src[i], 8, **kw)
+            assert torch.equal(outs[i][0], want["idx"]) and torch.equal(outs[i][1], want["w"])

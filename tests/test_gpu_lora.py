@@ -229,6 +229,55 @@ def test_argument_errors():
             moe.lora_add(**{**c, **change})
 
 
+def test_rows_past_32_bit_offsets():
+    """Rows 2^22 elements apart (the widest), 1100 of them, and an output 2^23 apart: byte offsets to 2^34; what lies
+    between x's rows is NaN and what lies between out's stays."""
+    T, K, N = 1100, 64, 40
+    c = make(12, T, K, N, 4, 16)
+    want = call(c)
+    x = torch.full((T, 1 << 22), torch.nan, dtype=torch.bfloat16, device="cuda")[:, 8:8 + K]
+    x.copy_(c["x"])
+    out = torch.full((T, 1 << 23), 3.0, dtype=torch.bfloat16, device="cuda")
+    ids, a, b = (c[n].cuda() for n in ("ids", "a", "b"))
+    moe.lora_add(x, c["base"].cuda(), ids, a, b, out=out[:, 1:1 + N])
+    assert torch.equal(out[:, 1:1 + N], want)
+    assert torch.all(out[:, 0] == 3) and torch.all(out[:, 1 + N:1 + 2 * N] == 3)
+
+
+def test_adapters_past_32_bit_offsets():
+    """The last of 2100 adapters lies 2^32 bytes from the first."""
+    L, K, N, R = 2100, 8192, 8192, 128
+    a = torch.zeros(L, R, K, dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros(L, N, R, dtype=torch.bfloat16, device="cuda")
+    c = make(13, 20, K, N, 1, R)
+    a[L - 1].copy_(c["a"][0])
+    b[L - 1].copy_(c["b"][0])
+    last = torch.full((20,), L - 1, dtype=torch.int32, device="cuda")
+    c["ids"] = torch.zeros(20, dtype=torch.int32)
+    assert torch.equal(moe.lora_add(c["x"].cuda(), c["base"].cuda(), last, a, b), call(c))
+
+
+def test_sixteen_bit_rows_of_a_long_batch():
+    """20000 tokens (313 chunks, one workgroup each) in runs, every 64 of them the same as alone."""
+    n, times = 64, 313
+    c = make(14, n, 128, 96, 5, 32)
+    one = call(c)
+    d = {m: c[m].cuda() for m in c}
+    many = moe.lora_add(d["x"].repeat(times, 1), d["base"].repeat(times, 1), d["ids"].repeat(times), d["a"], d["b"])
+    assert torch.all(many.view(times, n, 96) == one)
+
+
+def test_views_of_one_buffer_add_in_place():
+    """base and out as two views of the same rows are the in-place form."""
+    c = {n: t.cuda() for n, t in make(15, 33, 64, 24, 3, 8).items()}
+    want = moe.lora_add(**c)
+    buf = torch.zeros(33, 40, dtype=torch.bfloat16, device="cuda")
+    buf[:, 8:32] = c["base"]
+    c["base"] = buf[:, 8:32]
+    moe.lora_add(**c, out=buf[:, 8:32])
+    assert torch.equal(buf[:, 8:32], want) and torch.all(buf[:, :8] == 0) and torch.all(buf[:, 32:] == 0)
+
+
 # ------------------------------------- adapters on the router, gate, experts
 
 
