@@ -3,10 +3,10 @@
 //   out[t] = base[t] + scale_a * (x[t] A_a^T) B_a^T,   a = ids[t]
 //
 // with A_a [R, K] and B_a [N, R] of adapter a, in one launch.  Every wave of a
-// workgroup reads the 64 ids of its chunk of consecutive tokens (one a lane),
-// walks the chunk's distinct adapters with ballots and takes its turn at their
-// tiles: up to 16 tokens of one adapter on the matrix cores.  So ids come in
-// any order, without a sorting launch, and runs of one request fill the tiles.
+// workgroup reads the 64 ids of its chunk of consecutive tokens (one a lane)
+// and finds the chunk's tiles with ballots: up to 16 tokens of one adapter on
+// the matrix cores.  So ids come in any order, without a sorting launch, and
+// runs of one request fill the tiles.
 //
 // Rounding: x A^T has exact products and fp32 sums, which stay in fp32.  For
 // the second product v goes to the matrix cores as two 16-bit parts (hi + lo:
@@ -14,6 +14,19 @@
 // fp32 output, so the only rounding that shows is the output's.  fp16 parts are
 // taken of v * 2^-e_t, the token's largest |v| brought to 2^13 .. 2^14, which
 // keeps fp32's range.
+//
+// Time, and what bounds it (K = N = 4096 unless said; a card that copies 1 GB
+// at 5.1 TB/s and launches an empty kernel in 2.3 us):
+//   1 token, rank 16, fp16                    8.1 us   0.3 MB: a chain of dependent
+//       loads (ids, A, the sums through LDS, B and base), each 0.5 .. 1 us, and
+//       some 1100 instructions a wave in a row
+//   64 tokens of 48 adapters, rank 32, bf16  13.0 us  16.5 MB: the same chain, with
+//       A's and B's rows from HBM in it (1.3 TB/s over the whole call)
+//   777 tokens, N = 64, rank 8, fp32 out     10.2 us   7.6 MB: likewise
+//   4096 tokens in runs of 6, rank 64, bf16  48.5 us   105 MB, 2.2 TB/s: a tile's
+//       workgroup takes 1.2 MB through its CU (x and base 0.25 MB, A and B 1 MB
+//       from L2), some 20 us for each product; the two do not overlap, as there
+//       is one workgroup a CU (its registers), and all start together
 #include <algorithm>
 #include <type_traits>
 
@@ -56,6 +69,35 @@ __device__ __forceinline__ int chunk_id(const int32_t* __restrict__ ids, int64_t
   const int a = ids[t];
   return a >= 0 && a < L ? a : -1;
 }
+
+// The tiles of a chunk: runs of up to 16 of the lanes with one id, each known
+// by its first lane.  Lanes of equal ids are found bit by bit of the id.
+struct Tiles {
+  uint64_t same, first;  // lanes of this lane's id; the tiles' first lanes
+  int at, count;         // this lane's place among them; the tiles
+
+  __device__ __forceinline__ Tiles(int id, int L) {
+    same = ~0ull;
+    uint32_t key = (uint32_t)(id + 2);
+#pragma unroll 1
+    for (uint32_t top = (uint32_t)L + 1; top != 0; top >>= 1, key >>= 1) {
+      const bool on = key & 1;
+      same &= __ballot(on) ^ (on ? 0ull : ~0ull);
+    }
+    at = (int)__popcll(same & lanemask_lt());
+    first = __ballot(id >= -1 && at % 16 == 0);
+    count = (int)__popcll(first);
+  }
+  // the j-th tile's first lane (j < count)
+  __device__ __forceinline__ int leader(int j) const {
+    return (int)__builtin_ctzll(__ballot((first >> lane_id() & 1) && (int)__popcll(first & lanemask_lt()) == j));
+  }
+  __device__ __forceinline__ uint64_t of(int lane) const {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(same >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)same, lane);
+  }
+  __device__ __forceinline__ int place(int lane) const { return __builtin_amdgcn_readlane(at, lane); }
+};
 
 // lane p receives the lane of the p-th set bit of `set` (p < popcount)
 __device__ __forceinline__ int nth_lane(uint64_t set) {
@@ -321,10 +363,18 @@ __device__ __forceinline__ void add_store(const u32x4 (&o)[F32 ? 2 : 1], const f
 // Both products of a tile (up to 16 tokens of one adapter) in one workgroup
 // of eight waves: the waves take consecutive parts of K and are added through
 // LDS in wave order, the tokens' sums are split into the parts the matrix
-// cores take, and the waves share the output's columns.  Workgroup
-// (chunk, q, z) takes every Q-th of the chunk's tiles and the z-th part of the
-// output's columns, repeating the first product for each part.
-constexpr int FW = 8;  // waves
+// cores take, and the waves share the output's columns.
+//
+// The chunk's work comes in units of one tile and one of 2^cut parts of the
+// columns (the first product is repeated for each part), which its gridDim.y
+// workgroups take in turn.  `cut` grows while the chunk's units fit its share
+// of 256 workgroups side by side, so a few tiles still fill the chip: the
+// number of tiles is known only here, from the ids.  Against parts chosen by T
+// alone: 1024 tokens in runs, rank 64, 22.0 against 27.3 us; 300 tokens, rank
+// 16, 12.5 against 17.8; 64 tokens of 48 adapters, rank 32, 13.0 against 14.4; 8
+// tokens, rank 64, 15.9 against 14.8.  The result does not depend on it.
+constexpr int FW = 8;        // waves (sixteen, with 128 registers each: 79 us for 4096 tokens)
+constexpr int MOST_CUT = 3;  // at most 2^3 parts of the columns
 
 template <int ACT, bool F32, int RT>
 __global__ __launch_bounds__(64 * FW) void lora_kernel(const uint16_t* __restrict__ x, int64_t ldx,
@@ -334,18 +384,20 @@ __global__ __launch_bounds__(64 * FW) void lora_kernel(const uint16_t* __restric
                                                        const int32_t* __restrict__ ids,
                                                        const int32_t* __restrict__ ranks, const void* base,
                                                        int64_t ldb, void* out, int64_t ldo, int T, int L, int R, int K,
-                                                       int N, int vec) {
+                                                       int N, int vec, int share, int most) {
   constexpr int NP = F32 && ACT == ACT_BF16 ? 3 : 2;
   constexpr int STEPS = RT == 1 ? 1 : RT / 2;  // 32-rank steps of the second product
   constexpr int RP = RT * 16, TILE = 16;
   constexpr int RB = RT < 4 ? RT : RT == 8 ? 2 : 4;  // rank tiles loaded, and summed over the waves, together
   constexpr int H = RT / RB;
-  // loads in flight a wave: items of the first product, and of the second
-  // base's blocks (from HBM) and B's (from L2).  Sixteen waves a CU (128
-  // registers) overlap two workgroups.
+  // Loads in flight a wave: items of the first product, and of the second
+  // base's blocks (from HBM) and B's (from L2).  More of them spill (RT = 4) or
+  // only lengthen the code (RT = 1, four items: 8.8 against 8.4 us for one token;
+  // RT <= 2, four of base's blocks: 14.8 against 14.4 us for 64 tokens of 48
+  // adapters; RT = 4, two of them: 51 against 48.7 us for 4096 tokens).
   constexpr int DEEP = RT == 4 ? 1 : 2;
   constexpr int TURN = DEEP < H ? H : DEEP;
-  constexpr int AHEAD = F32 ? 2 : 4, BAHEAD = RT == 8 ? 1 : 2;
+  constexpr int AHEAD = F32 || RT <= 2 ? 2 : 4, BAHEAD = RT == 8 ? 1 : 2;
   constexpr int OV = F32 ? 2 : 1;
   constexpr int VR = (RP + WAVE - 1) / WAVE;
   union Shared {
@@ -362,183 +414,188 @@ __global__ __launch_bounds__(64 * FW) void lora_kernel(const uint16_t* __restric
   const int id = chunk_id(ids, t0, T, L);
   const int kb = (K + 127) / 128, k0 = kb * wave / FW, k1 = kb * (wave + 1) / FW;
   const int nb = (N + 31) / 32;
-  const int per = (nb + (int)gridDim.z - 1) / (int)gridDim.z;
-  const int b0 = min(nb, (int)blockIdx.z * per), b1 = min(nb, b0 + per);
   const rsrc_t rx = chunk_rows(x, 2, t0, ldx, T, K);
   const rsrc_t rb = chunk_rows(base, F32 ? 4 : 2, t0, ldb, T, N);
-  uint64_t left = __ballot(id >= -1);
-  int seen = 0, turn = blockIdx.y;  // tiles walked past, and the next one of this workgroup
-  while (left != 0) {
-    const int a = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(left));
-    const uint64_t mine = __ballot(id == a);
-    left &= ~mine;
-    const int m = (int)__popcll(mine);
-    const int tiles = (m + TILE - 1) / TILE;
-    if (turn >= seen + tiles) {
-      seen += tiles;
+  const Tiles tiles(id, L);
+  int cut = 0;  // the output's columns in 2^cut parts
+  while (tiles.count << (cut + 1) <= share && cut < most) ++cut;
+  const int per = (nb + (1 << cut) - 1) >> cut;
+  for (int unit = blockIdx.y; unit < tiles.count << cut; unit += gridDim.y) {
+    const int z = unit & ((1 << cut) - 1), tile = unit >> cut;
+    const int b0 = min(nb, z * per), b1 = min(nb, b0 + per);
+    const int first = tiles.leader(tile);
+    const int a = __builtin_amdgcn_readlane(id, first);
+    const uint64_t mine = tiles.of(first);
+    const int p0 = tiles.place(first), cnt = min(TILE, (int)__popcll(mine) - p0);
+    const int nth = nth_lane(mine);
+    if (a < 0) {
+      // no adapter: out is base, moved only if the two are not one buffer
+      if (out != base) copy_rows<F32>(base, ldb, out, ldo, t0, nth, p0, cnt, b0 * 32, min(N, b1 * 32), vec);
       continue;
     }
-    const int nth = nth_lane(mine);
-    for (; turn < seen + tiles; turn += gridDim.y) {
-      const int p0 = (turn - seen) * TILE, cnt = min(TILE, m - p0);
-      if (a < 0) {
-        // no adapter: out is base, moved only if the two are not one buffer
-        if (out != base) copy_rows<F32>(base, ldb, out, ldo, t0, nth, p0, cnt, b0 * 32, min(N, b1 * 32), vec);
-        continue;
-      }
-      const int rank = adapter_rank(ranks, a, R);
-      // sizes the compiler must not know from here on: it would keep every
-      // product of them in registers over the loop, and spill
-      asm volatile("" : "+s"(K), "+s"(N), "+s"(R));
+    const int rank = adapter_rank(ranks, a, R);
+    // sizes the compiler must not know from here on: it would keep every
+    // product of them in registers over the loop, and spill
+    asm volatile("" : "+s"(K), "+s"(N), "+s"(R));
 
-      // ---- x A^T over this wave's columns.  A: load j is this lane's piece of
-      // row lrow + j of a 16-row tile, eight columns from lcol of a 128-column
-      // block, and the quad transpose makes it columns 32 g + 8 j of row l16.
-      // x, read once, comes in that place.
-      const bool have = l16 < cnt;
-      const int tok = __builtin_amdgcn_ds_bpermute((p0 + (have ? l16 : 0)) << 2, nth);
-      const int64_t t = t0 + tok;
-      const uint32_t xoff = have ? (uint32_t)tok * (uint32_t)ldx * 2 + g * 64 : FAR;
-      const uint32_t at = have && vec ? (uint32_t)tok * (uint32_t)ldb * (F32 ? 4 : 2) + g * (F32 ? 32 : 16) : FAR;
-      f32x4 acc[RT];
+    // ---- x A^T over this wave's columns.  A: load j is this lane's piece of
+    // row lrow + j of a 16-row tile, eight columns from lcol of a 128-column
+    // block, and the quad transpose makes it columns 32 g + 8 j of row l16.
+    // x, read once, comes in that place.
+    const bool have = l16 < cnt;
+    const int tok = __builtin_amdgcn_ds_bpermute((p0 + (have ? l16 : 0)) << 2, nth);
+    const int64_t t = t0 + tok;
+    const uint32_t xoff = have ? (uint32_t)tok * (uint32_t)ldx * 2 + g * 64 : FAR;
+    const uint32_t at = have && vec ? (uint32_t)tok * (uint32_t)ldb * (F32 ? 4 : 2) + g * (F32 ? 32 : 16) : FAR;
+    f32x4 acc[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      const rsrc_t ra = make_rsrc(am + (int64_t)a * R * K, (uint32_t)rank * K * 2);  // rows up to the rank
-      const int lrow = lane / 4 % 4 * 4, lcol = g * 32 + lane % 4 * 8;
-      const uint32_t aoff = (uint32_t)(lrow * K + lcol) * 2;
-      struct Item {
-        u32x4 x[4], a[RB][4];
-      } it[DEEP];
-      const int items = (k1 - k0) * H;
-      auto load = [&](Item& t, int i, int r0) __attribute__((always_inline)) {  // r0 = i % H * RB
-        const int c = (k0 + i / H) * 128;
-        const int end = i < items ? K : 0;  // past the last item: zeros, unread
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const rsrc_t ra = make_rsrc(am + (int64_t)a * R * K, (uint32_t)rank * K * 2);  // rows up to the rank
+    const int lrow = lane / 4 % 4 * 4, lcol = g * 32 + lane % 4 * 8;
+    const uint32_t aoff = (uint32_t)(lrow * K + lcol) * 2;
+    struct Item {
+      u32x4 x[4], a[RB][4];
+    } it[DEEP];
+    const int items = (k1 - k0) * H;
+    auto load_x = [&](u32x4 (&v)[4], int i) __attribute__((always_inline)) {
+      const int c = (k0 + i / H) * 128;
+      const int end = i < items ? K : 0;  // past the last item: zeros, unread
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t.x[j] = buf_load16(rx, c + g * 32 + 8 * j < end ? xoff + (c + 8 * j) * 2 : FAR);
-        const uint32_t off = c + lcol < end ? aoff + c * 2 : FAR;
+      for (int j = 0; j < 4; ++j) v[j] = buf_load16(rx, c + g * 32 + 8 * j < end ? xoff + (c + 8 * j) * 2 : FAR);
+    };
+    auto load_a = [&](u32x4 (&v)[4], int i, int r) __attribute__((always_inline)) {  // rank tile r
+      const int c = (k0 + i / H) * 128;
+      const uint32_t off = c + lcol < (i < items ? K : 0) ? aoff + c * 2 : FAR;
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+      for (int j = 0; j < 4; ++j) v[j] = buf_load16(ra, off + (uint32_t)((r * 16 + j) * K) * 2);
+    };
+    u32x4 xn[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) t.a[r][j] = buf_load16(ra, off + (uint32_t)(((r0 + r) * 16 + j) * K) * 2);
-      };
+    for (int h = 0; h < DEEP; ++h) {
+      load_x(it[h].x, h);
 #pragma unroll
-      for (int h = 0; h < DEEP; ++h) load(it[h], h, h % H * RB);
+      for (int r = 0; r < RB; ++r) load_a(it[h].a[r], h, h % H * RB + r);
+    }
 #pragma unroll 1
-      for (int i = 0; i < items; i += TURN) {
+    for (int i = 0; i < items; i += TURN) {
 #pragma unroll
-        for (int h = 0; h < TURN; ++h) {
-          Item& now = it[h % DEEP];
+      for (int h = 0; h < TURN; ++h) {
+        Item& now = it[h % DEEP];
+        if (DEEP == 1) load_x(xn, i + h + 1);
 #pragma unroll
-          for (int r = 0; r < RB; ++r) {
-            quad_transpose(now.a[r]);
+        for (int r = 0; r < RB; ++r) {
+          quad_transpose(now.a[r]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[h % H * RB + r] = mfma16<ACT>(now.a[r][j], now.x[j], acc[h % H * RB + r]);
-          }
-          load(now, i + h + DEEP, (h + DEEP) % H * RB);
+          for (int j = 0; j < 4; ++j) acc[h % H * RB + r] = mfma16<ACT>(now.a[r][j], now.x[j], acc[h % H * RB + r]);
+          if (DEEP > 1 && r == RB - 1) load_x(now.x, i + h + DEEP);
+          load_a(now.a[r], i + h + DEEP, (h + DEEP) % H * RB + r);
         }
-      }
-
-      // ---- the second product's first loads, which do not wait for the sums
-      const BRows<RT> rows(bm, a, N, R, rank);
-      u32x4 braw[BAHEAD][RT], o[AHEAD][OV];
-      auto load_o = [&](u32x4 (&v)[OV], int blk) __attribute__((always_inline)) {
-        const uint32_t off = blk < b1 && blk * 32 + 8 * g + 8 <= N ? at + (uint32_t)(blk * 32) * (F32 ? 4 : 2) : FAR;
+        if (DEEP == 1) {
 #pragma unroll
-        for (int h = 0; h < OV; ++h) v[h] = buf_load16(rb, off + 16 * h);
-      };
-#pragma unroll
-      for (int h = 0; h < BAHEAD; ++h) rows.load(braw[h], b0 + wave + FW * h, b1);
-#pragma unroll
-      for (int h = 0; h < AHEAD; ++h) load_o(o[h], b0 + wave + FW * h);
-
-      // ---- the waves' sums, token by token as 16-bit parts
-#pragma unroll
-      for (int r0 = 0; r0 < RT; r0 += RB) {
-        __syncthreads();  // the last tile's B rows, or the sums before these, are read
-#pragma unroll
-        for (int r = 0; r < RB; ++r) sh.red[wave][r][lane] = acc[r0 + r];
-        __syncthreads();
-        for (int i = threadIdx.x; i < RB * 256; i += 64 * FW) {
-          float v = 0.0f;
-#pragma unroll
-          for (int w = 0; w < FW; ++w) v += ((const float*)sh.red[w])[i];
-          vsum[i / 4 % 16][(r0 + i / 256) * 16 + i % 256 / 64 * 4 + i % 4] = v;
-        }
-      }
-      __syncthreads();
-      const float sc = scale ? scale[a] : 1.0f;
-      for (int p = wave; p < TILE; p += FW) {
-        float v[VR], top = 0.0f;
-#pragma unroll
-        for (int q = 0; q < VR; ++q) {
-          const int r = lane + WAVE * q;
-          v[q] = r < rank ? vsum[p][r] * sc : 0.0f;  // past the rank zero, also where x is not finite
-          top = fmaxf(top, fabsf(v[q]));
-        }
-        int e = 0;
-        if constexpr (ACT == ACT_F16) {
-          top = wave_max(top);
-          if (top > 0.0f && top < INFINITY) e = __builtin_amdgcn_frexp_expf(top) - 14;
-          if (lane == 0) exps[p] = e;
-        }
-#pragma unroll
-        for (int q = 0; q < VR; ++q) {
-          const int r = lane + WAVE * q;
-          uint16_t parts[NP];
-          split_parts<ACT, NP>(ACT == ACT_F16 ? ldexp_f(v[q], -e) : v[q], parts);
-          if (r < RP) {
-#pragma unroll
-            for (int h = 0; h < NP; ++h) vs[h][p][r] = parts[h];
-          }
-        }
-      }
-      __syncthreads();
-
-      // ---- base + v B^T: this wave's every FW-th block of 32 columns
-      u32x4 vv[NP][STEPS];
-      load_parts<RT>(vs, l16, vv);
-      const int e = ACT == ACT_F16 ? exps[l16] : 0;
-      const int whole = vec ? min(b1, N / 32) : b0;  // blocks of 32 columns that can be moved in 16 bytes
-      int b = b0 + wave;
-#pragma unroll 1
-      for (; b < whole; b += FW * AHEAD) {
-#pragma unroll
-        for (int h = 0; h < AHEAD; ++h) {
-          const int now = b + FW * h;
-          if (now < whole) {
-            u32x4 bv[STEPS][2];
-            take_rows<RT>(braw[h % BAHEAD], rows, rank, sh.b[wave], bv);
-            rows.load(braw[h % BAHEAD], now + FW * BAHEAD, b1);
-            float d[8];
-            block_product<ACT, RT, NP>(bv, vv, e, d);
-            if (have) add_store<ACT, F32>(o[h], d, out, t * ldo + now * 32 + 8 * g);
-            load_o(o[h], now + FW * AHEAD);
-          }
-        }
-      }
-      // the others, element by element
-      b = b0 + wave + (max(whole - b0 - wave, 0) + FW - 1) / FW * FW;
-#pragma unroll 1
-      for (; b < b1; b += FW) {
-        u32x4 bv[STEPS][2];
-        rows.load(braw[0], b, b1);
-        take_rows<RT>(braw[0], rows, rank, sh.b[wave], bv);
-        float d[8];
-        block_product<ACT, RT, NP>(bv, vv, e, d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = b * 32 + 8 * g + j;
-          if (have && c < N) {
-            if constexpr (F32)
-              ((float*)out)[t * ldo + c] = ((const float*)base)[t * ldb + c] + d[j];
-            else
-              ((uint16_t*)out)[t * ldo + c] =
-                  (uint16_t)pack2<ACT>(act_to_f32(((const uint16_t*)base)[t * ldb + c], ACT) + d[j], 0.0f);
-          }
+          for (int j = 0; j < 4; ++j) now.x[j] = xn[j];
         }
       }
     }
-    seen += tiles;
+
+    // ---- the second product's first loads, which do not wait for the sums
+    const BRows<RT> rows(bm, a, N, R, rank);
+    u32x4 braw[BAHEAD][RT], o[AHEAD][OV];
+    auto load_o = [&](u32x4 (&v)[OV], int blk) __attribute__((always_inline)) {
+      const uint32_t off = blk < b1 && blk * 32 + 8 * g + 8 <= N ? at + (uint32_t)(blk * 32) * (F32 ? 4 : 2) : FAR;
+#pragma unroll
+      for (int h = 0; h < OV; ++h) v[h] = buf_load16(rb, off + 16 * h);
+    };
+#pragma unroll
+    for (int h = 0; h < BAHEAD; ++h) rows.load(braw[h], b0 + wave + FW * h, b1);
+#pragma unroll
+    for (int h = 0; h < AHEAD; ++h) load_o(o[h], b0 + wave + FW * h);
+
+    // ---- the waves' sums, token by token as 16-bit parts
+#pragma unroll
+    for (int r0 = 0; r0 < RT; r0 += RB) {
+      __syncthreads();  // the last tile's B rows, or the sums before these, are read
+#pragma unroll
+      for (int r = 0; r < RB; ++r) sh.red[wave][r][lane] = acc[r0 + r];
+      __syncthreads();
+      for (int i = threadIdx.x; i < RB * 256; i += 64 * FW) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < FW; ++w) v += ((const float*)sh.red[w])[i];
+        vsum[i / 4 % 16][(r0 + i / 256) * 16 + i % 256 / 64 * 4 + i % 4] = v;
+      }
+    }
+    __syncthreads();
+    const float sc = scale ? scale[a] : 1.0f;
+    for (int p = wave; p < TILE; p += FW) {
+      float v[VR], top = 0.0f;
+#pragma unroll
+      for (int q = 0; q < VR; ++q) {
+        const int r = lane + WAVE * q;
+        v[q] = r < rank ? vsum[p][r] * sc : 0.0f;  // past the rank zero, also where x is not finite
+        top = fmaxf(top, fabsf(v[q]));
+      }
+      int e = 0;
+      if constexpr (ACT == ACT_F16) {
+        top = wave_max(top);
+        if (top > 0.0f && top < INFINITY) e = __builtin_amdgcn_frexp_expf(top) - 14;
+        if (lane == 0) exps[p] = e;
+      }
+#pragma unroll
+      for (int q = 0; q < VR; ++q) {
+        const int r = lane + WAVE * q;
+        uint16_t parts[NP];
+        split_parts<ACT, NP>(ACT == ACT_F16 ? ldexp_f(v[q], -e) : v[q], parts);
+        if (r < RP) {
+#pragma unroll
+          for (int h = 0; h < NP; ++h) vs[h][p][r] = parts[h];
+        }
+      }
+    }
+    __syncthreads();
+
+    // ---- base + v B^T: this wave's every FW-th block of 32 columns
+    u32x4 vv[NP][STEPS];
+    load_parts<RT>(vs, l16, vv);
+    const int e = ACT == ACT_F16 ? exps[l16] : 0;
+    const int whole = vec ? min(b1, N / 32) : b0;  // blocks of 32 columns that can be moved in 16 bytes
+    int b = b0 + wave;
+#pragma unroll 1
+    for (; b < whole; b += FW * AHEAD) {
+#pragma unroll
+      for (int h = 0; h < AHEAD; ++h) {
+        const int now = b + FW * h;
+        if (now < whole) {
+          u32x4 bv[STEPS][2];
+          take_rows<RT>(braw[h % BAHEAD], rows, rank, sh.b[wave], bv);
+          rows.load(braw[h % BAHEAD], now + FW * BAHEAD, b1);
+          float d[8];
+          block_product<ACT, RT, NP>(bv, vv, e, d);
+          if (have) add_store<ACT, F32>(o[h], d, out, t * ldo + now * 32 + 8 * g);
+          load_o(o[h], now + FW * AHEAD);
+        }
+      }
+    }
+    // the others, element by element
+    b = b0 + wave + (max(whole - b0 - wave, 0) + FW - 1) / FW * FW;
+#pragma unroll 1
+    for (; b < b1; b += FW) {
+      u32x4 bv[STEPS][2];
+      rows.load(braw[0], b, b1);
+      take_rows<RT>(braw[0], rows, rank, sh.b[wave], bv);
+      float d[8];
+      block_product<ACT, RT, NP>(bv, vv, e, d);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = b * 32 + 8 * g + j;
+        if (have && c < N) {
+          if constexpr (F32)
+            ((float*)out)[t * ldo + c] = ((const float*)base)[t * ldb + c] + d[j];
+          else
+            ((uint16_t*)out)[t * ldo + c] =
+                (uint16_t)pack2<ACT>(act_to_f32(((const uint16_t*)base)[t * ldb + c], ACT) + d[j], 0.0f);
+        }
+      }
+    }
   }
 }
 
@@ -550,18 +607,19 @@ hipError_t launch_lora(const void* x, int act, int64_t ldx, int T, const LoraDev
   const int vec = ldb % per == 0 && ldo % per == 0 &&
                   ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
   const int chunks = (int)(((int64_t)T + CHUNK - 1) / CHUNK);
-  // About 256 workgroups side by side, from the sizes alone (the ids are on the
-  // device).  Few tokens cannot fill the chip with tiles: the output's columns
-  // are split, at the price of repeating x A^T (K = N = 4096: one token, rank
-  // 16: 8.3 us in eight parts, 12.7 in one; 64 tokens of 48 adapters, rank 32:
-  // 15.2 in four, 22.7 in one; 512 tokens of 48 adapters: 52 in two, 41 in one).
-  const int parts = T <= 16 ? 8 : T <= 128 ? 4 : T <= 256 ? 2 : 1;
-  const int Q = std::max(1, std::min(std::min(T, CHUNK), 256 / chunks));
-  const dim3 grid(chunks, Q, std::max(1, std::min(parts, (ad.N + 31) / 32 / FW)));
+  // A CU holds one workgroup: a chunk's share of 256 of them (512: 51.7 against
+  // 48.8 us for 4096 tokens, 20.5 against 14.0 for 64 tokens of 48 adapters).
+  // At most eight parts, each of a block of 32 columns a wave or more (one
+  // token, rank 16: 8.1 us in eight parts, 12.7 in one; sixteen: no faster).
+  const int share = std::max(1, 256 / chunks);
+  int most = 0;
+  while (most < MOST_CUT && (2 * FW) << most <= (ad.N + 31) / 32) ++most;
+  const int W = std::min(std::min(T, CHUNK) << most, share);
+  const dim3 grid(chunks, W);
   auto go = [&](auto kern) {
     return launch_kernel(kern, grid, 64 * FW, 0, st, (const uint16_t*)x, ldx, (const uint16_t*)ad.a,
                          (const uint16_t*)ad.b, ad.scale, ids, ad.ranks, base, ldb, out, ldo, T, ad.L, ad.R, ad.K, ad.N,
-                         vec);
+                         vec, share, most);
   };
   auto rank = [&](auto ac, auto fc) {
     constexpr int A = decltype(ac)::value;
