@@ -12,9 +12,8 @@
 //
 // Which of two experts is chosen is decided as keys formed in 64 bits decide
 // it, whatever the rounding of a 32-bit score: the selection runs on fp32
-// keys, whose error is bounded below, and a round in which another live key
-// lies within that bound of the best is decided again among those candidates
-// with keys in fp64.  Without a bias, and with groups ranked by their best
+// keys, whose error is bounded below, and a token in which two keys that matter
+// lie within that bound of each other is selected again with keys in fp64.  Without a bias, and with groups ranked by their best
 // expert, the logits give the order exactly and no score is formed for it.
 #include <type_traits>
 
@@ -46,6 +45,10 @@ __device__ __forceinline__ uint64_t key_of64(double v) {
   uint64_t u = __builtin_bit_cast(uint64_t, v);
   u ^= (uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull;
   return v != v ? 1u : u;
+}
+
+__device__ __forceinline__ double value_of64(uint64_t key) {
+  return __builtin_bit_cast(double, (key >> 63) != 0 ? key ^ 0x8000000000000000ull : ~key);
 }
 
 template <int CTRL, int ROWS>
@@ -170,11 +173,11 @@ constexpr float SIGMOID_EPS = 1e-20f;  // added to the selected scores' sum
 // ------------------------------------------------------ the exact order --
 //
 // One wave, one token: the k experts by keys in fp64, lane s returning slot
-// s's.  Taken only for tokens whose fp32 keys do not decide.  lds: one double
-// per expert.
+// s's.  Taken only for tokens whose fp32 keys do not decide.  lds: one key per
+// expert.
 template <int VPL, int LT>
 __device__ __forceinline__ int exact_experts(const void* __restrict__ logits, int64_t ld, int64_t t, int E, int k,
-                                             const GateDev& g, double* __restrict__ lds) {
+                                             const GateDev& g, uint64_t* __restrict__ lds) {
   const int lane = lane_id(), e0 = lane * VPL;
   double d[VPL];
   float m = -INFINITY;
@@ -212,33 +215,37 @@ __device__ __forceinline__ int exact_experts(const void* __restrict__ logits, in
     const int G = g.groups, gs = E / G;
     wave_lds_fence();
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) lds[e0 + j] = d[j];
+    for (int j = 0; j < VPL; ++j) lds[e0 + j] = key[j];
     wave_lds_fence();
-    uint64_t worth = 0ull;  // of group `lane`; G <= 64
-    if (lane < G) {
-      uint64_t b1 = 0, b2 = 0;
-      int i1 = 0, i2 = 0;
+    // `per` lanes a group (G <= 64) find its best two keys together
+    int shift = 0;
+    while (G << (shift + 1) <= WAVE) ++shift;
+    const int per = 1 << shift, group = lane >> shift, part = lane & (per - 1);
+    uint64_t b1 = 0, b2 = 0;
+    if (group < G) {
 #pragma unroll 4
-      for (int i = 0; i < gs; ++i) {
-        const uint64_t u = key_of64(lds[lane * gs + i]);
-        if (u > b1) {
-          b2 = b1, i2 = i1;
-          b1 = u, i1 = i;
-        } else if (u > b2) {
-          b2 = u, i2 = i;
-        }
+      for (int i = part; i < gs; i += per) {
+        const uint64_t u = lds[group * gs + i];
+        b2 = max(b2, min(b1, u));
+        b1 = max(b1, u);
       }
-      double v = lds[lane * gs + i1];
-      const double second = lds[lane * gs + i2];
-      if (g.group_best == 2 && second != -INFINITY) v = v + second;
-      worth = key_of64(v);
     }
+#pragma unroll 1
+    for (int off = 1; off < per; off <<= 1) {
+      const uint64_t o1 = lane_read64(b1, lane ^ off), o2 = lane_read64(b2, lane ^ off);
+      b2 = max(max(b2, o2), min(b1, o1));
+      b1 = max(b1, o1);
+    }
+    double v = value_of64(b1);
+    const double second = value_of64(b2);
+    if (g.group_best == 2 && second != -INFINITY) v = v + second;
+    uint64_t worth = group < G && part == 0 ? key_of64(v) : 0ull;
     uint64_t kept = 0;
 #pragma unroll 1
     for (int s = 0; s < g.group_k; ++s) {
-      const int win = wave_best64(worth, lane);
+      const int win = wave_best64(worth, group);
       kept |= 1ull << win;
-      if (lane == win) worth = 0ull;
+      if (group == win) worth = 0ull;
     }
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
@@ -299,10 +306,25 @@ __device__ __forceinline__ void sort8(double* v) {
 // and the lowest index) and one lane moves to its next, which is in registers
 // already while the one after it is read.
 //
+// Bound by vector instructions: 1000 a wave for 256 experts in groups with a
+// bias (16 exponentials and reciprocals a lane; 110 for the sort; 300 for nine
+// rounds), 27 us of the 30.4 that 65536 tokens take (67 MB of logits: 10 us at
+// the rate of a fill of that size).  A wave a token with 64-bit keys took 158 us.
+//   65536 x 256, sigmoid, bias, 8 groups of two's worth  30.4 us  (2.3 TB/s)
+//   65536 x 256, softmax, nothing else                   19.5 us  (3.6 TB/s)
+//   65536 x 64, sigmoid, bias                            11.0 us
+//   4096 x 64, sigmoid, bias  3.5 us;   64 x 256 in groups  4.8;   1 x 64  2.9
+// (an empty kernel: 2.3 us).  A workgroup is one wave: groups of four run
+// 0.4 us slower at 65536 tokens and 0.3 at 64, and 0.3 faster at 16384 x 64.  At
+// least five waves a SIMD: six spill (8192 x 256 in groups 0.3 us slower), eight
+// spill more (4 us slower at 65536).
+//
 // Where scores order the experts, the fp32 keys decide unless two that matter
 // lie within the window of their error: two slots next to each other, the
 // last slot and the best key left out, or the border of the kept groups.  Such
-// a token (under 1% of ordinary ones) is selected again by exact_experts.
+// a token (some 0.1% of ordinary ones at 256 experts) is selected again by
+// exact_experts, some 3 us of latency for its wave: 1.5 us of 4096 x 256 in
+// groups, and of 65536.
 // Equal logits with equal biases are exact ties and need no second look.
 //
 // Error bounds of the fp32 keys (u = 2^-24, products and sums rounded once,
@@ -319,21 +341,20 @@ __device__ __forceinline__ void sort8(double* v) {
 // KEY_ERR, SOFTMAX_ERR p_max and KEY_ROUND |key| are these with a margin.  Two
 // keys further apart than the sum of their errors keep their order.
 constexpr float KEY_ERR = 0x1.1p-22f, SOFTMAX_ERR = 0x1.48p-19f, KEY_ROUND = 0x1.1p-24f;
-constexpr int GATE_PITCH = 260;             // LDS words a token holds its keys in
-constexpr int GATE_WAVE_WORDS = 9 * 64 * 2;  // LDS words a wave: nine list entries a lane (the last is the end), four
-                                             // tokens' keys, or one double per expert of one token
-static_assert(GATE_WAVE_WORDS >= 4 * GATE_PITCH && GATE_WAVE_WORDS >= 2 * 256, "LDS of a wave");
+constexpr int GATE_PITCH = 260;         // LDS words a token holds its keys in
+constexpr int GATE_WORDS = 9 * 64 * 2;  // LDS words: nine list entries a lane (the last is the end), four tokens' keys,
+                                        // or one 64-bit key per expert of one token
+static_assert(GATE_WORDS >= 4 * GATE_PITCH && GATE_WORDS >= 2 * 256, "LDS of a wave");
 
 template <int EPL, int LT, bool by_score>
-__global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ logits, int64_t ld, int vec, int T, int E,
+__global__ __launch_bounds__(64, 5) void gate_kernel(const void* __restrict__ logits, int64_t ld, int vec, int T, int E,
                                                    int k, GateDev g, int32_t* __restrict__ idx,
                                                    float* __restrict__ w, int32_t* __restrict__ k_used,
                                                    float* __restrict__ entropy, int32_t* __restrict__ clear_word) {
-  extern __shared__ __attribute__((aligned(16))) uint32_t gate_lds[];
+  __shared__ __attribute__((aligned(16))) uint32_t wlds[GATE_WORDS];
   constexpr int LL = EPL < 8 ? EPL : 8;  // a lane's list: at most MOE_MAX_K of its experts are chosen
   const int lane = lane_id(), i16 = lane % 16, r = lane / 16;
-  uint32_t* const wlds = gate_lds + wave_id() * GATE_WAVE_WORDS;
-  const int64_t t0 = (int64_t)blockIdx.x * (blockDim.x / 16) + wave_id() * 4;
+  const int64_t t0 = (int64_t)blockIdx.x * 4;
   const int64_t t = t0 + r;
   const bool tv = t < T;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -617,7 +638,7 @@ __global__ __launch_bounds__(256, 6) void gate_kernel(const void* __restrict__ l
     while (again) {
       const int rr = (int)__builtin_ctzll(again) / 16;
       again &= ~(0xFFFFull << (16 * rr));
-      const int e = exact_experts<EPL / 4, LT>(logits, ld, t0 + rr, E, k, g, (double*)wlds);
+      const int e = exact_experts<EPL / 4, LT>(logits, ld, t0 + rr, E, k, g, (uint64_t*)wlds);
       const int mv = __builtin_amdgcn_ds_bpermute(i16 << 2, e);
       if (r == rr && i16 < k) {
         me = mv;
@@ -787,14 +808,12 @@ hipError_t launch_gate(const void* logits, int lt, int64_t ld, int T, int E, int
                        float* w, hipStream_t st, int32_t* k_used, float* entropy, int32_t* clear_word) {
   // four logits a load where rows start aligned to that
   const int vec = E % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) % (4 * lt_bytes(lt))) == 0;
-  const int waves = T <= 4096 ? 1 : 4;  // few tokens: a wave to a CU
-  const unsigned grid = (unsigned)(((int64_t)T + 4 * waves - 1) / (4 * waves));
-  const uint32_t lds = waves * GATE_WAVE_WORDS * 4;
+  const unsigned grid = (unsigned)(((int64_t)T + 3) / 4);
   auto go = [&](auto kern) {
-    return launch_kernel(kern, grid, 64 * waves, lds, st, logits, ld, vec, T, E, k, g, idx, w, k_used, entropy,
-                         clear_word);
+    return launch_kernel(kern, grid, 64, 0, st, logits, ld, vec, T, E, k, g, idx, w, k_used, entropy, clear_word);
   };
   // a bias, or groups ranked by two experts, order by scores; else the logits do
+  // (65536 x 256: 30 against 20 us)
   const bool by_score = g.bias != nullptr || (g.groups > 1 && g.group_best == 2);
   auto size = [&](auto lc, auto sc) {
     constexpr int LT = decltype(lc)::value;
