@@ -13,8 +13,9 @@
 // Which of two experts is chosen is decided as keys formed in 64 bits decide
 // it, whatever the rounding of a 32-bit score: the selection runs on fp32
 // keys, whose error is bounded below, and a token in which two keys that matter
-// lie within that bound of each other is selected again with keys in fp64.  Without a bias, and with groups ranked by their best
-// expert, the logits give the order exactly and no score is formed for it.
+// lie within that bound of each other is selected again with keys in fp64.
+// Without a bias, and with groups ranked by their best expert, the logits give
+// the order exactly and no score is formed for it.
 #include <type_traits>
 
 #include "common.hpp"
