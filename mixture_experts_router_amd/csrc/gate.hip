@@ -629,10 +629,13 @@ __global__ __launch_bounds__(64, 5) void gate_kernel(const void* __restrict__ lo
   float ls = held ? load_logit<LT>(logits, t * ld + me) : 0.0f;
   if (by_score) {
     const float bs = held && g.bias ? g.bias[me] : 0.0f;
-    const float v = value_of(mine), nv = value_of(dpp_next(mine));
+    // read from the next lane by every lane of the row: never behind a condition,
+    // which would switch the lane that is read off
+    const uint32_t after = dpp_next(mine);
+    const float v = value_of(mine), nv = value_of(after);
     const float nl = __builtin_bit_cast(float, dpp_next(__builtin_bit_cast(uint32_t, ls)));
     const float nb = __builtin_bit_cast(float, dpp_next(__builtin_bit_cast(uint32_t, bs)));
-    const bool rival = i16 < k && dpp_next(mine) != 0u;
+    const bool rival = i16 < k && after != 0u;
     const bool apart = v - nv > 2.0f * (key_err + KEY_ROUND * fabsf(v));  // false for NaN and infinities
     const bool tie = i16 + 1 < k && ls == nl && (bs == nb || ls == -INFINITY);
     uint64_t again = __ballot(tv && ((rival && !apart && !tie) || unsure));

@@ -439,3 +439,60 @@ def test_two_graphs_and_eager_calls_interleaved():
         for i in range(2):
             want = moe.gate_from_logits(src[i], 8, **kw)
             assert torch.equal(outs[i][0], want["idx"]) and torch.equal(outs[i][1], want["w"])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(16, 1, 0), (16, 3, 0), (64, 4, 0), (64, 8, 0), (100, 7, 0), (256, 8, 0), (256, 8, 8),
+                                        (256, 5, 8)])
+def test_only_the_last_slot_is_close(score, E, k, groups):
+    """The last slot and the best expert left out have keys that fp32 cannot tell apart; every other key is far off."""
+    T, a, b = 3000, E // 2 + 1, 2
+    rng = np.random.default_rng(E + k)
+    l = np.full((T, E), -4.0)
+    high = [e for e in range(E) if e not in (a, b)][::-1][:k - 1]
+    l[:, high] = 2.0 + 0.25 * np.arange(k - 1)
+    l[:, a] = rng.uniform(0.5, 1.5, T)
+    l[:, a] = l[:, b] = l[:, a].astype(np.float32)
+    bias = np.zeros(E, np.float32)
+    bias[a], bias[high] = 0.0625, 0.25
+    for _ in range(200):  # the logit of b that gives it a's key
+        if score == "sigmoid":
+            key = 1 / (1 + np.exp(-l[:, a])) + bias[a]
+            l[:, b] = np.log(key / (1 - key))
+        else:
+            z = np.exp(l).sum(1)
+            l[:, b] = np.log((np.exp(l[:, a]) / z + bias[a]) * (z - np.exp(l[:, b])) / (1 - np.exp(l[:, a]) / z - bias[a]))
+    logits = torch.from_numpy(l.astype(np.float32))
+    l64 = f64(logits)
+    s = 1 / (1 + np.exp(-l64)) if score == "sigmoid" else np.exp(l64) / np.exp(l64).sum(1, keepdims=True)
+    gap = s[:, a] + bias[a] - s[:, b]
+    assert np.median(np.abs(gap)) < 1e-7 and 0.2 < np.mean(gap > 0) < 0.8
+    rest = np.delete(s + bias, [a, b], 1)
+    assert np.sum(np.abs(rest - s[:, a:a + 1] - bias[a]) < 1e-3) == 0
+    kw = dict(groups=groups, group_k=groups, group_best=2) if groups else {}
+    check(logits, k, bias=torch.from_numpy(bias), score=score, **kw)
+
+
+@pytest.mark.parametrize("E,G,group_k", [(256, 8, 4), (64, 8, 2), (64, 2, 1), (128, 4, 3), (96, 6, 3), (60, 6, 4), (250, 50, 2),
+                                         (24, 3, 2), (128, 64, 3)])
+def test_only_the_border_of_the_groups_is_close(E, G, group_k):
+    """The last group kept and the first one left out are worth the same up to less than fp32's rounding; the keys
+    themselves, and the other groups, are far apart."""
+    T, gs, k = 2000, E // G, 2 * group_k
+    rng = np.random.default_rng(E + G)
+    order = rng.permutation(G)
+    a, b, high = order[0] * gs, order[1] * gs, order[2:group_k + 1] * gs
+    sig = lambda v: 1 / (1 + np.exp(-v))  # noqa: E731
+    l = np.full((T, E), -4.0)
+    for i, g in enumerate(high):
+        l[:, g], l[:, g + gs - 1] = 3.0 + 0.4 * i, 3.2 + 0.4 * i
+    l[:, a], l[:, a + gs - 1], l[:, b] = rng.uniform(0.5, 1.0, T).astype(np.float32), 0.25, 1.125
+    bias = np.zeros(E, np.float32)
+    bias[b], bias[b + gs - 1] = 0.0625, 0.0625
+    other = sig(l[:, a]) + sig(l[:, a + gs - 1]) - sig(l[:, b]) - 0.125
+    l[:, b + gs - 1] = np.log(other / (1 - other))
+    logits = torch.from_numpy(l.astype(np.float32))
+    keys = sig(f64(logits)) + bias
+    gap = keys[:, a] + keys[:, a + gs - 1] - keys[:, b] - keys[:, b + gs - 1]
+    assert np.median(np.abs(gap)) < 1e-7 and 0.2 < np.mean(gap > 0) < 0.8
+    check(logits, k, bias=torch.from_numpy(bias), score="sigmoid", groups=G, group_k=group_k, group_best=2)

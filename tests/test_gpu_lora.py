@@ -365,3 +365,32 @@ def test_gated_layer_replays_in_a_graph():
         torch.cuda.synchronize()
         got = host_bits(out)
         assert np.array_equal(got, host_bits(run(None, ws)))  # an eager call on the same workspace in between
+
+
+def test_threads_calling_at_once():
+    """Four host threads, each on a stream of its own: the calls share no state."""
+    import threading
+    c = {n: t.cuda() for n, t in make(21, 40, 256, 96, 5, 32, "bf16", "f32").items()}
+    opts = dict(score="sigmoid", groups=8, group_k=4, group_best=2)
+    want = moe.lora_add(**c)
+    gate = moe.gate_from_logits(want, 6, **opts)
+    grad = moe.gate_backward(want, gate["idx"], gate["w"], score="sigmoid")
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(40):
+            y = moe.lora_add(**c, stream=s)
+            r = moe.gate_from_logits(y, 6, stream=s, **opts)
+            g = moe.gate_backward(y, r["idx"], r["w"], score="sigmoid", stream=s)
+            s.synchronize()
+            if not (torch.equal(y, want) and torch.equal(r["idx"], gate["idx"]) and torch.equal(g, grad)):
+                bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
