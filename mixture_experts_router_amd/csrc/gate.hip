@@ -314,7 +314,7 @@ __device__ __forceinline__ void sort8(double* v) {
 //   65536 x 256, sigmoid, bias, 8 groups of two's worth  30.4 us  (2.3 TB/s)
 //   65536 x 256, softmax, nothing else                   19.5 us  (3.6 TB/s)
 //   65536 x 64, sigmoid, bias                            11.0 us
-//   4096 x 64, sigmoid, bias  3.5 us;   64 x 256 in groups  4.8;   1 x 64  2.9
+//   4096 x 64, sigmoid, bias  3.8 us;   64 x 256 in groups  4.7;   1 x 64  2.9
 // (an empty kernel: 2.3 us).  A workgroup is one wave: groups of four run
 // 0.4 us slower at 65536 tokens and 0.3 at 64, and 0.3 faster at 16384 x 64.  At
 // least five waves a SIMD: six spill (8192 x 256 in groups 0.3 us slower), eight

@@ -496,3 +496,31 @@ def test_only_the_border_of_the_groups_is_close(E, G, group_k):
     gap = keys[:, a] + keys[:, a + gs - 1] - keys[:, b] - keys[:, b + gs - 1]
     assert np.median(np.abs(gap)) < 1e-7 and 0.2 < np.mean(gap > 0) < 0.8
     check(logits, k, bias=torch.from_numpy(bias), score="sigmoid", groups=G, group_k=group_k, group_best=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,group_k,dtype", [(256, 8, 8, 4, "f32"), (256, 8, 0, 0, "f32"), (128, 6, 4, 2, "f32"),
+                                                      (160, 6, 10, 3, "f32"), (64, 4, 0, 0, "bf16"), (48, 8, 6, 5, "f16")])
+def test_long_batches_against_64_bits(score, E, k, groups, group_k, dtype):
+    """131072 tokens, with the same order formed in 64 bits by torch's stable sorts: enough for dozens of near ties."""
+    l = logits_of(E + k, 131072, E, dtype).cuda()
+    bias = (torch.randn(E, generator=torch.Generator().manual_seed(4)) * 0.05).cuda()
+    kw = dict(groups=groups, group_k=group_k, group_best=2) if groups else {}
+    got = moe.gate_from_logits(l, k, score=score, bias=bias, **kw)
+    l64 = l.double()
+    keys = (torch.sigmoid(l64) if score == "sigmoid" else torch.softmax(l64, 1)) + bias.double()
+    if groups:
+        worth = keys.view(-1, groups, E // groups).topk(2, -1).values.sum(-1)
+        kept = worth.sort(dim=1, descending=True, stable=True).indices[:, :group_k]
+        live = torch.zeros_like(worth, dtype=torch.bool).scatter_(1, kept, True)
+        keys = torch.where(live.repeat_interleave(E // groups, 1), keys, -torch.inf)
+    vals, want = keys.sort(dim=1, descending=True, stable=True)
+    # near ties among the inputs: k gaps a token of some 0.02 on average, so 131072 * 4 * 1e-6 / 0.02 = 26 for the fewest
+    # slots, with a deviation of 5: five deviations leave none below 1
+    assert ((vals[:, :k] - vals[:, 1:k + 1]).min(1).values < 1e-6).sum() >= 1
+    # the reference's own 64-bit rounding decides below 2^-50
+    close = (vals[:, :k] - vals[:, 1:k + 1]).min(1).values
+    bad = (got["idx"] != want[:, :k]).any(1) & ((close > 2.0 ** -50) | (close == 0))
+    if dtype != "f32":  # equal logits of unequal biases: equal keys only by rounding
+        bad &= close > 2.0 ** -50
+    assert int(bad.sum()) == 0, bad.nonzero().flatten()[:4].tolist()
