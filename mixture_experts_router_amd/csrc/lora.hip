@@ -17,16 +17,18 @@
 //
 // Time, and what bounds it (K = N = 4096 unless said; a card that copies 1 GB
 // at 5.1 TB/s and launches an empty kernel in 2.3 us):
-//   1 token, rank 16, fp16                    8.1 us   0.3 MB: a chain of dependent
+//   1 token, rank 16, fp16                    7.8 us   0.3 MB: a chain of dependent
 //       loads (ids, A, the sums through LDS, B and base), each 0.5 .. 1 us, and
-//       some 1100 instructions a wave in a row
-//   64 tokens of 48 adapters, rank 32, bf16  13.0 us  16.5 MB: the same chain, with
+//       some thousand instructions a wave in a row
+//   64 tokens of 48 adapters, rank 32, bf16  12.3 us  16.5 MB: the same chain, with
 //       A's and B's rows from HBM in it (1.3 TB/s over the whole call)
-//   777 tokens, N = 64, rank 8, fp32 out     10.2 us   7.6 MB: likewise
-//   4096 tokens in runs of 6, rank 64, bf16  48.5 us   105 MB, 2.2 TB/s: a tile's
-//       workgroup takes 1.2 MB through its CU (x and base 0.25 MB, A and B 1 MB
-//       from L2), some 20 us for each product; the two do not overlap, as there
-//       is one workgroup a CU (its registers), and all start together
+//   777 tokens, N = 64, rank 8, fp32 out     10.3 us   7.6 MB: likewise
+//   4096 tokens in runs of 6, rank 64, bf16  48.5 us   105 MB, 2.2 TB/s: some 20 us for
+//       each product, which do not overlap (one workgroup a CU).  Neither is
+//       bound by one thing: without the loads of A 38 us, of B 45, of x 46, of
+//       base 45, without the stores 42.5, without base and stores 40.  Eight
+//       waves hide the latencies of loads, LDS and matrix instructions only in
+//       part, and sixteen do not fit the registers of 64 ranks
 #include <algorithm>
 #include <type_traits>
 
@@ -361,7 +363,7 @@ __device__ __forceinline__ void add_store(const u32x4 (&o)[F32 ? 2 : 1], const f
 // ----------------------------------------------------------- the kernel --
 //
 // Both products of a tile (up to 16 tokens of one adapter) in one workgroup
-// of eight waves: the waves take consecutive parts of K and are added through
+// of eight or sixteen waves: the waves take consecutive parts of K and are added through
 // LDS in wave order, the tokens' sums are split into the parts the matrix
 // cores take, and the waves share the output's columns.
 //
@@ -373,11 +375,18 @@ __device__ __forceinline__ void add_store(const u32x4 (&o)[F32 ? 2 : 1], const f
 // alone: 1024 tokens in runs, rank 64, 22.0 against 27.3 us; 300 tokens, rank
 // 16, 12.5 against 17.8; 64 tokens of 48 adapters, rank 32, 13.0 against 14.4; 8
 // tokens, rank 64, 15.9 against 14.8.  The result does not depend on it.
-constexpr int FW = 8;        // waves (sixteen, with 128 registers each: 79 us for 4096 tokens)
+
+// Waves by the ranks: sixteen of 128 registers where their operands fit, up to
+// 32 ranks (against eight: 64 tokens of 48 adapters, rank 32, 12.3 and 13.1 us; 4096
+// tokens of 48 adapters, K = N = 1024, rank 16, 38 and 50; one token, rank 16, 7.8 and
+// 8.1; the same within 0.3 us for runs of one adapter), eight above (rank 64, 4096
+// tokens: 48.5 us, 62 with sixteen).
+template <int RT>
+constexpr int WAVES = RT <= 2 ? 16 : 8;
 constexpr int MOST_CUT = 3;  // at most 2^3 parts of the columns
 
 template <int ACT, bool F32, int RT>
-__global__ __launch_bounds__(64 * FW) void lora_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+__global__ __launch_bounds__(64 * WAVES<RT>) void lora_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                                        const uint16_t* __restrict__ am,
                                                        const uint16_t* __restrict__ bm,
                                                        const float* __restrict__ scale,
@@ -385,19 +394,18 @@ __global__ __launch_bounds__(64 * FW) void lora_kernel(const uint16_t* __restric
                                                        const int32_t* __restrict__ ranks, const void* base,
                                                        int64_t ldb, void* out, int64_t ldo, int T, int L, int R, int K,
                                                        int N, int vec, int share, int most) {
-  constexpr int NP = F32 && ACT == ACT_BF16 ? 3 : 2;
+  constexpr int FW = WAVES<RT>, NP = F32 && ACT == ACT_BF16 ? 3 : 2;
   constexpr int STEPS = RT == 1 ? 1 : RT / 2;  // 32-rank steps of the second product
   constexpr int RP = RT * 16, TILE = 16;
   constexpr int RB = RT < 4 ? RT : RT == 8 ? 2 : 4;  // rank tiles loaded, and summed over the waves, together
   constexpr int H = RT / RB;
   // Loads in flight a wave: items of the first product, and of the second
-  // base's blocks (from HBM) and B's (from L2).  More of them spill (RT = 4) or
-  // only lengthen the code (RT = 1, four items: 8.8 against 8.4 us for one token;
-  // RT <= 2, four of base's blocks: 14.8 against 14.4 us for 64 tokens of 48
-  // adapters; RT = 4, two of them: 51 against 48.7 us for 4096 tokens).
-  constexpr int DEEP = RT == 4 ? 1 : 2;
+  // base's blocks (from HBM) and B's (from L2).  With sixteen waves one of each;
+  // two items spill (one token: 9.9 against 7.8 us).  RT = 4: two items spill, two
+  // of base's blocks give 51 us for 4096 tokens against 48.7, and four of B's 50.4.
+  constexpr int DEEP = RT <= 4 ? 1 : 2;
   constexpr int TURN = DEEP < H ? H : DEEP;
-  constexpr int AHEAD = F32 || RT <= 2 ? 2 : 4, BAHEAD = RT == 8 ? 1 : 2;
+  constexpr int AHEAD = RT <= 2 ? 1 : F32 ? 2 : 4, BAHEAD = RT == 4 ? 2 : 1;
   constexpr int OV = F32 ? 2 : 1;
   constexpr int VR = (RP + WAVE - 1) / WAVE;
   union Shared {
@@ -609,25 +617,25 @@ hipError_t launch_lora(const void* x, int act, int64_t ldx, int T, const LoraDev
   const int chunks = (int)(((int64_t)T + CHUNK - 1) / CHUNK);
   // A CU holds one workgroup: a chunk's share of 256 of them (512: 51.7 against
   // 48.8 us for 4096 tokens, 20.5 against 14.0 for 64 tokens of 48 adapters).
-  // At most eight parts, each of a block of 32 columns a wave or more (one
-  // token, rank 16: 8.1 us in eight parts, 12.7 in one; sixteen: no faster).
+  // At most eight parts, each of eight blocks of 32 columns or more (one token,
+  // rank 16: 8 us in eight parts, 12.7 in one; sixteen: no faster).
   const int share = std::max(1, 256 / chunks);
   int most = 0;
-  while (most < MOST_CUT && (2 * FW) << most <= (ad.N + 31) / 32) ++most;
+  while (most < MOST_CUT && 16 << most <= (ad.N + 31) / 32) ++most;
   const int W = std::min(std::min(T, CHUNK) << most, share);
   const dim3 grid(chunks, W);
-  auto go = [&](auto kern) {
-    return launch_kernel(kern, grid, 64 * FW, 0, st, (const uint16_t*)x, ldx, (const uint16_t*)ad.a,
+  auto go = [&](auto kern, int threads) {
+    return launch_kernel(kern, grid, threads, 0, st, (const uint16_t*)x, ldx, (const uint16_t*)ad.a,
                          (const uint16_t*)ad.b, ad.scale, ids, ad.ranks, base, ldb, out, ldo, T, ad.L, ad.R, ad.K, ad.N,
                          vec, share, most);
   };
   auto rank = [&](auto ac, auto fc) {
     constexpr int A = decltype(ac)::value;
     constexpr bool F = decltype(fc)::value;
-    return ad.R <= 16   ? go(lora_kernel<A, F, 1>)
-           : ad.R <= 32 ? go(lora_kernel<A, F, 2>)
-           : ad.R <= 64 ? go(lora_kernel<A, F, 4>)
-                        : go(lora_kernel<A, F, 8>);
+    return ad.R <= 16   ? go(lora_kernel<A, F, 1>, 64 * WAVES<1>)
+           : ad.R <= 32 ? go(lora_kernel<A, F, 2>, 64 * WAVES<2>)
+           : ad.R <= 64 ? go(lora_kernel<A, F, 4>, 64 * WAVES<4>)
+                        : go(lora_kernel<A, F, 8>, 64 * WAVES<8>);
   };
   auto type = [&](auto ac) { return out_f32 ? rank(ac, std::true_type{}) : rank(ac, std::false_type{}); };
   return act == ACT_BF16 ? type(std::integral_constant<int, ACT_BF16>{}) : type(std::integral_constant<int, ACT_F16>{});
