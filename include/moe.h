@@ -380,10 +380,13 @@ moe_status moe_layer_forward_noalloc(const void* x, moe_dtype dt, int32_t T, int
  * compared as if formed in 64 bits; weights are fp32.
  * A logit of -inf masks an expert: its score and its weight are 0 (also in a
  * row that masks every expert) and its key is -inf whatever its bias, so the
- * other experts of the kept groups come first.  A key of -inf adds nothing to
- * its group's sum as the second best.  A NaN logit is the last choice of all;
- * it makes softmax weights (renormalised: only if it is chosen) NaN.  Chosen
- * indices are always distinct and within [0, E).
+ * other experts of the kept groups come first.  A NaN logit is the last choice
+ * of all, after the masked ones: its key is NaN, and the softmax that orders
+ * the others leaves it out.  A key of -inf or NaN adds nothing to its group's
+ * sum as the second best.  Where there are logits of +inf, the softmax that
+ * orders is its limit: 1 / n for each of n, and 0 for the others.  Softmax
+ * weights are NaN in a row with a NaN or +inf (renormalised: if it is chosen).
+ * Chosen indices are always distinct and within [0, E).
  *
  *   score      moe_score
  *   bias       fp32 [E] on the device, or NULL

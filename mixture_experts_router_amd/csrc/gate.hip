@@ -7,7 +7,9 @@
 //   keys; the group_k best groups stay; the k best keys among them are chosen,
 //   the lower index first among equal keys
 //   l_e = -inf masks e: s_e = 0 and key_e = -inf, whatever the bias; a key of
-//   -inf adds nothing as a group's second best
+//   -inf or NaN adds nothing as a group's second best
+//   for the order, a softmax leaves NaN logits out of its maximum and sum, and
+//   takes its limit where there are logits of +inf
 //   w_j   = c s_j,  or renormalised  c s_j / sum_r s_r   (sigmoid: + 1e-20)
 //
 // Which of two experts is chosen is decided as keys formed in 64 bits decide
@@ -191,16 +193,19 @@ __device__ __forceinline__ int exact_experts(const void* __restrict__ logits, in
     d[j] = (double)l;
   }
   if (g.score == GATE_SOFTMAX) {
-    m = wave_max(m);
+    m = wave_max(m);  // fmaxf passes over NaN
     double z = 0.0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      d[j] = masked[j] ? 0.0 : exp(d[j] - (double)m);
-      z += d[j];
+      const bool nan = d[j] != d[j];
+      if (masked[j]) d[j] = 0.0;
+      else if (m < INFINITY) d[j] = exp(d[j] - (double)m);
+      else if (!nan) d[j] = d[j] == INFINITY ? 1.0 : 0.0;
+      z += nan ? 0.0 : d[j];
     }
     z = wave_sum64(z);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) d[j] = d[j] / z;  // z = 0 only where all are masked
+    for (int j = 0; j < VPL; ++j) d[j] = d[j] / z;  // z = 0 only where all are masked or NaN
   } else {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) d[j] = 1.0 / (1.0 + exp(-d[j]));
@@ -239,7 +244,7 @@ __device__ __forceinline__ int exact_experts(const void* __restrict__ logits, in
     }
     double v = value_of64(b1);
     const double second = value_of64(b2);
-    if (g.group_best == 2 && second != -INFINITY) v = v + second;
+    if (g.group_best == 2 && second > -INFINITY) v = v + second;
     uint64_t worth = group < G && part == 0 ? key_of64(v) : 0ull;
     uint64_t kept = 0;
 #pragma unroll 1
