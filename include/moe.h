@@ -384,9 +384,11 @@ moe_status moe_layer_forward_noalloc(const void* x, moe_dtype dt, int32_t T, int
  * of all, after the masked ones: its key is NaN, and the softmax that orders
  * the others leaves it out.  A key of -inf or NaN adds nothing to its group's
  * sum as the second best.  Where there are logits of +inf, the softmax that
- * orders is its limit: 1 / n for each of n, and 0 for the others.  Softmax
- * weights are NaN in a row with a NaN or +inf (renormalised: if it is chosen).
- * Chosen indices are always distinct and within [0, E).
+ * orders is its limit: 1 / n for each of n, and 0 for the others.  Weights are
+ * NaN where their formula is: with softmax in a row with a NaN or +inf
+ * (renormalised: if it is chosen), with sigmoid for a NaN that is chosen
+ * (renormalised: and for those beside it); never for a masked expert.  Chosen
+ * indices are always distinct and within [0, E).
  *
  *   score      moe_score
  *   bias       fp32 [E] on the device, or NULL

@@ -668,11 +668,11 @@ __global__ __launch_bounds__(64, 5) void gate_kernel(const void* __restrict__ lo
     } else {
       wt = expf(ls - m_all) / z_all;
     }
-    wt = masked ? 0.0f : wt;
   } else {
     const float s1 = on ? sigmoid_f32(ls) : 0.0f;
     wt = g.renorm ? s1 / (sum8(s1) + SIGMOID_EPS) : s1;
   }
+  wt = masked ? 0.0f : wt;  // also beside a NaN
   if (on) {
     idx[t * k + i16] = me;
     w[t * k + i16] = g.scale * wt;

@@ -2,13 +2,14 @@
 
 A NaN logit is the last choice of all, after the masked experts: the softmax that orders the others leaves it out, and
 it adds nothing to its group's worth as the second best.  A logit of +inf has the softmax's limit as its score: 1 / n
-for each of n, and 0 for the others.
+for each of n, and 0 for the others.  Weights of such rows are NaN where their formula is, and 0 for masked experts all
+the same.
 """
 import numpy as np
 import pytest
 import torch
 
-from gate_ref64 import rank_order
+from gate_ref64 import rank_order, weights64
 
 
 def scores64(l, score):
@@ -110,3 +111,22 @@ def test_order_of_rows_that_are_not_finite(score, with_bias, E, k, groups, group
         idx = r["idx"].cpu().numpy()
         bad = np.flatnonzero((idx != want).any(1))
         assert bad.size == 0, (bad[:5], idx[bad[:3]], want[bad[:3]])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k,groups,group_k,group_best", SHAPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_weights_of_rows_that_are_not_finite(score, renorm, E, k, groups, group_k, group_best):
+    import mixture_experts_router_amd as moe
+    l = rows(E + k, E)
+    r = moe.gate_from_logits(l.cuda(), k, score=score, renorm=renorm, groups=groups, group_k=group_k, group_best=group_best)
+    idx, w, l64 = r["idx"].cpu().numpy(), r["w"].double().cpu().numpy(), l.double().numpy()
+    with np.errstate(all="ignore"):
+        want = weights64(l64, idx, score, renorm)
+    masked = np.isneginf(np.take_along_axis(l64, idx.astype(np.int64), 1))
+    assert masked.any() and np.all(w[masked] == 0)
+    want[masked] = 0.0
+    assert np.isnan(want).any() and np.array_equal(np.isnan(w), np.isnan(want))
+    # 2^-17: an exponent of up to 40 rounded once, two ulps each of exponential, division and logistic, eight sums
+    assert np.all(np.abs(np.nan_to_num(w) - np.nan_to_num(want)) <= 2.0 ** -17 * np.nan_to_num(want) + 1e-37)
