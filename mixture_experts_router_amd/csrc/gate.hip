@@ -182,39 +182,35 @@ template <int VPL, int LT>
 __device__ __forceinline__ int exact_experts(const void* __restrict__ logits, int64_t ld, int64_t t, int E, int k,
                                              const GateDev& g, uint64_t* __restrict__ lds) {
   const int lane = lane_id(), e0 = lane * VPL;
+  // +inf lies far beyond every other logit, which makes the scores their limits
+  auto finite = [](float l) { return l == INFINITY ? 1e300 : (double)l; };
   double d[VPL];
-  float m = -INFINITY;
-  bool masked[VPL];
+  float l[VPL], m = -__FLT_MAX__;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    const float l = e0 + j < E ? load_logit<LT>(logits, t * ld + e0 + j) : -INFINITY;
-    masked[j] = l == -INFINITY;
-    m = fmaxf(m, l);
-    d[j] = (double)l;
+    l[j] = e0 + j < E ? load_logit<LT>(logits, t * ld + e0 + j) : -INFINITY;
+    m = fmaxf(m, l[j]);  // passes over NaN
   }
   if (g.score == GATE_SOFTMAX) {
-    m = wave_max(m);  // fmaxf passes over NaN
+    const double top = finite(wave_max(m));
     double z = 0.0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      const bool nan = d[j] != d[j];
-      if (masked[j]) d[j] = 0.0;
-      else if (m < INFINITY) d[j] = exp(d[j] - (double)m);
-      else if (!nan) d[j] = d[j] == INFINITY ? 1.0 : 0.0;
-      z += nan ? 0.0 : d[j];
+      d[j] = exp(finite(l[j]) - top);
+      z += __builtin_fmax(d[j], 0.0);  // NaN adds nothing
     }
     z = wave_sum64(z);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) d[j] = d[j] / z;  // z = 0 only where all are masked or NaN
   } else {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) d[j] = 1.0 / (1.0 + exp(-d[j]));
+    for (int j = 0; j < VPL; ++j) d[j] = 1.0 / (1.0 + exp(-(double)l[j]));
   }
   uint64_t key[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     if (g.bias && e0 + j < E) d[j] = d[j] + (double)g.bias[e0 + j];
-    if (masked[j]) d[j] = -INFINITY;
+    if (l[j] == -INFINITY) d[j] = -INFINITY;
     key[j] = e0 + j < E ? key_of64(d[j]) : 0ull;
   }
   if (g.groups > 1) {
