@@ -457,6 +457,7 @@ __global__ __launch_bounds__(64, 5) void gate_kernel(const void* __restrict__ lo
   auto range = [&](uint32_t best, uint32_t next, uint32_t& low, uint32_t& high) __attribute__((always_inline)) {
     low = high = best;
     if (!by_score || best == 0u) return;
+    if (value_of(best) == -INFINITY) return;  // every expert masked (or its bias -inf): worth -inf, exactly
     float v = value_of(best), err = key_err + KEY_ROUND * fabsf(v);
     if (g.group_best == 2) {
       const float v2 = value_of(next);
