@@ -12,8 +12,8 @@
 // the second product v goes to the matrix cores as two 16-bit parts (hi + lo:
 // 2^-18 relative for bf16, 2^-22 for fp16), three for a bf16 adapter with an
 // fp32 output, so the only rounding that shows is the output's.  fp16 parts are
-// taken of v * 2^-e_t, the token's largest |v| brought to 2^13 .. 2^14, which
-// keeps fp32's range.
+// taken of v * 2^-e_t, the token's largest finite |v| brought to 2^13 .. 2^14,
+// which keeps fp32's range.
 //
 // Time, and what bounds it (K = N = 4096 unless said; a card that copies 1 GB
 // at 5.1 TB/s and launches an empty kernel in 2.3 us):
@@ -540,12 +540,13 @@ __global__ __launch_bounds__(64 * WAVES<RT>) void lora_kernel(const uint16_t* __
       for (int q = 0; q < VR; ++q) {
         const int r = lane + WAVE * q;
         v[q] = r < rank ? vsum[p][r] * sc : 0.0f;  // past the rank zero, also where x is not finite
-        top = fmaxf(top, fabsf(v[q]));
+        const float size = fabsf(v[q]);
+        top = fmaxf(top, size < INFINITY ? size : 0.0f);  // an infinite or NaN rank leaves the others their scale
       }
       int e = 0;
       if constexpr (ACT == ACT_F16) {
         top = wave_max(top);
-        if (top > 0.0f && top < INFINITY) e = __builtin_amdgcn_frexp_expf(top) - 14;
+        if (top > 0.0f) e = __builtin_amdgcn_frexp_expf(top) - 14;
         if (lane == 0) exps[p] = e;
       }
 #pragma unroll

@@ -1,0 +1,42 @@
+"""Adapters with infinite or huge values on the GPU against 64-bit numpy: infinite and NaN where the definition is,
+and within the bounds of test_gpu_lora.py elsewhere."""
+import numpy as np
+import pytest
+import torch
+
+from gate_ref64 import lora64
+from test_gpu_lora import call, f64, make
+
+pytestmark = pytest.mark.gpu
+
+
+def compare(c, **kw):
+    got = f64(call(c, **kw))
+    ref = {n: None if v is None else f64(v) if n == "scale" else v.numpy() for n, v in kw.items()}
+    with np.errstate(all="ignore"):
+        want, mag, vmag = lora64(f64(c["x"]), f64(c["base"]), c["ids"].numpy(), f64(c["a"]), f64(c["b"]), **ref)
+    assert np.array_equal(np.isnan(got), np.isnan(want)), "NaN in other places"
+    assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)]), "infinities"
+    fin = np.isfinite(want)
+    K, R, dt = c["x"].shape[1], c["a"].shape[1], c["base"].dtype
+    left = 2.0 ** -17 if c["x"].dtype == torch.bfloat16 and dt != torch.float32 else 2.0 ** -21
+    with np.errstate(all="ignore"):
+        tol = (K + 3 * R + 64) * 2.0 ** -24 * (mag + np.abs(want)) + left * vmag
+        if dt != torch.float32:
+            tol += torch.finfo(dt).eps / 2 * (np.abs(want) + tol)
+        assert np.all(np.abs(got - want)[fin] <= tol[fin] + 1e-37)
+    return want
+
+
+@pytest.mark.parametrize("out", ["same", "f32"])
+@pytest.mark.parametrize("R", [16, 128])
+def test_an_infinite_rank_beside_values_beyond_fp16(out, R):
+    """An infinite row of A makes its own rank infinite; the other ranks, past fp16's range, still count as numbers."""
+    c = make(R, 20, 64, 48, 2, R, "f16", out)
+    c["x"], c["a"], c["b"] = c["x"].abs() + 50, c["a"].abs() * 8 + 30, c["b"].abs() + 0.5
+    c["a"][0, 0, 7], c["a"][1, R - 1, 8] = torch.inf, -torch.inf
+    c["b"][0, :, 3], c["b"][1, :, 4] = -1.0, 2.0
+    c["b"][:, ::2, 0] *= -1
+    want = compare(c)
+    ids = c["ids"].numpy()
+    assert np.isinf(want[ids >= 0]).all() and (want[ids == 0] > 0).any() and (want[ids == 0] < 0).any()
