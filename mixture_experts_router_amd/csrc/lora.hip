@@ -127,14 +127,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // splits v (finite or not) into NP 16-bit parts, each the rounding of what
-// the earlier ones leave
+// the earlier ones leave; a number between bf16's largest and fp32's has the
+// largest as its first part
 template <int ACT, int NP>
 __device__ __forceinline__ void split_parts(float v, uint16_t* o) {
+  constexpr float MOST = 0x1.fefffep127f;  // rounds to bf16's largest
+  const bool finite = fabsf(v) < INFINITY;  // inf and NaN are the first part alone
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    o[i] = (uint16_t)pack2<ACT>(v, 0.0f);
-    const float f = act_to_f32(o[i], ACT);
-    v = fabsf(f) < INFINITY ? v - f : 0.0f;  // inf and NaN are the first part alone
+    o[i] = (uint16_t)pack2<ACT>(ACT == ACT_BF16 && i == 0 && finite ? __builtin_amdgcn_fmed3f(v, -MOST, MOST) : v, 0.0f);
+    v = finite ? v - act_to_f32(o[i], ACT) : 0.0f;
   }
 }
 

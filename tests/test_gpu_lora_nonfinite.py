@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gate_ref64 import lora64
-from test_gpu_lora import call, f64, make
+from test_gpu_lora import call, check, f64, make
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,17 @@ def test_an_infinite_rank_beside_values_beyond_fp16(out, R):
     want = compare(c)
     ids = c["ids"].numpy()
     assert np.isinf(want[ids >= 0]).all() and (want[ids == 0] > 0).any() and (want[ids == 0] < 0).any()
+
+
+@pytest.mark.parametrize("out", ["same", "f32"])
+@pytest.mark.parametrize("R", [8, 32, 64])
+def test_values_beyond_bf16(out, R):
+    """v = 3.4e38 is an fp32 number that rounds to infinity in bf16 (whose largest is 3.3895e38)."""
+    c = make(R, 20, 64, 40, 2, R, "bf16", out)
+    c["a"].zero_()
+    c["a"][:, 0, 0] = 1.0
+    c["x"][:, 0] = 1.0
+    c["x"][3:9, 0] = -1.0
+    c["base"].zero_()
+    c["b"] *= 2.0 ** -20
+    check(c, scale=torch.tensor([3.4e38, -3.4e38]))
