@@ -63,6 +63,19 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
                                                   0);
 }
 
+// up to 16 ranks: half the columns an instruction
+template <int ACT>
+__device__ __forceinline__ f32x4 mfma16(u32x2 a, u32x2 b, f32x4 c) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+  if constexpr (ACT == ACT_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0,
+                                                     0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(f16x4, a), __builtin_bit_cast(f16x4, b), c, 0, 0,
+                                                 0);
+}
+
 // the chunk's adapter of this lane's token: -1 none (also for ids outside
 // [0, L)), -2 past the last token
 __device__ __forceinline__ int chunk_id(const int32_t* __restrict__ ids, int64_t t0, int T, int L) {
@@ -136,6 +149,8 @@ __device__ __forceinline__ void split_parts(float v, uint16_t* o) {
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     o[i] = (uint16_t)pack2<ACT>(ACT == ACT_BF16 && i == 0 && finite ? __builtin_amdgcn_fmed3f(v, -MOST, MOST) : v, 0.0f);
+    // scaled fp16: never 0 for a number that is not, which an infinity in B would show
+    if (ACT == ACT_F16 && i == 0 && v != 0.0f && (o[i] & 0x7FFFu) == 0) o[i] |= 1u;
     v = finite ? v - act_to_f32(o[i], ACT) : 0.0f;
   }
 }
@@ -245,28 +260,25 @@ __device__ __forceinline__ rsrc_t chunk_rows(const void* p, int es, int64_t t0, 
   return make_rsrc((const uint8_t*)p + t0 * ld * es, (uint32_t)(((rows - 1) * ld + n) * es));
 }
 
-// the parts of token p's v as operands: RT = 1 (up to 16 ranks) puts the first
-// two side by side in one instruction's 32 columns
+// what a lane holds of a rank step: eight of 32 ranks, four of 16
+template <int RT>
+using Piece = std::conditional_t<RT == 1, u32x2, u32x4>;
+
+// the parts of token p's v as operands
 template <int RT, int NP, int STEPS, int ROWS, int PITCH>
-__device__ __forceinline__ void load_parts(const uint16_t (&vs)[NP][ROWS][PITCH], int p, u32x4 (&vv)[NP][STEPS]) {
+__device__ __forceinline__ void load_parts(const uint16_t (&vs)[NP][ROWS][PITCH], int p, Piece<RT> (&vv)[NP][STEPS]) {
+  constexpr int N = sizeof(Piece<RT>) / 2;
   const int g = lane_id() / 16;
 #pragma unroll
   for (int h = 0; h < NP; ++h)
 #pragma unroll
-    for (int q = 0; q < STEPS; ++q) {
-      if constexpr (RT == 1)
-        vv[h][q] = h == 0 ? *(const u32x4*)&vs[g / 2][p][g % 2 * 8]
-                          : (h == 2 && g < 2 ? *(const u32x4*)&vs[NP - 1][p][g * 8] : u32x4{0u, 0u, 0u, 0u});
-      else
-        vv[h][q] = *(const u32x4*)&vs[h][p][32 * q + 8 * g];
-    }
+    for (int q = 0; q < STEPS; ++q) vv[h][q] = *(const Piece<RT>*)&vs[h][p][(4 * q + g) * N];
 }
 
 // Columns n0 .. n0 + 31 of 16 tokens (token l16 of lane group g): D = B v^T,
 // where tile u's row i is column 8 (i / 4) + 4 u + i % 4 of the 32, so a lane
-// ends with eight consecutive columns of one token.  RT = 1: up to 16 ranks,
-// where one matrix instruction takes the first two parts of v side by side.
-// Loads and use are apart, so a wave has the next blocks' loads in flight.
+// ends with eight consecutive columns of one token.  Loads and use are apart, so
+// a wave has the next blocks' loads in flight.
 template <int RT>
 struct BRows {  // this lane's 16-byte pieces of 32 rows of B: RT of them, 32 / RT rows apart
   static constexpr int PR = 2 * RT, STEP = WAVE / PR;  // pieces a row, rows a load
@@ -296,7 +308,8 @@ struct BRows {  // this lane's 16-byte pieces of 32 rows of B: RT of them, 32 / 
 // the loaded rows through LDS, from which every lane takes its own row's pieces
 template <int RT, int STEPS = RT == 1 ? 1 : RT / 2>
 __device__ __forceinline__ void take_rows(const u32x4 (&raw)[RT], const BRows<RT>& rows, int rank, uint8_t* lds,
-                                          u32x4 (&bv)[STEPS][2]) {
+                                          Piece<RT> (&bv)[STEPS][2]) {
+  constexpr int N = sizeof(Piece<RT>) / 2;  // ranks a lane holds
   const int l16 = lane_id() % 16, g = lane_id() / 16;
   wave_order();  // the block before is read
 #pragma unroll
@@ -306,16 +319,16 @@ __device__ __forceinline__ void take_rows(const u32x4 (&raw)[RT], const BRows<RT
   for (int q = 0; q < STEPS; ++q)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      bv[q][u] = *(const u32x4*)(lds + (l16 / 4 * 8 + 4 * u + l16 % 4) * BRows<RT>::BP +
-                                 (RT == 1 ? g % 2 * 16 : 64 * q + 16 * g));
+      bv[q][u] =
+          *(const Piece<RT>*)(lds + (l16 / 4 * 8 + 4 * u + l16 % 4) * BRows<RT>::BP + (4 * q + g) * N * 2);
   if (rows.ragged) {
     // columns past the rank may hold anything (whole pieces of them are zeros)
     asm volatile("");  // a branch: these masks are not worth computing otherwise
 #pragma unroll
     for (int q = 0; q < STEPS; ++q)
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int r = (RT == 1 ? g % 2 * 8 : 32 * q + 8 * g) + 2 * h;
+      for (int h = 0; h < N / 2; ++h) {
+        const int r = (4 * q + g) * N + 2 * h;
         const uint32_t mask = (r < rank ? 0xFFFFu : 0u) | (r + 1 < rank ? 0xFFFF0000u : 0u);
         bv[q][0][h] &= mask;
         bv[q][1][h] &= mask;
@@ -323,19 +336,26 @@ __device__ __forceinline__ void take_rows(const u32x4 (&raw)[RT], const BRows<RT
   }
 }
 
-// v B^T of the block's 32 columns: this lane's eight columns of its token
+// v B^T of the block's 32 columns: this lane's eight columns of its token.  The
+// low parts go first.  With an infinity in B their sum is infinite, or NaN by a
+// low part of 0, whatever v is; brought back to a number, it leaves the result
+// to the first part, which has v's sign and is 0 only where v is.
 template <int ACT, int RT, int NP, int STEPS = RT == 1 ? 1 : RT / 2>
-__device__ __forceinline__ void block_product(const u32x4 (&bv)[STEPS][2], const u32x4 (&vv)[NP][STEPS], int e,
+__device__ __forceinline__ void block_product(const Piece<RT> (&bv)[STEPS][2], const Piece<RT> (&vv)[NP][STEPS], int e,
                                               float (&d)[8]) {
   f32x4 acc[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-  for (int q = 0; q < STEPS; ++q)
+  for (int h = NP - 1; h >= 0; --h) {
 #pragma unroll
-    for (int h = NP - 1; h >= 0; --h) {  // small parts first
-      if (RT == 1 && h == 1) continue;   // beside the first part
+    for (int q = 0; q < STEPS; ++q)
 #pragma unroll
       for (int u = 0; u < 2; ++u) acc[u] = mfma16<ACT>(bv[q][u], vv[h][q], acc[u]);
+    if (h == 1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        acc[j / 4][j % 4] = __builtin_amdgcn_fmed3f(acc[j / 4][j % 4], -__FLT_MAX__, __FLT_MAX__);
     }
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) d[j] = ACT == ACT_F16 ? ldexp_f(acc[j / 4][j % 4], e) : acc[j / 4][j % 4];
 }
@@ -565,7 +585,7 @@ __global__ __launch_bounds__(64 * WAVES<RT>) void lora_kernel(const uint16_t* __
     __syncthreads();
 
     // ---- base + v B^T: this wave's every FW-th block of 32 columns
-    u32x4 vv[NP][STEPS];
+    Piece<RT> vv[NP][STEPS];
     load_parts<RT>(vs, l16, vv);
     const int e = ACT == ACT_F16 ? exps[l16] : 0;
     const int whole = vec ? min(b1, N / 32) : b0;  // blocks of 32 columns that can be moved in 16 bytes
@@ -576,7 +596,7 @@ __global__ __launch_bounds__(64 * WAVES<RT>) void lora_kernel(const uint16_t* __
       for (int h = 0; h < AHEAD; ++h) {
         const int now = b + FW * h;
         if (now < whole) {
-          u32x4 bv[STEPS][2];
+          Piece<RT> bv[STEPS][2];
           take_rows<RT>(braw[h % BAHEAD], rows, rank, sh.b[wave], bv);
           rows.load(braw[h % BAHEAD], now + FW * BAHEAD, b1);
           float d[8];
@@ -590,7 +610,7 @@ __global__ __launch_bounds__(64 * WAVES<RT>) void lora_kernel(const uint16_t* __
     b = b0 + wave + (max(whole - b0 - wave, 0) + FW - 1) / FW * FW;
 #pragma unroll 1
     for (; b < b1; b += FW) {
-      u32x4 bv[STEPS][2];
+      Piece<RT> bv[STEPS][2];
       rows.load(braw[0], b, b1);
       take_rows<RT>(braw[0], rows, rank, sh.b[wave], bv);
       float d[8];
