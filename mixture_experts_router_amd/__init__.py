@@ -518,6 +518,32 @@ def _routing_out(like: torch.Tensor, T: int, k: int, out):
     return idx, w
 
 
+def _no_graph(name: str) -> None:
+    """Refuses inputs that autograd follows: the call has no backward pass, and a
+    result without a graph would drop their gradient silently."""
+    if torch.is_grad_enabled():
+        raise RuntimeError("%s has no backward pass, and an input requires grad: call it under torch.no_grad() or on "
+                           "detached tensors" % name)
+
+
+class _GateFromLogits(torch.autograd.Function):
+    """gate_from_logits for logits that require grad, with gate_backward as its gradient."""
+
+    @staticmethod
+    def forward(ctx, logits, k, opts):
+        r = gate_from_logits(logits, k, **opts)  # grad mode is off in here
+        ctx.mark_non_differentiable(r["idx"])
+        ctx.save_for_backward(logits, r["idx"])
+        ctx.opts = {n: opts[n] for n in ("score", "renorm", "scale")}
+        return r["idx"], r["w"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, grad_w):
+        logits, idx = ctx.saved_tensors
+        return gate_backward(logits, idx, grad_w.contiguous(), **ctx.opts), None, None
+
+
 def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Optional[torch.Tensor] = None,
                      groups: int = 0, group_k: int = 0, group_best: int = 1, renorm: bool = True, scale: float = 1.0,
                      out=None, stream=None):
@@ -526,11 +552,19 @@ def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bi
     float32 is added to the scores for the selection only; groups: only the
     experts of the group_k best of `groups` groups can be chosen, a group being
     worth the sum of its group_best best keys; renorm: the weights of a token
-    sum to `scale` (moe_gate_opts).  out: (idx, w) to write into."""
+    sum to `scale` (moe_gate_opts).  out: (idx, w) to write into.  For logits
+    that require grad (and no `out`) w carries the graph of gate_backward, of
+    first order."""
     if not _here(logits, stream):
         with _elsewhere(logits, stream):
             return gate_from_logits(logits, k, score=score, bias=bias, groups=groups, group_k=group_k,
                                     group_best=group_best, renorm=renorm, scale=scale, out=out)
+    if logits.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise RuntimeError("gate_from_logits: `out` has no graph, and the logits require grad")
+        idx, w = _GateFromLogits.apply(logits, k, dict(score=score, bias=bias, groups=groups, group_k=group_k,
+                                                       group_best=group_best, renorm=renorm, scale=scale))
+        return dict(idx=idx, w=w)
     code = _gate_type(logits)
     logits, T, E, ld = _rows(logits, "logits")
     dev = logits.get_device()
@@ -545,11 +579,14 @@ def gate(x: torch.Tensor, router_w: torch.Tensor, k: int, *, score: str = "softm
          bias: Optional[torch.Tensor] = None, groups: int = 0, group_k: int = 0, group_best: int = 1,
          renorm: bool = True, scale: float = 1.0, want_logits: bool = False, out=None, stream=None):
     """Router projection of x [T, H] and the gate on its fp32 logits (options as
-    in gate_from_logits): dict(idx, w[, logits])."""
+    in gate_from_logits): dict(idx, w[, logits]).  Refuses x and router_w that
+    require grad in grad mode."""
     if not _here(x, stream):
         with _elsewhere(x, stream):
             return gate(x, router_w, k, score=score, bias=bias, groups=groups, group_k=group_k,
                         group_best=group_best, renorm=renorm, scale=scale, want_logits=want_logits, out=out)
+    if x.requires_grad or router_w.requires_grad:
+        _no_graph("gate")
     code = _dtype_code(x)
     if x.dim() != 2 or router_w.dim() != 2:
         raise ValueError("x and router_w must have two dimensions")
@@ -574,7 +611,7 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
     """The gradient [T, E] of the gate's weights with respect to the logits, in
     their type: idx [T, k] int32 as the gate returned it, grad_w [T, k] float32,
     score, renorm and scale as in the forward call (a bias and groups only
-    select: they change nothing here)."""
+    select: they change nothing here).  The result has no graph of its own."""
     if not _here(logits, stream):
         with _elsewhere(logits, stream):
             return gate_backward(logits, idx, grad_w, score=score, renorm=renorm, scale=scale, out=out)
@@ -604,12 +641,15 @@ def layer_forward_gated(x: torch.Tensor, router_w: Optional[torch.Tensor], k: in
                         bias: Optional[torch.Tensor] = None, groups: int = 0, group_k: int = 0, group_best: int = 1,
                         renorm: bool = True, scale: float = 1.0, capacity: int = 0) -> torch.Tensor:
     """layer_forward with the gate's routing (options as in gate_from_logits).
-    logits [T, E] float32, with router_w None: the caller's router logits."""
+    logits [T, E] float32, with router_w None: the caller's router logits.
+    Refuses x, router_w and logits that require grad in grad mode."""
     if not _here(x, stream):
         with _elsewhere(x, stream):
             return layer_forward_gated(x, router_w, k, down, gate_up, gate, up, flags, taps, out, workspace,
                                        logits=logits, score=score, bias=bias, groups=groups, group_k=group_k,
                                        group_best=group_best, renorm=renorm, scale=scale, capacity=capacity)
+    if any(t is not None and t.requires_grad for t in (x, router_w, logits)):
+        _no_graph("layer_forward_gated")
     code = _dtype_code(x)
     T, H = x.shape
     E = down.E
@@ -643,10 +683,13 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
     and b [L, N, R] in x's type; ids [T] int32 in any order, outside [0, L) for a
     token without an adapter; scale [L] float32; ranks [L] int32, the ranks in
     use of adapters smaller than R.  out: written instead of a new tensor; pass
-    base itself to add in place."""
+    base itself to add in place.  Refuses inputs that require grad in grad mode."""
     if not _here(x, stream):
         with _elsewhere(x, stream):
             return lora_add(x, base, ids, a, b, scale=scale, ranks=ranks, out=out)
+    if (x.requires_grad or base.requires_grad or a.requires_grad or b.requires_grad or
+            (scale is not None and scale.requires_grad)):
+        _no_graph("lora_add")
     dtype, odt = x.dtype, base.dtype
     code = _dtype_code(x)
     if odt is not dtype and odt is not torch.float32:
