@@ -112,7 +112,8 @@ struct LoraDev {
   int L, R, K, N;
 };
 hipError_t launch_lora(const void* x, int act, int64_t ldx, int T, const LoraDev& ad, const int32_t* ids,
-                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, hipStream_t st);
+                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, int num_cu,
+                       hipStream_t st);
 
 // ------------------------------------------------------------------ sort
 // k_used_dev may be NULL (then k_static is used); capacity > 0 lists only the

@@ -392,7 +392,7 @@ __device__ __forceinline__ void add_store(const u32x4 (&o)[F32 ? 2 : 1], const f
 // The chunk's work comes in units of one tile and one of 2^cut parts of the
 // columns (the first product is repeated for each part), which its gridDim.y
 // workgroups take in turn.  `cut` grows while the chunk's units fit its share
-// of 256 workgroups side by side, so a few tiles still fill the chip: the
+// of the CUs side by side, so a few tiles still fill the chip: the
 // number of tiles is known only here, from the ids.  Against parts chosen by T
 // alone: 1024 tokens in runs, rank 64, 22.0 against 27.3 us; 300 tokens, rank
 // 16, 12.5 against 17.8; 64 tokens of 48 adapters, rank 32, 13.0 against 14.4; 8
@@ -633,16 +633,17 @@ __global__ __launch_bounds__(64 * WAVES<RT>) void lora_kernel(const uint16_t* __
 }  // namespace
 
 hipError_t launch_lora(const void* x, int act, int64_t ldx, int T, const LoraDev& ad, const int32_t* ids,
-                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, hipStream_t st) {
+                       const void* base, int64_t ldb, void* out, int64_t ldo, bool out_f32, int num_cu,
+                       hipStream_t st) {
   const int per = out_f32 ? 4 : 8;  // elements of 16 bytes
   const int vec = ldb % per == 0 && ldo % per == 0 &&
                   ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
   const int chunks = (int)(((int64_t)T + CHUNK - 1) / CHUNK);
-  // A CU holds one workgroup: a chunk's share of 256 of them (512: 51.7 against
-  // 48.8 us for 4096 tokens, 20.5 against 14.0 for 64 tokens of 48 adapters).
+  // A CU holds one workgroup: a chunk's share of the CUs (twice as many: 51.7
+  // against 48.8 us for 4096 tokens, 20.5 against 14.0 for 64 tokens of 48 adapters).
   // At most eight parts, each of eight blocks of 32 columns or more (one token,
   // rank 16: 8 us in eight parts, 12.7 in one; sixteen: no faster).
-  const int share = std::max(1, 256 / chunks);
+  const int share = std::max(1, num_cu / chunks);
   int most = 0;
   while (most < MOST_CUT && 16 << most <= (ad.N + 31) / 32) ++most;
   const int W = std::min(std::min(T, CHUNK) << most, share);

@@ -887,7 +887,8 @@ moe_status moe_lora_add(const void* x, moe_dtype dt, int64_t ldx, int32_t T, con
     hipStream_t st = (hipStream_t)stream;
     plan_begin(st);
     const moe::LoraDev ad{lora->a, lora->b, lora->scale, lora->ranks, lora->L, lora->R, lora->K, lora->N};
-    HIP_TRY(moe::launch_lora(x, (int)dt, ldx, T, ad, ids, base, ld_base, out, ld_out, out_dt == MOE_F32, st));
+    HIP_TRY(moe::launch_lora(x, (int)dt, ldx, T, ad, ids, base, ld_base, out, ld_out, out_dt == MOE_F32, props.num_cu,
+                             st));
     plan_step("lora", st);
     return MOE_OK;
   } catch (...) {
