@@ -611,7 +611,8 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
     """The gradient [T, E] of the gate's weights with respect to the logits, in
     their type: idx [T, k] int32 as the gate returned it, grad_w [T, k] float32,
     score, renorm and scale as in the forward call (a bias and groups only
-    select: they change nothing here).  The result has no graph of its own."""
+    select: they change nothing here).  The result has no graph of its own; `out`
+    must not overlap the inputs."""
     if not _here(logits, stream):
         with _elsewhere(logits, stream):
             return gate_backward(logits, idx, grad_w, score=score, renorm=renorm, scale=scale, out=out)
@@ -683,7 +684,8 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
     and b [L, N, R] in x's type; ids [T] int32 in any order, outside [0, L) for a
     token without an adapter; scale [L] float32; ranks [L] int32, the ranks in
     use of adapters smaller than R.  out: written instead of a new tensor; pass
-    base itself to add in place.  Refuses inputs that require grad in grad mode."""
+    base itself to add in place (otherwise it must not overlap base, nor ever x).
+    Refuses inputs that require grad in grad mode."""
     if not _here(x, stream):
         with _elsewhere(x, stream):
             return lora_add(x, base, ids, a, b, scale=scale, ranks=ranks, out=out)

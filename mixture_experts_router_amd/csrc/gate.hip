@@ -308,14 +308,15 @@ __device__ __forceinline__ void sort8(double* v) {
 // and the lowest index) and one lane moves to its next, which is in registers
 // already while the one after it is read.
 //
-// Bound by vector instructions: 1000 a wave for 256 experts in groups with a
+// Bound by vector instructions: 850 a wave for 256 experts in groups with a
 // bias (16 exponentials and reciprocals a lane; 110 for the sort; 300 for nine
-// rounds), 27 us of the 30.4 that 65536 tokens take (67 MB of logits: 10 us at
-// the rate of a fill of that size).  A wave a token with 64-bit keys took 158 us.
-//   65536 x 256, sigmoid, bias, 8 groups of two's worth  30.4 us  (2.3 TB/s)
-//   65536 x 256, softmax, nothing else                   19.5 us  (3.6 TB/s)
-//   65536 x 64, sigmoid, bias                            11.0 us
-//   4096 x 64, sigmoid, bias  3.8 us;   64 x 256 in groups  4.7;   1 x 64  2.9
+// rounds), counted as 890 issue slots of four cycles, 24 us at 2.4 GHz of the
+// 30.3 that 65536 tokens take (67 MB of logits: 10 us at the rate of a fill of
+// that size).  A wave a token with 64-bit keys took 158 us.
+//   65536 x 256, sigmoid, bias, 8 groups of two's worth  30.3 us  (2.3 TB/s); bf16, fp16 30.8, 30.2
+//   65536 x 256, softmax, nothing else                   19.3 us  (3.7 TB/s); bf16, fp16 19.3, 19.4
+//   65536 x 64, sigmoid, bias                            11.3 us
+//   4096 x 64, sigmoid, bias  3.8 us;   64 x 256 in groups  4.8;   1 x 64  2.9
 // (an empty kernel: 2.3 us).  A workgroup is one wave: groups of four run
 // 0.4 us slower at 65536 tokens and 0.3 at 64, and 0.3 faster at 16384 x 64.  At
 // least five waves a SIMD: six spill (8192 x 256 in groups 0.3 us slower), eight
@@ -324,10 +325,17 @@ __device__ __forceinline__ void sort8(double* v) {
 // Where scores order the experts, the fp32 keys decide unless two that matter
 // lie within the window of their error: two slots next to each other, the
 // last slot and the best key left out, or the border of the kept groups.  Such
-// a token (some 0.1% of ordinary ones at 256 experts) is selected again by
-// exact_experts, some 3 us of latency for its wave: 1.5 us of 4096 x 256 in
-// groups, and of 65536.
-// Equal logits with equal biases are exact ties and need no second look.
+// a token is selected again by exact_experts, some 3 us of latency for its wave.
+// Of fp32 logits around 0 with ordinary biases that are 0.1% or less at 256
+// experts: 1.5 us of 4096 x 256 in groups, and of 65536.  An exact tie (equal
+// logits, equal biases) between two slots needs no second look, nor does a group
+// masked whole, whose worth is -inf; an exact tie at the last slot does, and so
+// do the many close keys where sigmoids saturate, as the window is absolute.
+// 65536 x 256, sigmoid, top-8:
+//   fp32, 8 groups, bias                               30.3 us, a group masked 28.9
+//   bf16, 8 groups, bias 30.8; bias 0 (many ties at the last slot)      43.6
+//   bf16, no groups, bias 0                                             38.8
+//   fp32, no groups, bias 0, logits around 0: 25.9; around -12: 49.8; around +8: 97.8
 //
 // Error bounds of the fp32 keys (u = 2^-24, products and sums rounded once,
 // v_exp_f32 and v_rcp_f32 within one ulp, 2 u):
@@ -688,7 +696,9 @@ __global__ __launch_bounds__(64, 5) void gate_kernel(const void* __restrict__ lo
 // The selected gradients are scattered into an LDS row that is written out
 // whole, so the kernel is bound by the [T, E] gradient's bytes (65536 x 256
 // fp32, 67 MB: 18 us, 3.7 TB/s written beside the selected logits' lines; 25 us
-// with stores that stay in the caches).  Only the dense form reads every logit.
+// with stores that stay in the caches; bf16 12.7, fp16 11.9).  Only the dense
+// form reads every logit, three times and one a load, and forms each exponential
+// twice: 65536 x 256 in 47 us (fp32; 27 by its bytes), 40 (bf16), 39 (fp16).
 // 1 - s is formed as 1 / (1 + exp(l)).
 template <int LT>
 __global__ __launch_bounds__(256) void gate_backward_kernel(const void* __restrict__ logits, int64_t ld, int T, int E,

@@ -11,24 +11,34 @@
 // Rounding: x A^T has exact products and fp32 sums, which stay in fp32.  For
 // the second product v goes to the matrix cores as two 16-bit parts (hi + lo:
 // 2^-18 relative for bf16, 2^-22 for fp16), three for a bf16 adapter with an
-// fp32 output, so the only rounding that shows is the output's.  fp16 parts are
+// fp32 output.  Of a 16-bit output only its own rounding shows; of an fp32 one
+// the 2^-22 of fp16 adapters is less than the fp32 sums over K and the ranks
+// round, and a third part would take it below 2^-24.  fp16 parts are
 // taken of v * 2^-e_t, the token's largest finite |v| brought to 2^13 .. 2^14,
 // which keeps fp32's range.
 //
 // Time, and what bounds it (K = N = 4096 unless said; a card that copies 1 GB
 // at 5.1 TB/s and launches an empty kernel in 2.3 us):
-//   1 token, rank 16, fp16                    7.8 us   0.3 MB: a chain of dependent
+//   1 token, rank 16, fp16                    7.6 us   0.3 MB: a chain of dependent
 //       loads (ids, A, the sums through LDS, B and base), each 0.5 .. 1 us, and
 //       some thousand instructions a wave in a row
-//   64 tokens of 48 adapters, rank 32, bf16  12.3 us  16.5 MB: the same chain, with
-//       A's and B's rows from HBM in it (1.3 TB/s over the whole call)
-//   777 tokens, N = 64, rank 8, fp32 out     10.3 us   7.6 MB: likewise
+//   64 tokens of 48 adapters, rank 32, bf16  12.5 us  12 MB (34 adapters in use):
+//       the same chain with A's and B's rows in it (1.0 TB/s over the whole call).
+//       They come from the Infinity Cache, which holds the three sets of inputs
+//       taken in turn; over forty sets, which it does not, 14.7
+//   777 tokens, N = 64, rank 8, fp32 out     10.2 us   7.6 MB: likewise
 //   4096 tokens in runs of 6, rank 64, bf16  48.5 us   105 MB, 2.2 TB/s: some 20 us for
 //       each product, which do not overlap (one workgroup a CU).  Neither is
 //       bound by one thing: without the loads of A 38 us, of B 45, of x 46, of
 //       base 45, without the stores 42.5, without base and stores 40.  Eight
 //       waves hide the latencies of loads, LDS and matrix instructions only in
 //       part, and sixteen do not fit the registers of 64 ranks
+//   4096 tokens of 48 adapters in no order, K = N = 1024, rank 16, bf16  36.5 us, 28 MB;
+//       N = 256, fp32 out 52 us (fp16 55), 49 MB; 512 tokens, rank 32, 35 us, 38 MB:
+//       among 64 tokens an adapter has one or two, so a tile is a tenth full, and
+//       A and B of most adapters are read again for each 64 tokens
+//   rank 128, bf16: 1 token 25 us, 64 tokens of 48 adapters 32 .. 47 (77 MB), 4096
+//       tokens in runs 82 (113 MB): eight waves take two rank tiles at a time
 #include <algorithm>
 #include <type_traits>
 
