@@ -554,7 +554,7 @@ def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bi
     worth the sum of its group_best best keys; renorm: the weights of a token
     sum to `scale` (moe_gate_opts).  out: (idx, w) to write into.  For logits
     that require grad (and no `out`) w carries the graph of gate_backward, of
-    first order."""
+    first order; refused while the stream is captured."""
     if not _here(logits, stream):
         with _elsewhere(logits, stream):
             return gate_from_logits(logits, k, score=score, bias=bias, groups=groups, group_k=group_k,
@@ -562,6 +562,10 @@ def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bi
     if logits.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise RuntimeError("gate_from_logits: `out` has no graph, and the logits require grad")
+        if torch.cuda.is_current_stream_capturing():
+            # its backward pass would be captured too, which an eager graph of the same leaves can make an abort
+            raise RuntimeError("gate_from_logits: while a stream is captured, call it under torch.no_grad() with "
+                               "gate_backward for the gradient")
         idx, w = _GateFromLogits.apply(logits, k, dict(score=score, bias=bias, groups=groups, group_k=group_k,
                                                        group_best=group_best, renorm=renorm, scale=scale))
         return dict(idx=idx, w=w)

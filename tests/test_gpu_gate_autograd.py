@@ -59,6 +59,33 @@ def test_modes_without_a_graph():
     assert empty.grad.shape == (0, 32)
 
 
+def test_a_captured_step_calls_the_gradient_itself():
+    """Logits that require grad are refused during capture, before anything is enqueued; the two calls under no_grad
+    are what a captured step records."""
+    leaf = logits_of(3, 50, 64).cuda().requires_grad_()
+    eager = moe.gate_from_logits(leaf, 4, score="sigmoid")  # a graph of the same leaf that stays alive
+    dw, count = torch.randn(50, 4, device="cuda"), torch.zeros(1, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        count += 1
+        with pytest.raises(RuntimeError, match="captured"):
+            moe.gate_from_logits(leaf, 4, score="sigmoid")
+        with torch.no_grad():
+            r = moe.gate_from_logits(leaf, 4, score="sigmoid")
+            grad = moe.gate_backward(leaf, r["idx"], dw, score="sigmoid")
+    for i in range(3):
+        with torch.no_grad():
+            leaf.copy_(logits_of(10 + i, 50, 64))
+        graph.replay()
+        torch.cuda.synchronize()
+        with torch.no_grad():
+            now = moe.gate_from_logits(leaf, 4, score="sigmoid")
+        assert torch.equal(r["idx"], now["idx"]) and torch.equal(r["w"], now["w"])
+        assert torch.equal(grad, moe.gate_backward(leaf, now["idx"], dw, score="sigmoid"))
+    assert int(count) == 3 and eager["w"].requires_grad
+
+
 def test_calls_without_a_backward_pass_refuse():
     c = {n: t.cuda() for n, t in make(3, 12, 64, 32, 3, 8).items()}
     c["scale"] = torch.ones(3, device="cuda")
