@@ -84,9 +84,10 @@ def test_infinities_in_b(R, N, dtype, out):
 
 
 @pytest.mark.parametrize("out", ["same", "f32"])
-def test_the_smallest_of_a_tokens_values_meets_an_infinity(out):
+@pytest.mark.parametrize("R", [16, 32, 128])
+def test_the_smallest_of_a_tokens_values_meets_an_infinity(out, R):
     """v of one rank 2^-45 of another's: fp16 parts, scaled by the largest, round it to 0, yet it is not."""
-    c = make(5, 9, 64, 40, 1, 16, "f16", out)
+    c = make(5, 9, 64, 40, 1, R, "f16", out)
     c["ids"].zero_()
     c["a"].zero_()
     c["x"][:, 0], c["x"][:, 1] = 2.0 ** 14, 2.0 ** -10
