@@ -22,10 +22,10 @@
 //   1 token, rank 16, fp16                    7.6 us   0.3 MB: a chain of dependent
 //       loads (ids, A, the sums through LDS, B and base), each 0.5 .. 1 us, and
 //       some thousand instructions a wave in a row
-//   64 tokens of 48 adapters, rank 32, bf16  12.5 us  12 MB (34 adapters in use):
+//   64 tokens of 48 adapters, rank 32, bf16  12.3 us  12 MB (34 adapters in use):
 //       the same chain with A's and B's rows in it (1.0 TB/s over the whole call).
 //       They come from the Infinity Cache, which holds the three sets of inputs
-//       taken in turn; over forty sets, which it does not, 14.7
+//       taken in turn; over forty sets, which it does not, 14.4
 //   777 tokens, N = 64, rank 8, fp32 out     10.2 us   7.6 MB: likewise
 //   4096 tokens in runs of 6, rank 64, bf16  48.5 us   105 MB, 2.2 TB/s: some 20 us for
 //       each product, which do not overlap (one workgroup a CU).  Neither is
@@ -34,7 +34,7 @@
 //       waves hide the latencies of loads, LDS and matrix instructions only in
 //       part, and sixteen do not fit the registers of 64 ranks
 //   4096 tokens of 48 adapters in no order, K = N = 1024, rank 16, bf16  36.5 us, 28 MB;
-//       N = 256, fp32 out 52 us (fp16 55), 49 MB; 512 tokens, rank 32, 35 us, 38 MB:
+//       N = 256, fp32 out 52 us (fp16 55), 49 MB; 512 tokens, rank 32, 34.7 us, 38 MB:
 //       among 64 tokens an adapter has one or two, so a tile is a tenth full, and
 //       A and B of most adapters are read again for each 64 tokens
 //   rank 128, bf16: 1 token 25 us, 64 tokens of 48 adapters 32 .. 47 (77 MB), 4096
@@ -361,9 +361,12 @@ __device__ __forceinline__ void block_product(const Piece<RT> (&bv)[STEPS][2], c
 #pragma unroll
       for (int u = 0; u < 2; ++u) acc[u] = mfma16<ACT>(bv[q][u], vv[h][q], acc[u]);
     if (h == 1) {
+      // one scalar, with its sign and without: two constants would hold a vector
+      // register too, over the whole kernel (64 tokens of 48 adapters: 12.6 against 12.3 us)
+      float most = __FLT_MAX__;
+      asm("" : "+s"(most));
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        acc[j / 4][j % 4] = __builtin_amdgcn_fmed3f(acc[j / 4][j % 4], -__FLT_MAX__, __FLT_MAX__);
+      for (int j = 0; j < 8; ++j) acc[j / 4][j % 4] = __builtin_amdgcn_fmed3f(acc[j / 4][j % 4], -most, most);
     }
   }
 #pragma unroll
