@@ -82,7 +82,7 @@ typedef enum {
                                 MOE_NOALLOC_SCRATCH_BYTES of workspace */
 } moe_status;
 
-/* MOE_F32: logits of the gate and outputs of moe_lora_add only */
+/* MOE_F32: logits of the gate and of the balance loss, outputs of moe_lora_add and moe_linear only */
 typedef enum { MOE_F16 = 1, MOE_BF16 = 2, MOE_F32 = 3 } moe_dtype;
 
 /* k argument value selecting the entropy-adaptive top-1/2/3 routing */
@@ -502,6 +502,139 @@ typedef struct {
 moe_status moe_lora_add(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const moe_lora* lora, const int32_t* ids,
                         const void* base, int64_t ld_base, void* out, int64_t ld_out, moe_dtype out_dt,
                         void* stream);
+
+/*
+ * Balance loss of a routing and the experts' counts, per sequence of tokens:
+ *
+ *   p_te      = softmax(l_t)_e over the E experts (MOE_SCORE_SOFTMAX), or
+ *               s_te / (sum_j s_tj + 1e-20), s = 1 / (1 + exp(-l)) (MOE_SCORE_SIGMOID)
+ *   over the n live tokens t of sequence s:
+ *   counts[s, e] = number of (t, slot) with topk_idx[t, slot] == e
+ *   prob[s, e]   = sum_t p_te / n
+ *   loss[s]      = E / (k n) * sum_e counts[s, e] * prob[s, e]
+ *   z[s]         = sum_t (log sum_e exp l_te)^2 / n      (MOE_SCORE_SOFTMAX only)
+ *
+ * (1 where tokens or probabilities are spread evenly.)  A sequence without a
+ * live token has all of them 0.  A logit of -inf masks an expert: its
+ * probability is 0, also in a row that masks every expert, which counts as a
+ * token and adds nothing to prob and z.  NaN and +inf make p NaN as the formula
+ * does.  Indices outside [0, E) are not counted.
+ *
+ *   score    moe_score
+ *   seqs     sequences S >= 1
+ *   offsets  int32 [S + 1] on the device: sequence s is the tokens offsets[s] ..
+ *            offsets[s + 1] - 1, 0 <= offsets[0] <= ... <= offsets[S] <= T; tokens
+ *            outside belong to none.  NULL (S = 1): all tokens.  Offsets out of
+ *            order give unspecified values, within the caller's buffers
+ *   mask     uint8 [T] on the device: tokens of 0 are not live (padding), and
+ *            nothing of theirs is looked at.  NULL: all are
+ * NULL moe_balance_opts: softmax, one sequence, no mask.
+ * MOE_ERR_OPTION: a score or number of sequences out of range.
+ */
+#define MOE_BALANCE_MAX_SEQS (1 << 20)
+typedef struct {
+  int32_t score;
+  int32_t seqs;
+  const int32_t* offsets;
+  const uint8_t* mask;
+} moe_balance_opts;
+
+/*
+ *   logits    [T, E] of type lt, rows ld >= E elements apart
+ *   topk_idx  int32 [T, k]
+ *   loss fp32 [S], z fp32 [S] (or NULL; MOE_ERR_OPTION with sigmoid scores), prob
+ *   fp32 [S, E] (or NULL), counts int32 [S, E], tokens int32 [S] (the n): out
+ *   ws        moe_balance_workspace_size(T, E, S) bytes, 16-byte aligned
+ * T == 0 writes zeros (with offsets: they are read).
+ */
+size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S);
+moe_status moe_balance_loss(const void* logits, moe_dtype lt, int64_t ld, int32_t T, int32_t E, int32_t k,
+                            const int32_t* topk_idx, const moe_balance_opts* opts, float* loss, float* z, float* prob,
+                            int32_t* counts, int32_t* tokens, void* ws, size_t ws_bytes, void* stream);
+/*
+ * grad_logits[t, e] = d (sum_s grad_loss[s] loss[s] + grad_z[s] z[s]) / d logits[t, e]
+ * at fixed counts and tokens (as moe_balance_loss wrote them), [T, E] in the
+ * logits' type, rows ld_grad >= E elements apart, every element written: 0 for
+ * tokens that are not live or in no sequence, and where p is 0.  Must not
+ * overlap the inputs.  grad_loss or grad_z fp32 [S] may be NULL (0); grad_z
+ * needs softmax scores.
+ */
+moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, int64_t ld, int32_t T, int32_t E, int32_t k,
+                                     const moe_balance_opts* opts, const int32_t* counts, const int32_t* tokens,
+                                     const float* grad_loss, const float* grad_z, void* grad_logits, int64_t ld_grad,
+                                     void* stream);
+
+/*
+ * A dense product with its epilogue, for what every token takes beside the
+ * routed experts: a shared expert's projections, the router with a bias, any
+ * projection next to the layer.
+ *
+ *   z   = x W^T + bias                       [T, N]
+ *   out = residual + row_scale * act(z)      [T, C]
+ *
+ *   act: none; relu(z) = max(z, 0); silu(z) = z / (1 + exp(-z)); gelu(z) = z (1 +
+ *   erf(z / sqrt 2)) / 2; sigmoid(z); swiglu: silu(z[:, :C]) * z[:, C:]
+ *   C = N, with swiglu C = N / 2 (N even)
+ *   w     [N, K] in x's type, rows ldw >= K elements apart
+ *   bias  [N] of type bias_dt (x's or MOE_F32), or NULL
+ * Sums, the activation and the epilogue are fp32; one rounding gives out.
+ *   K % 8 == 0; ldw % 8 == 0; w 16-byte aligned; K and N at least 1, all of K, N
+ *   and the row distances at most MOE_LINEAR_MAX_COLUMNS
+ */
+#define MOE_LINEAR_MAX_COLUMNS (1 << 22)
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_SIGMOID = 4,
+  MOE_ACT_SWIGLU = 5
+} moe_act;
+typedef struct {
+  const void* w;
+  int64_t ldw;
+  const void* bias;
+  int32_t bias_dt;
+  int32_t N;
+  int32_t K;
+  int32_t act;
+} moe_dense;
+
+/*
+ *   x          [T, K] of type dt (MOE_F16 / MOE_BF16), rows ldx apart, ldx % 8 == 0,
+ *              16-byte aligned; 0 <= T <= MOE_GATE_MAX_TOKENS
+ *   residual   [T, C] of out's type, rows ld_residual apart, or NULL.  It may be
+ *              out itself (with the same row distance); otherwise out overlaps
+ *              no input
+ *   row_scale  fp32 [T], or NULL (1)
+ *   preact     [T, N] of type dt out: z rounded once, for the gradient; or NULL
+ *   out        [T, C] of type out_dt (dt or MOE_F32), rows ld_out apart
+ *   ws         moe_linear_workspace_size(T, N, K) bytes (may be 0), 16-byte aligned
+ */
+size_t moe_linear_workspace_size(int32_t T, int32_t N, int32_t K);
+moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const moe_dense* dense,
+                      const void* residual, int64_t ld_residual, const float* row_scale, void* preact,
+                      int64_t ld_preact, void* out, int64_t ld_out, moe_dtype out_dt, void* ws, size_t ws_bytes,
+                      void* stream);
+/*
+ * Its gradients, from g = d loss / d out [T, C] of type grad_dt (dt or MOE_F32):
+ *
+ *   dz = row_scale * g * act'(preact), rounded to dt where it enters the products
+ *   grad_x [T, K] = dz W,  grad_w [N, K] = dz^T x      in dt
+ *   grad_bias [N] = sum_t dz,  grad_row_scale [T] = sum_c g act(preact)    fp32
+ * (the residual's gradient is g).  Each output may be NULL.  preact [T, N] as
+ * moe_linear kept it; it may be NULL with act none where grad_row_scale is NULL.
+ * dense->bias is not read; w is read for grad_x only and may be NULL without,
+ * and so x for grad_w.  Outputs overlap nothing.  T == 0 writes zeros to grad_w
+ * and grad_bias.
+ *   ws  moe_linear_backward_workspace_size(T, N, K) bytes, 16-byte aligned
+ */
+size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t K);
+moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_grad, const void* x, moe_dtype dt,
+                               int64_t ldx, int32_t T, const moe_dense* dense, const void* preact, int64_t ld_preact,
+                               const float* row_scale, void* grad_x, int64_t ld_grad_x, void* grad_w,
+                               int64_t ld_grad_w, float* grad_bias, float* grad_row_scale, void* ws, size_t ws_bytes,
+                               void* stream);
 
 /*
  * Health figures of per-expert activation counts (page "Qwen3.5-MoE与Qwen3-MoE

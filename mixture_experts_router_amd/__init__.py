@@ -6,7 +6,8 @@ mirror the C ABI in include/moe.h:
 
     route, topk_from_logits, layer_forward, fuse_gate_up,
     layer_workspace_size, route_workspace_size,
-    gate, gate_from_logits, gate_backward, layer_forward_gated, lora_add
+    gate, gate_from_logits, gate_backward, layer_forward_gated, lora_add,
+    balance_loss, balance_loss_backward, linear, linear_backward
 
 If the library is not built this module raises on first use; there is no
 fallback implementation.
@@ -38,7 +39,8 @@ EXPORTS = ("moe_route_workspace_size", "moe_route", "moe_route_ex", "moe_topk_fr
            "moe_topk_from_logits_ex", "moe_layer_workspace_size", "moe_layer_forward", "moe_layer_forward_ex",
            "moe_layer_forward_noalloc", "moe_layer_forward_gated",
            "moe_gate_workspace_size", "moe_gate", "moe_gate_from_logits", "moe_gate_backward",
-           "moe_lora_add",
+           "moe_lora_add", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
+           "moe_linear_workspace_size", "moe_linear", "moe_linear_backward_workspace_size", "moe_linear_backward",
            "moe_expert_load_stats", "moe_fuse_gate_up", "moe_packed_sb_bytes", "moe_pack_sb", "moe_packed_q_bytes", "moe_pack_q", "moe_status_string",
            "moe_debug_set_events",
            "moe_debug_last_plan", "moe_debug_set_tuning", "moe_debug_stream_read")
@@ -76,6 +78,16 @@ class CLora(ctypes.Structure):
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("ranks", ctypes.c_void_p), ("L", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int32),
                 ("N", ctypes.c_int32)]
+
+
+class CBalanceOpts(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("seqs", ctypes.c_int32), ("offsets", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p)]
+
+
+class CDense(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("bias", ctypes.c_void_p),
+                ("bias_dt", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 class CTaps(ctypes.Structure):
@@ -132,6 +144,22 @@ def lib() -> ctypes.CDLL:
     L.moe_layer_forward_gated.restype = i32
     L.moe_lora_add.argtypes = [vp, i32, i64, i32, ctypes.POINTER(CLora), vp, vp, i64, vp, i64, i32, vp]
     L.moe_lora_add.restype = i32
+    bopt, dense = ctypes.POINTER(CBalanceOpts), ctypes.POINTER(CDense)
+    L.moe_balance_workspace_size.argtypes = [i32, i32, i32]
+    L.moe_balance_workspace_size.restype = sz
+    L.moe_balance_loss.argtypes = [vp, i32, i64, i32, i32, i32, vp, bopt, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_balance_loss.restype = i32
+    L.moe_balance_loss_backward.argtypes = [vp, i32, i64, i32, i32, i32, bopt, vp, vp, vp, vp, vp, i64, vp]
+    L.moe_balance_loss_backward.restype = i32
+    L.moe_linear_workspace_size.argtypes = [i32, i32, i32]
+    L.moe_linear_workspace_size.restype = sz
+    L.moe_linear.argtypes = [vp, i32, i64, i32, dense, vp, i64, vp, vp, i64, vp, i64, i32, vp, sz, vp]
+    L.moe_linear.restype = i32
+    L.moe_linear_backward_workspace_size.argtypes = [i32, i32, i32]
+    L.moe_linear_backward_workspace_size.restype = sz
+    L.moe_linear_backward.argtypes = [vp, i32, i64, vp, i32, i64, i32, dense, vp, i64, vp, vp, i64, vp, i64, vp, vp,
+                                      vp, sz, vp]
+    L.moe_linear_backward.restype = i32
     L.moe_expert_load_stats.argtypes = [vp, i32, vp, vp, vp]
     L.moe_expert_load_stats.restype = i32
     L.moe_layer_workspace_size.argtypes = [i32, i32, i32, i32, i32, u32]
@@ -725,6 +753,297 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
     _check(lib().moe_lora_add(x.data_ptr(), code, ldx, T, lora, pids, base.data_ptr(), ldb, out.data_ptr(), ldo,
                               _TYPES[odt], _current(dev)), "moe_lora_add")
     return out
+
+
+# ------------------------------------------ balance loss and dense products --
+
+
+def _capture_refused(name: str, instead: str) -> None:
+    """Refuses to record a graph of autograd while a stream is captured: its backward pass would be captured too,
+    which an eager graph of the same leaves can make an abort."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("%s: while a stream is captured, call it under torch.no_grad() with %s for the gradient" %
+                           (name, instead))
+
+
+def _balance_opts(dev: int, T: int, score: str, offsets, mask):
+    """(moe_balance_opts, S) of a call on T tokens."""
+    kind = SCORES.get(score)
+    if kind is None:
+        raise ValueError("score must be one of %s, got %r" % (sorted(SCORES), score))
+    S = 1
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError("offsets must have one dimension of at least two, got shape %s" % (tuple(offsets.shape),))
+        S = offsets.numel() - 1
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("mask must be bool or uint8, got %s" % mask.dtype)
+    return CBalanceOpts(kind, S, _operand(offsets, "offsets", dev, torch.int32, (S + 1,)),
+                        None if mask is None else _operand(mask, "mask", dev, mask.dtype, (T,))), S
+
+
+class _BalanceLoss(torch.autograd.Function):
+    """balance_loss for logits that require grad, with balance_loss_backward as its gradient."""
+
+    @staticmethod
+    def forward(ctx, logits, idx, opts):
+        r = balance_loss(logits, idx, **opts)  # grad mode is off in here
+        ctx.save_for_backward(logits, r["counts"], r["tokens"], opts["offsets"], opts["mask"])
+        ctx.k, ctx.score = idx.shape[1], opts["score"]
+        z = r.get("z")
+        if z is None:
+            z = r["loss"].new_empty(0)
+            ctx.mark_non_differentiable(z)
+        ctx.mark_non_differentiable(r["prob"], r["counts"], r["tokens"])
+        return r["loss"], z, r["prob"], r["counts"], r["tokens"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_loss, grad_z, *_):
+        logits, counts, tokens, offsets, mask = ctx.saved_tensors
+        grad_z = grad_z.contiguous() if ctx.score == "softmax" else None
+        return balance_loss_backward(logits, counts, tokens, grad_loss.contiguous(), ctx.k, grad_z=grad_z,
+                                     score=ctx.score, offsets=offsets, mask=mask), None, None
+
+
+def balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, score: str = "softmax",
+                 offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None, stream=None):
+    """Balance loss and expert counts of a routing, per sequence (moe_balance_loss):
+    logits [T, E] (float32, float16 or bfloat16), idx [T, k] int32 as the gate
+    returned it.  dict(loss [S] = E / (k n) sum_e counts_e prob_e, prob [S, E] the
+    mean probabilities, counts [S, E] int32, tokens [S] int32 the live tokens n and,
+    with softmax scores, z [S] the mean squared logsumexp), all float32 but the
+    whole numbers.  offsets [S + 1] int32: sequence s is the tokens offsets[s] up to
+    offsets[s + 1] (None: one sequence); mask [T] bool or uint8: the live tokens.
+    For logits that require grad loss and z carry the graph of
+    balance_loss_backward, of first order; refused while the stream is captured."""
+    if not _here(logits, stream):
+        with _elsewhere(logits, stream):
+            return balance_loss(logits, idx, score=score, offsets=offsets, mask=mask)
+    if logits.requires_grad and torch.is_grad_enabled():
+        _capture_refused("balance_loss", "balance_loss_backward")
+        loss, z, prob, counts, tokens = _BalanceLoss.apply(logits, idx, dict(score=score, offsets=offsets, mask=mask))
+        r = dict(loss=loss, prob=prob, counts=counts, tokens=tokens)
+        if score == "softmax":
+            r["z"] = z
+        return r
+    code = _gate_type(logits)
+    logits, T, E, ld = _rows(logits, "logits")
+    if idx.dim() != 2:
+        raise ValueError("idx must have two dimensions")
+    k = idx.shape[1]
+    dev = logits.get_device()
+    pi = _operand(idx, "idx", dev, torch.int32, (T, k))
+    o, S = _balance_opts(dev, T, score, offsets, mask)
+    loss = logits.new_empty(S, dtype=torch.float32)
+    z = logits.new_empty(S, dtype=torch.float32) if score == "softmax" else None
+    prob = _new(logits, S, E, torch.float32)
+    counts = _new(logits, S, E, torch.int32)
+    tokens = logits.new_empty(S, dtype=torch.int32)
+    need = lib().moe_balance_workspace_size(T, E, S)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=logits.device)
+    _check(lib().moe_balance_loss(logits.data_ptr(), code, ld, T, E, k, pi, o, loss.data_ptr(),
+                                  None if z is None else z.data_ptr(), prob.data_ptr(), counts.data_ptr(),
+                                  tokens.data_ptr(), ws.data_ptr(), ws.numel(), _current(dev)), "moe_balance_loss")
+    r = dict(loss=loss, prob=prob, counts=counts, tokens=tokens)
+    if z is not None:
+        r["z"] = z
+    return r
+
+
+def balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor,
+                          grad_loss: Optional[torch.Tensor], k: int, *, grad_z: Optional[torch.Tensor] = None,
+                          score: str = "softmax", offsets: Optional[torch.Tensor] = None,
+                          mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """The gradient [T, E] of balance_loss's losses with respect to the logits, in
+    their type: counts [S, E] and tokens [S] as balance_loss returned them,
+    grad_loss [S] and grad_z [S] (softmax scores) float32 or None, k the routed
+    experts of a token, score, offsets and mask as in the forward call.  Tokens
+    that are not live have gradient 0.  The result has no graph of its own; `out`
+    must not overlap the inputs."""
+    if not _here(logits, stream):
+        with _elsewhere(logits, stream):
+            return balance_loss_backward(logits, counts, tokens, grad_loss, k, grad_z=grad_z, score=score,
+                                         offsets=offsets, mask=mask, out=out)
+    code = _gate_type(logits)
+    logits, T, E, ld = _rows(logits, "logits")
+    dev = logits.get_device()
+    o, S = _balance_opts(dev, T, score, offsets, mask)
+    pc = _operand(counts, "counts", dev, torch.int32, (S, E))
+    pt = _operand(tokens, "tokens", dev, torch.int32, (S,))
+    pg = _operand(grad_loss, "grad_loss", dev, torch.float32, (S,))
+    pz = _operand(grad_z, "grad_z", dev, torch.float32, (S,))
+    if out is None:
+        g, ldg = _new(logits, T, E, logits.dtype), E
+    else:
+        g, ldg = out, _out_rows(out, "out", dev, logits.dtype, (T, E))
+    _check(lib().moe_balance_loss_backward(logits.data_ptr(), code, ld, T, E, k, o, pc, pt, pg, pz, g.data_ptr(), ldg,
+                                           _current(dev)), "moe_balance_loss_backward")
+    return g
+
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4, "swiglu": 5}
+
+
+def _act_code(act: str) -> int:
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError("act must be one of %s, got %r" % (sorted(ACTS), act))
+    return code
+
+
+def _operand_rows(t: torch.Tensor, name: str):
+    """_rows for an operand of the matrix cores: rows 16-byte aligned, or a copy."""
+    t, n, columns, ld = _rows(t, name)
+    if ld % 8 or t.data_ptr() % 16:
+        t, ld = t.clone(memory_format=torch.contiguous_format), columns
+    return t, n, columns, ld
+
+
+def _beside(t: torch.Tensor, name: str, dev: int, dtype, shape):
+    """(t, elements between rows) of an input matrix of that type and shape."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape or t.get_device() != dev:
+        raise ValueError("%s must have shape %s on GPU %d, got %s on %s" %
+                         (name, tuple(shape), dev, tuple(t.shape), t.device))
+    t, _, _, ld = _rows(t, name)
+    return t, ld
+
+
+class _Linear(torch.autograd.Function):
+    """linear for inputs that require grad, with linear_backward as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, row_scale, act, out_dtype):
+        keep = act != "none" or (row_scale is not None and row_scale.requires_grad)
+        r = linear(x, w, bias, act=act, residual=residual, row_scale=row_scale, out_dtype=out_dtype, want_preact=keep)
+        out, z = r if keep else (r, None)
+        ctx.save_for_backward(x, w, row_scale, z)
+        ctx.act, ctx.bias_type = act, None if bias is None else bias.dtype
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        x, w, row_scale, z = ctx.saved_tensors
+        need = dict(zip(("x", "w", "bias", "residual", "row_scale"), ctx.needs_input_grad))
+        want = [n for n in ("x", "w", "bias", "row_scale") if need[n]]
+        r = linear_backward(grad, x, w, act=ctx.act, preact=z, row_scale=row_scale, want=want) if want else {}
+        db = r.get("bias")
+        return (r.get("x"), r.get("w"), None if db is None else db.to(ctx.bias_type), grad if need["residual"] else None,
+                r.get("row_scale"), None, None)
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *, act: str = "none",
+           residual: Optional[torch.Tensor] = None, row_scale: Optional[torch.Tensor] = None, out_dtype=None,
+           want_preact: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """residual + row_scale * act(x w^T + bias) (moe_linear): x [T, K] and w [N, K]
+    float16 or bfloat16, bias [N] of their type or float32, act "none", "relu",
+    "silu", "gelu", "sigmoid" or "swiglu" (the first N / 2 columns gate the others),
+    row_scale [T] float32.  The result [T, N] (swiglu: [T, N / 2]) and residual
+    have x's type or, with out_dtype, float32.  K a multiple of 8.  want_preact:
+    (result, x w^T + bias in x's type), the latter for linear_backward.  out:
+    written instead of a new tensor; the residual itself adds in place.  For
+    inputs that require grad (and no `out` or want_preact) the result carries the
+    graph of linear_backward, of first order; refused while the stream is
+    captured."""
+    if not _here(x, stream):
+        with _elsewhere(x, stream):
+            return linear(x, w, bias, act=act, residual=residual, row_scale=row_scale, out_dtype=out_dtype,
+                          want_preact=want_preact, out=out)
+    code, dtype = _dtype_code(x), x.dtype
+    odt = dtype if out_dtype is None else out_dtype
+    if odt is not dtype and odt is not torch.float32:
+        raise TypeError("out_dtype must be %s or float32, got %s" % (dtype, odt))
+    kind = _act_code(act)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w, bias, residual, row_scale)):
+        if out is not None or want_preact:
+            raise RuntimeError("linear: `out` and the kept product have no graph, and an input requires grad")
+        _capture_refused("linear", "linear_backward")
+        return _Linear.apply(x, w, bias, residual, row_scale, act, odt)
+    x, T, K, ldx = _operand_rows(x, "x")
+    dev = x.get_device()
+    if w.dtype is not dtype:
+        raise TypeError("w must be %s, got %s" % (dtype, w.dtype))
+    if w.dim() != 2 or w.shape[1] != K or w.get_device() != dev:
+        raise ValueError("w must have shape (N, %d) on GPU %d, got %s on %s" % (K, dev, tuple(w.shape), w.device))
+    w, N, _, ldw = _operand_rows(w, "w")
+    C = N // 2 if act == "swiglu" else N
+    pb, bcode = None, code
+    if bias is not None:
+        bcode = _TYPES.get(bias.dtype)
+        if bcode != MOE_F32:
+            bcode = code
+        pb = _operand(bias, "bias", dev, torch.float32 if bcode == MOE_F32 else dtype, (N,))
+    ps = _operand(row_scale, "row_scale", dev, torch.float32, (T,))
+    pr, ldr = None, C
+    if residual is not None:
+        if residual is out:
+            ldr = _out_rows(out, "out", dev, odt, (T, C))
+        else:
+            residual, ldr = _beside(residual, "residual", dev, odt, (T, C))
+        pr = residual.data_ptr()
+    if out is None:
+        out, ldo = _new(x, T, C, odt), C
+    else:
+        ldo = _out_rows(out, "out", dev, odt, (T, C))
+    z = _new(x, T, N, dtype) if want_preact else None
+    need = lib().moe_linear_workspace_size(T, N, K)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _check(lib().moe_linear(x.data_ptr(), code, ldx, T, CDense(w.data_ptr(), ldw, pb, bcode, N, K, kind), pr, ldr, ps,
+                            None if z is None else z.data_ptr(), N, out.data_ptr(), ldo, _TYPES[odt],
+                            None if ws is None else ws.data_ptr(), need, _current(dev)), "moe_linear")
+    return (out, z) if want_preact else out
+
+
+def linear_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, act: str = "none",
+                    preact: Optional[torch.Tensor] = None, row_scale: Optional[torch.Tensor] = None,
+                    want: Sequence[str] = ("x", "w"), stream=None) -> dict:
+    """The gradients of linear that `want` names, from that of its result: dict of x
+    [T, K] and w [N, K] in x's type, bias [N] and row_scale [T] float32.  grad in
+    x's type or float32, preact as linear kept it (act "none" without the
+    gradient of row_scale needs none), act and row_scale as in the forward call.
+    The residual's gradient is grad itself.  The results have no graph."""
+    if not _here(x, stream):
+        with _elsewhere(x, stream):
+            return linear_backward(grad, x, w, act=act, preact=preact, row_scale=row_scale, want=want)
+    unknown = [n for n in want if n not in ("x", "w", "bias", "row_scale")]
+    if unknown:
+        raise ValueError('want names "x", "w", "bias" and "row_scale", got %r' % (unknown,))
+    code, dtype = _dtype_code(x), x.dtype
+    kind = _act_code(act)
+    x, T, K, ldx = _operand_rows(x, "x")
+    dev = x.get_device()
+    if w.dtype is not dtype:
+        raise TypeError("w must be %s, got %s" % (dtype, w.dtype))
+    if w.dim() != 2 or w.shape[1] != K or w.get_device() != dev:
+        raise ValueError("w must have shape (N, %d) on GPU %d, got %s on %s" % (K, dev, tuple(w.shape), w.device))
+    w, N, _, ldw = _operand_rows(w, "w")
+    C = N // 2 if act == "swiglu" else N
+    gcode = MOE_F32 if grad.dtype is torch.float32 else code
+    grad, ldg = _beside(grad, "grad", dev, torch.float32 if gcode == MOE_F32 else dtype, (T, C))
+    pz, ldz = None, N
+    if preact is not None:
+        preact, ldz = _beside(preact, "preact", dev, dtype, (T, N))
+        pz = preact.data_ptr()
+    elif act != "none" or "row_scale" in want:
+        raise ValueError("preact is needed: act is %r%s" % (act, ", the gradient of row_scale is wanted"
+                                                            if "row_scale" in want else ""))
+    ps = _operand(row_scale, "row_scale", dev, torch.float32, (T,))
+    r = {}
+    for n in want:
+        r[n] = (_new(x, T, K, dtype) if n == "x" else _new(x, N, K, dtype) if n == "w" else
+                torch.empty(N if n == "bias" else T, dtype=torch.float32, device=x.device))
+    at = lambda n: r[n].data_ptr() if n in r else None  # noqa: E731
+    need = lib().moe_linear_backward_workspace_size(T, N, K)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    _check(lib().moe_linear_backward(grad.data_ptr(), gcode, ldg, x.data_ptr(), code, ldx, T,
+                                     CDense(w.data_ptr(), ldw, None, code, N, K, kind), pz, ldz, ps, at("x"), K,
+                                     at("w"), K, at("bias"), at("row_scale"), ws.data_ptr(), ws.numel(),
+                                     _current(dev)), "moe_linear_backward")
+    return r
 
 
 def expert_load_stats(counts: torch.Tensor, stream=None):

@@ -186,6 +186,62 @@ hipError_t launch_gemm(GemmMode mode, const uint16_t* a, int64_t a_rows, const i
                        void* out, bool perm8_out, int bm, int max_mtiles, hipStream_t st, float* pre = nullptr,
                        const int32_t* tokexp = nullptr, const int32_t* any_scaled = nullptr);
 
+// ------------------------------------------------- dense products (linear.hip)
+// activations (same values as moe_act)
+enum { LIN_NONE = 0, LIN_RELU = 1, LIN_SILU = 2, LIN_GELU = 3, LIN_SIGMOID = 4, LIN_SWIGLU = 5 };
+
+// What becomes of the sums z [M, N]: out[t, :C] = res + row_scale[t] * act(z + bias), C = N, or N / 2 for LIN_SWIGLU
+struct LinearEpi {
+  const void* bias;  // [N] or NULL
+  const void* res;   // [M, C] of out's type, rows ldr apart, or NULL
+  const float* row_scale;
+  void* out;
+  void* pre;  // z as the operands' type [M, N], rows ldp apart, or NULL
+  int64_t ldr, ldo, ldp;
+  int C, act;
+  bool bias_f32, out_f32;
+  bool vec;  // every row of res, out and pre starts 16-byte aligned (gated: the up half of pre too)
+};
+
+// dz = row_scale g act'(z), and the sums of bias and row_scale
+struct LinearGrad {
+  const void* g;  // [T, C], rows ldg apart
+  const void* z;  // [T, N] in the operands' type, rows ldz_in apart; NULL: act is LIN_NONE
+  const float* rs;
+  uint16_t* dz;  // [T, ldz] out, or NULL
+  float* drs;    // [T] out, or NULL
+  float* part;   // column sums of the blocks [blocks, N], or NULL
+  int64_t ldg, ldz_in, ldz, T;
+  int C, N, act, rows, blocks;  // rows of a block: at most LINEAR_DZ_ROWS
+  bool g_f32, vec;
+};
+constexpr int LINEAR_DZ_ROWS = 64;
+
+// bytes of the partial sums of a product [M, N] over K (0: none)
+int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_linear(const void* x, int dt, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K,
+                         const LinearEpi& e, float* part, hipStream_t st);
+// dz: g.dz, or the gradient itself where that is dz (rows ldz apart, ldz % 8 == 0, N values and zeros up to the next
+// multiple of 8).  dx [T, K], dw [N, K], dbias [N] (with g.part) may be NULL
+hipError_t launch_linear_backward(const LinearGrad& g, int dt, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                  int K, void* dx, int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias,
+                                  const uint16_t* dz, int64_t ldz, float* part, hipStream_t st);
+
+// --------------------------------------------------- balance loss (balance.hip)
+struct BalanceDev {
+  int score;  // GATE_SOFTMAX / GATE_SIGMOID
+  int S;      // sequences
+  const int32_t* offsets;  // [S + 1], or NULL: one sequence of all tokens
+  const uint8_t* mask;     // [T], or NULL
+};
+int64_t balance_ws_bytes(int T, int E, int S);
+hipError_t launch_balance(const void* logits, int lt, int64_t ld, int T, int E, int k, const int32_t* idx,
+                          const BalanceDev& b, float* loss, float* z, float* prob, int32_t* counts, int32_t* tokens,
+                          void* ws, hipStream_t st);
+hipError_t launch_balance_backward(const void* logits, int lt, int64_t ld, int T, int E, int k, const BalanceDev& b,
+                                   const int32_t* counts, const int32_t* tokens, const float* grad_loss,
+                                   const float* grad_z, void* out, int64_t ldo, hipStream_t st);
+
 // --------------------------------------------------------- small kernels
 // h[i, j] = fp16(2^-2a swiglu(g[i, j], u[i, j])) for i < rows, a the
 // exponent of row i's token: tokexp[pair / kcap], pair = perm ? perm[i] : i

@@ -1,0 +1,712 @@
+// Dense products with a fused epilogue, and their gradients (gfx950):
+//
+//   z = x W^T + bias,   out = residual + row_scale * act(z)
+//   dz = row_scale * g * act'(z),  dx = dz W,  dW = dz^T x,  dbias = sum dz,  drow_scale = sum g act(z)
+//
+// All three products are C[m, n] = sum_k A(m, k) B(n, k) with fp16 or bf16
+// operands and fp32 sums; what differs is which index is contiguous in memory.
+#include "common.hpp"
+#include "kernels.hpp"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+typedef __bf16 bf16;
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int NUM_XCD = 8;  // workgroups go round-robin over 8 XCDs, each with its own L2
+constexpr uint32_t OUT_OF_RANGE = 0x80000000u;  // a byte offset past every descriptor: the load gives zeros
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(s16x8 a, s16x8 b, f32x16 c) {
+  if constexpr (DT == ACT_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (DT == ACT_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+
+__device__ __forceinline__ void dma16(rsrc_t r, uint32_t voff, uint32_t soff, uint8_t* lds_dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds_dst, 16, voff, soff, 0, 0);
+}
+
+// wait until at most N vector memory instructions of this wave are pending
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N <= 63, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+template <int V>
+struct IC {
+  static constexpr int value = V;
+};
+
+// f(IC<S>), f(IC<S + 1>), ... f(IC<N - 1>) while f returns true
+template <int S, int N, typename F>
+__device__ __forceinline__ void for_each(F&& f) {
+  if constexpr (S < N) {
+    if (f(IC<S>{})) for_each<S + 1, N>(f);
+  }
+}
+
+// ------------------------------------------------------------ activations --
+//
+// Exponentials are expf's (not the shorter hardware form): outputs may be fp32.
+
+__device__ __forceinline__ float sigmoid_(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+__device__ __forceinline__ float activate(int act, float z) {
+  switch (act) {
+    case LIN_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case LIN_SILU: return z * sigmoid_(z);
+    case LIN_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);  // (1 + erf(v)) = erfc(-v), without cancellation
+    case LIN_SIGMOID: return sigmoid_(z);
+    default: return z;
+  }
+}
+
+// act(z) and its slope
+__device__ __forceinline__ float activate_slope(int act, float z, float& slope) {
+  switch (act) {
+    case LIN_RELU:
+      slope = z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+      return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case LIN_SILU: {
+      const float s = sigmoid_(z);
+      slope = s * (1.0f + z * sigmoid_(-z));
+      return z * s;
+    }
+    case LIN_GELU: {
+      const float c = 0.5f * erfcf(-0.70710678118654752f * z);
+      slope = c + z * (0.39894228040143268f * expf(-0.5f * z * z));
+      return z * c;
+    }
+    case LIN_SIGMOID: {
+      const float s = sigmoid_(z);
+      slope = s * sigmoid_(-z);
+      return s;
+    }
+    default:
+      slope = 1.0f;
+      return z;
+  }
+}
+
+// ------------------------------------------------------------------ rows --
+
+template <int DT>
+__device__ __forceinline__ float half_to_f32(uint32_t bits) {
+  return act_to_f32(bits, DT);
+}
+
+// n..n+7 of a row of 16-bit (f32: 32-bit) values, `vec` if whole and aligned
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, bool f32, int64_t at, int left, bool vec, float (&v)[8]) {
+  if (f32) {
+    const float* q = (const float*)p + at;
+    if (vec) {
+      const f32x4 a = *(const f32x4*)q, b = *(const f32x4*)(q + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = a[j];
+        v[4 + j] = b[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < left ? q[j] : 0.0f;
+    }
+  } else {
+    const uint16_t* q = (const uint16_t*)p + at;
+    if (vec) {
+      const u32x4 a = load16(q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = half_to_f32<DT>(a[j] & 0xFFFFu);
+        v[2 * j + 1] = half_to_f32<DT>(a[j] >> 16);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = j < left ? half_to_f32<DT>(q[j]) : 0.0f;
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* p, bool f32, int64_t at, int left, bool vec, const float (&v)[8]) {
+  if (f32) {
+    float* q = (float*)p + at;
+    if (vec) {
+      *(f32x4*)q = f32x4{v[0], v[1], v[2], v[3]};
+      *(f32x4*)(q + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) q[j] = v[j];
+    }
+  } else {
+    uint16_t* q = (uint16_t*)p + at;
+    if (vec) {
+      u32x4 a;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        a[j] = (uint32_t)f32_to_act_bits(v[2 * j], DT) | (uint32_t)f32_to_act_bits(v[2 * j + 1], DT) << 16;
+      *(u32x4*)q = a;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) q[j] = f32_to_act_bits(v[j], DT);
+    }
+  }
+}
+
+// Eight columns n..n+7 of output row t from their fp32 sums (gated: u the sums
+// of the up columns).  Everything is fp32 up to the one rounding that gives
+// `out`; the kept z is rounded on its own.
+template <int DT, bool GATED>
+__device__ __forceinline__ void finish8(const LinearEpi& e, int64_t t, int n, float (&z)[8], float (&u)[8]) {
+  const int left = e.C - n;
+  const bool vec = e.vec && left >= 8;
+  if (e.bias) {
+    float b[8];
+    load8<DT>(e.bias, e.bias_f32, n, left, false, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] += b[j];
+    if (GATED) {
+      load8<DT>(e.bias, e.bias_f32, (int64_t)e.C + n, left, false, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += b[j];
+    }
+  }
+  if (e.pre) {
+    store8<DT>(e.pre, false, t * e.ldp + n, left, vec, z);
+    if (GATED) store8<DT>(e.pre, false, t * e.ldp + e.C + n, left, vec, u);
+  }
+  float r[8];
+  if (e.res) load8<DT>(e.res, e.out_f32, t * e.ldr + n, left, vec, r);
+  const float rs = e.row_scale ? e.row_scale[t] : 1.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float v = GATED ? z[j] * sigmoid_(z[j]) * u[j] : activate(e.act, z[j]);
+    if (e.row_scale) v *= rs;
+    z[j] = e.res ? r[j] + v : v;
+  }
+  store8<DT>(e.out, e.out_f32, t * e.ldo + n, left, vec, z);
+}
+
+// ------------------------------------------------------------ tile kernel --
+//
+// One workgroup computes BM x BN of C with WM x WN waves; k advances 64 a
+// step through NS stages in LDS that global_load_lds fills (16 bytes a lane, no
+// registers).  An operand whose k is contiguous stages rows of 64 k (128 bytes,
+// 16-byte pieces XORed with the row so that a wave's 16-byte reads meet no bank
+// twice); one whose m (n) is contiguous stages 64 rows of BM (BN) values and is
+// read with ds_read_b64_tr_b16, which transposes 4 x 16 blocks on the way into
+// the registers.  There the pieces are XORed so that the four k rows of a read
+// lie in different banks.
+//
+// Offsets: a descriptor starts at the tile's first element (64-bit), so that
+// offsets within it stay below 2^31; rows, columns and k past the operand's end
+// point past every descriptor and read zeros.
+struct Operand {
+  const uint16_t* p;
+  int64_t ld;  // elements between rows (of k, or of m)
+  int n;       // extent in m (or n)
+};
+
+template <bool TR, int R, int NI>
+struct Loader {
+  // R rows (m) of 64 k; NI load instructions of this wave
+  uint32_t off[NI];
+  int kc[NI];  // k-contiguous: first k of the lane's piece
+  const uint16_t* base;
+  int64_t ld;
+  uint32_t range;
+  int wide;  // m values left from the tile's first
+
+  __device__ __forceinline__ void init(const Operand& o, int m0, int q0, int lane) {
+    ld = o.ld;
+    const int left = o.n - m0;
+    wide = left;
+    if constexpr (!TR) {
+      base = o.p + (int64_t)m0 * ld;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = 8 * (q0 + i) + lane / 8;
+        const int piece = (lane & 7) ^ ((r / 2) & 7);
+        kc[i] = 8 * piece;
+        off[i] = r < left ? (uint32_t)((int64_t)r * ld * 2) + (uint32_t)piece * 16u : OUT_OF_RANGE;
+      }
+    } else {
+      base = o.p + m0;
+      constexpr int PPR = R / 8;  // pieces a row
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int at = 64 * (q0 + i) + lane;
+        const int kr = at / PPR;
+        const int piece = (at % PPR) ^ swizzle(kr);
+        kc[i] = kr;
+        off[i] = 8 * piece < left ? (uint32_t)((int64_t)kr * ld * 2) + (uint32_t)piece * 16u : OUT_OF_RANGE;
+      }
+    }
+  }
+  // which piece of k row kr holds logical piece 0: the four rows of a transposed read apart by 32 bytes
+  static __device__ __forceinline__ int swizzle(int kr) {
+    constexpr int PPR = R / 8;
+    return (((kr & 3) << 1) | (((kr >> 3) & 1) << 3)) & (PPR - 1);
+  }
+  // k0: first k of the step, kend: end of the workgroup's share
+  __device__ __forceinline__ void issue(int k0, int kend, int q0, uint8_t* lds) const {
+    if constexpr (!TR) {
+      const rsrc_t r = make_rsrc(base, OUT_OF_RANGE);
+      const int kl = kend - k0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        dma16(r, kc[i] < kl ? off[i] : OUT_OF_RANGE, (uint32_t)k0 * 2u, lds + (q0 + i) * 1024);
+    } else {
+      const rsrc_t r = make_rsrc(base + (int64_t)k0 * ld, OUT_OF_RANGE);
+      const int kl = kend - k0;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) dma16(r, kc[i] < kl ? off[i] : OUT_OF_RANGE, 0u, lds + (q0 + i) * 1024);
+    }
+  }
+  // fragment of 32 m (from m) and 16 k (step j of the stage): lane l holds m + l % 32, k = 16 j + 8 (l / 32) + 0..7
+  static __device__ __forceinline__ s16x8 read(const uint8_t* lds, int m, int j, int lane) {
+    if constexpr (!TR) {
+      const int row = m + lane % 32;
+      const int piece = (2 * j + lane / 32) ^ ((row / 2) & 7);
+      return *(const s16x8*)(lds + (row * 128 + (piece << 4)));
+    } else {
+      // lane i of a 16-lane group reads 4 values of row i / 4 and gets column i of the group's 4 x 16 block
+      const int col = m + 16 * ((lane / 16) & 1) + 4 * (lane & 3);
+      const int kr = 16 * j + 8 * (lane / 32) + ((lane & 15) >> 2);
+      auto half = [&](int kk) __attribute__((always_inline)) {
+        const int at = kk * (R * 2) + (((col >> 3) ^ swizzle(kk)) << 4) + (col & 7) * 2;
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at));
+      };
+      const s16x4 a = half(kr), b = half(kr + 4);
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+struct TileParams {
+  Operand a, b;
+  int K;
+  int m_tiles, n_tiles, splits, group_m, per_xcd;
+  int k_split;   // k of one split, a multiple of 64
+  float* part;   // splits > 1: fp32 sums [splits][M][N]
+  LinearEpi e;
+};
+
+// GATED: the wave's second column block holds the up columns of its first
+template <int DT, bool TA, bool TB, bool GATED, int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams prm) {
+  constexpr int WAVES = WM * WN;
+  constexpr int MS = BM / WM / 32, NSUB = BN / WN / 32;
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
+  constexpr int NIA = BM / 8 / WAVES, NIB = BN / 8 / WAVES, LOADS = NIA + NIB;
+  static_assert(NIA >= 1 && NIB >= 1, "every wave loads");
+  static_assert(!GATED || NSUB == 2, "one gate and one up block a wave");
+  static_assert(NS * STAGE <= 160 * 1024, "LDS");
+  // epilogue: each wave passes 32 rows of its columns through its own part of the stages
+  constexpr int ROWF = 32 * NSUB + 4;  // floats a row, with padding
+  static_assert(WAVES * 32 * ROWF * 4 <= NS * STAGE, "epilogue rows");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[NS * STAGE];
+
+  const int lane = lane_id(), wave = wave_id();
+  const int wm = wave / WN, wn = wave % WN;
+
+  // ---- the tile: XCD x takes a contiguous range of the tiles, which run over
+  // the row tiles of a group, then column tiles, then groups, then splits
+  const int logical = ((int)blockIdx.x % NUM_XCD) * prm.per_xcd + (int)blockIdx.x / NUM_XCD;
+  const int tiles = prm.m_tiles * prm.n_tiles;
+  const int split = logical / tiles;
+  if (split >= prm.splits) return;
+  const int in = logical - split * tiles;
+  const int per_group = prm.group_m * prm.n_tiles;
+  const int mg = in / per_group;
+  const int gm = min(prm.group_m, prm.m_tiles - mg * prm.group_m);
+  const int rem = in - mg * per_group;
+  const int mt = mg * prm.group_m + rem % gm, nt = rem / gm;
+  const int m0 = mt * BM;
+  const int c0 = nt * (GATED ? BN / 2 : BN);  // first output column
+
+  const int k_lo = split * prm.k_split, k_hi = min(prm.K, k_lo + prm.k_split);
+  const int steps = (k_hi - k_lo + 63) / 64;
+
+  Loader<TA, BM, NIA> la;
+  Loader<TB, BN, NIB> lb;
+  la.init(prm.a, m0, wave * NIA, lane);
+  if constexpr (!GATED) {
+    lb.init(prm.b, c0, wave * NIB, lane);
+  } else {
+    // tile row 64 w + r: gate row c0 + 32 w + r (r < 32), else up row
+    lb.ld = prm.b.ld;
+    lb.base = prm.b.p;
+#pragma unroll
+    for (int i = 0; i < NIB; ++i) {
+      const int r = 8 * (wave * NIB + i) + lane / 8;
+      const int piece = (lane & 7) ^ ((r / 2) & 7);
+      const int col = c0 + 32 * (r / 64) + r % 32;
+      lb.kc[i] = 8 * piece;
+      lb.off[i] = 0u;
+      if (col >= prm.e.C) lb.kc[i] = 0x7FFFFFFF;
+      lb.off[i] = (uint32_t)((int64_t)(32 * (r / 64) + r % 32) * lb.ld * 2) + (uint32_t)piece * 16u;
+    }
+  }
+
+  f32x16 acc[MS][NSUB];
+#pragma unroll
+  for (int mi = 0; mi < MS; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < NSUB; ++ni)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.0f;
+
+  auto issue = [&](int s, int step) __attribute__((always_inline)) {
+    const int k0 = k_lo + 64 * min(step, steps - 1);
+    uint8_t* st = lds + s * STAGE;
+    la.issue(k0, k_hi, wave * NIA, st);
+    if constexpr (!GATED) {
+      lb.issue(k0, k_hi, wave * NIB, st + A_BYTES);
+    } else {
+      // gate and up rows through two descriptors: instruction i of this wave covers eight rows of one kind
+#pragma unroll
+      for (int i = 0; i < NIB; ++i) {
+        const int q = wave * NIB + i;
+        const int64_t row = (int64_t)c0 + ((q / 4) & 1 ? prm.e.C : 0);
+        const rsrc_t r = make_rsrc(lb.base + row * lb.ld, OUT_OF_RANGE);
+        dma16(r, lb.kc[i] < k_hi - k0 ? lb.off[i] : OUT_OF_RANGE, (uint32_t)k0 * 2u, st + A_BYTES + q * 1024);
+      }
+    }
+  };
+
+  if (steps > 0) {
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      issue(s, s);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    int s = 0;
+    for (int step = 0; step < steps; ++step) {
+      wait_vmcnt<(NS - 2) * LOADS>();  // this wave's loads of the step have landed
+      __builtin_amdgcn_s_barrier();    // every wave's have; the stage before is free
+      issue(s == 0 ? NS - 1 : s - 1, step + NS - 1);
+      __builtin_amdgcn_sched_barrier(0);
+      const uint8_t* st = lds + s * STAGE;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s16x8 af[MS], bf[NSUB];
+#pragma unroll
+        for (int mi = 0; mi < MS; ++mi) af[mi] = Loader<TA, BM, NIA>::read(st, (wm * MS + mi) * 32, j, lane);
+#pragma unroll
+        for (int ni = 0; ni < NSUB; ++ni)
+          bf[ni] = Loader<TB, BN, NIB>::read(st + A_BYTES, (wn * NSUB + ni) * 32, j, lane);
+#pragma unroll
+        for (int mi = 0; mi < MS; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < NSUB; ++ni) acc[mi][ni] = mfma32<DT>(af[mi], bf[ni], acc[mi][ni]);
+      }
+      s = s + 1 == NS ? 0 : s + 1;
+    }
+  }
+  wait_vmcnt<0>();  // no load into LDS lands after this
+  __syncthreads();
+
+  // ---- epilogue: register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+  const int M = prm.a.n;
+  float* rows = (float*)lds + wave * (32 * ROWF);
+  const int hh = lane / 32, col = lane % 32;
+  constexpr int LPR = GATED ? 4 : 4 * NSUB;  // lanes a row, eight columns each
+#pragma unroll
+  for (int mi = 0; mi < MS; ++mi) {
+#pragma unroll
+    for (int ni = 0; ni < NSUB; ++ni)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        rows[(8 * (r / 4) + 4 * hh + r % 4) * ROWF + ni * 32 + col] = acc[mi][ni][r];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const int t0 = m0 + (wm * MS + mi) * 32;
+#pragma unroll 1
+    for (int r = lane / LPR; r < 32; r += 64 / LPR) {
+      const int c = 8 * (lane % LPR);
+      const int n = c0 + wn * (GATED ? 32 : 32 * NSUB) + c;
+      const float* src = rows + r * ROWF + c;
+      float z[8], u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        z[j] = src[j];
+        u[j] = GATED ? src[32 + j] : 0.0f;
+      }
+      if (t0 + r < M && n < prm.e.C) {
+        if (prm.splits > 1) {
+          const bool vec = prm.e.C % 4 == 0 && n + 8 <= prm.e.C;
+          store8<DT>(prm.part, true, ((int64_t)split * M + t0 + r) * prm.e.C + n, prm.e.C - n, vec, z);
+        } else {
+          finish8<DT, GATED>(prm.e, t0 + r, n, z, u);
+        }
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// The sums of the splits in order, and the epilogue: a thread eight columns of a row
+template <int DT>
+__global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ part, int splits, int M, int N,
+                                                          LinearEpi e) {
+  const int chunks = (e.C + 7) / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)M * chunks) return;
+  const int64_t t = i / chunks;
+  const int n = (int)(i - t * chunks) * 8;
+  const bool gated = e.act == LIN_SWIGLU;
+  const bool vec = N % 4 == 0 && n + 8 <= e.C && (!gated || e.C % 4 == 0);
+  float z[8], u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) z[j] = u[j] = 0.0f;
+  for (int s = 0; s < splits; ++s) {
+    const int64_t row = ((int64_t)s * M + t) * N + n;
+    float v[8];
+    load8<DT>(part, true, row, e.C - n, vec, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] += v[j];
+    if (gated) {
+      load8<DT>(part, true, row + e.C, e.C - n, vec, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += v[j];
+    }
+  }
+  if (gated) finish8<DT, true>(e, t, n, z, u);
+  else finish8<DT, false>(e, t, n, z, u);
+}
+
+// ------------------------------------------------------- gradient of z ----
+//
+// A workgroup takes `rows` rows; a thread eight columns at a time.  dz (rounded
+// to the operands' 16 bits: the matrix cores' input) is the operand of both
+// products; the sums of bias and row_scale use it unrounded.  Columns from C up
+// to ldz are zero.  Column sums go to part[block][N], joined in order.
+template <int DT>
+__global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
+  __shared__ float row_sum[4][64];
+  const int lane = lane_id(), wave = wave_id();
+  const bool gated = g.act == LIN_SWIGLU;
+  const int64_t t0 = (int64_t)blockIdx.x * g.rows;
+  const int rows = (int)min((int64_t)g.rows, g.T - t0);
+  if (g.drs)
+    for (int i = threadIdx.x; i < 256; i += 256) row_sum[i / 64][i % 64] = 0.0f;
+  __syncthreads();
+  for (int base = 0; base < g.C; base += 2048) {
+    const int n = base + 8 * (int)threadIdx.x;
+    const int left = g.C - n;
+    const bool on = left > 0;
+    const bool vec = g.vec && left >= 8;
+    float cs[8], cu[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cs[j] = cu[j] = 0.0f;
+    for (int r = 0; r < rows; ++r) {
+      const int64_t t = t0 + r;
+      float d[8], d2[8], dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = d2[j] = 0.0f;
+      if (on) {
+        load8<DT>(g.g, g.g_f32, t * g.ldg + n, left, vec, d);
+        const float rs = g.rs ? g.rs[t] : 1.0f;
+        float z[8], u[8];  // columns past the end: all 0
+        if (g.z) load8<DT>(g.z, false, t * g.ldz_in + n, left, vec, z);
+        if (gated) load8<DT>(g.z, false, t * g.ldz_in + g.C + n, left, vec, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float gv = g.rs ? d[j] * rs : d[j];
+          float a = 0.0f, slope = 1.0f;
+          if (g.z) a = activate_slope(gated ? LIN_SILU : g.act, z[j], slope);
+          if (gated) {
+            dot += d[j] * (a * u[j]);
+            d2[j] = gv * a;
+            slope *= u[j];
+          } else {
+            dot += d[j] * a;
+          }
+          d[j] = gv * slope;
+        }
+        if (g.dz) {
+          store8<DT>(g.dz, false, t * g.ldz + n, left, vec, d);
+          if (gated) store8<DT>(g.dz, false, t * g.ldz + g.C + n, left, vec, d2);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          cs[j] += d[j];
+          cu[j] += d2[j];
+        }
+      }
+      if (g.drs) {
+        const float s = wave_sum(dot);
+        if (lane == 0) row_sum[wave][r] += s;
+      }
+    }
+    if (g.part && on) {
+      float* p = g.part + (int64_t)blockIdx.x * g.N;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) {
+          p[n + j] = cs[j];
+          if (gated) p[g.C + n + j] = cu[j];
+        }
+    }
+  }
+  // the padding of dz rows
+  if (g.dz) {
+    const int pad = (int)(g.ldz - g.N);
+    for (int i = threadIdx.x; i < rows * pad; i += 256)
+      ((uint16_t*)g.dz)[(t0 + i / pad) * g.ldz + g.N + i % pad] = 0;
+  }
+  __syncthreads();
+  if (g.drs)
+    for (int r = threadIdx.x; r < rows; r += 256)
+      g.drs[t0 + r] = ((row_sum[0][r] + row_sum[1][r]) + row_sum[2][r]) + row_sum[3][r];
+}
+
+__global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restrict__ part, int blocks, int N,
+                                                          float* __restrict__ out) {
+  const int n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= N) return;
+  float s = 0.0f;
+  for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * N + n];
+  out[n] = s;
+}
+
+// -------------------------------------------------------------- launchers --
+
+struct Plan {
+  int bm, bn, splits;
+};
+
+// The tile and the split of k of a product M x N over K
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  Plan p{128, 128, 1};
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  const int64_t steps = (K + 63) / 64;
+  // fewer tiles than CUs: shares of k of at least eight steps
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), steps / 8));
+  return p;
+}
+
+template <int DT, bool TA, bool TB, bool GATED>
+hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const LinearEpi& e, float* part,
+                       hipStream_t st) {
+  TileParams prm;
+  prm.a = a;
+  prm.b = b;
+  prm.K = K;
+  prm.e = e;
+  prm.part = part;
+  const Plan p = plan_of(a.n, N, K);
+  const bool split = p.splits > 1;
+  const int64_t steps = (K + 63) / 64;
+  prm.splits = p.splits;
+  prm.k_split = (int)((steps + p.splits - 1) / p.splits) * 64;
+  prm.m_tiles = (a.n + 127) / 128;
+  const int C = split ? N : e.C;
+  prm.e.C = C;
+  const int cols = GATED && !split ? 64 : 128;
+  prm.n_tiles = (C + cols - 1) / cols;
+  prm.group_m = std::min(prm.m_tiles, 8);
+  const int64_t total = (int64_t)prm.m_tiles * prm.n_tiles * prm.splits;
+  prm.per_xcd = (int)((total + NUM_XCD - 1) / NUM_XCD);
+  const dim3 grid((unsigned)(prm.per_xcd * NUM_XCD));
+  if (!split) return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
+  hipError_t r = launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
+  if (r != hipSuccess) return r;
+  const int64_t threads = (int64_t)a.n * ((e.C + 7) / 8);
+  return launch_kernel(linear_join_kernel<DT>, (unsigned)((threads + 255) / 256), 256, 0, st, part, p.splits, a.n, N,
+                       e);
+}
+
+template <int DT>
+hipError_t forward(const void* x, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K, const LinearEpi& e,
+                   float* part, hipStream_t st) {
+  const Operand a{(const uint16_t*)x, ldx, T}, b{(const uint16_t*)w, ldw, N};
+  if (e.act == LIN_SWIGLU) return launch_tile<DT, false, false, true>(a, b, N, K, e, part, st);
+  return launch_tile<DT, false, false, false>(a, b, N, K, e, part, st);
+}
+
+LinearEpi plain_out(void* out, int64_t ld, int C) {
+  LinearEpi e{};
+  e.out = out;
+  e.ldo = ld;
+  e.C = C;
+  e.act = LIN_NONE;
+  e.vec = ld % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+  return e;
+}
+
+template <int DT>
+hipError_t backward(const LinearGrad& g, const void* x, int64_t ldx, const void* w, int64_t ldw, int K, void* dx,
+                    int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias, const uint16_t* dz, int64_t ldz,
+                    float* part, hipStream_t st) {
+  if (g.dz || g.part || g.drs) {
+    if (g.T) {
+      const hipError_t r = launch_kernel(linear_dz_kernel<DT>, (unsigned)g.blocks, 256, 0, st, g);
+      if (r != hipSuccess) return r;
+    }
+    if (dbias) {
+      const hipError_t r2 = launch_kernel(linear_bias_kernel, (unsigned)((g.N + 255) / 256), 256, 0, st, g.part,
+                                          g.blocks, g.N, dbias);
+      if (r2 != hipSuccess) return r2;
+    }
+  }
+  if (dx) {
+    const Operand a{dz, ldz, (int)g.T}, b{(const uint16_t*)w, ldw, K};
+    const hipError_t r =
+        launch_tile<DT, false, true, false>(a, b, K, g.N, plain_out(dx, ldx_out, K), part, st);
+    if (r != hipSuccess) return r;
+  }
+  if (dw) {
+    const Operand a{dz, ldz, g.N}, b{(const uint16_t*)x, ldx, K};
+    return launch_tile<DT, true, true, false>(a, b, K, (int)g.T, plain_out(dw, ldw_out, K), part, st);
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K) {
+  const Plan p = plan_of(M, N, K);
+  return p.splits > 1 ? (int64_t)p.splits * M * N * 4 : 0;
+}
+
+hipError_t launch_linear(const void* x, int dt, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K,
+                         const LinearEpi& e, float* part, hipStream_t st) {
+  return dt == ACT_BF16 ? forward<ACT_BF16>(x, ldx, T, w, ldw, N, K, e, part, st)
+                        : forward<ACT_F16>(x, ldx, T, w, ldw, N, K, e, part, st);
+}
+
+hipError_t launch_linear_backward(const LinearGrad& g, int dt, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                  int K, void* dx, int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias,
+                                  const uint16_t* dz, int64_t ldz, float* part, hipStream_t st) {
+  return dt == ACT_BF16
+             ? backward<ACT_BF16>(g, x, ldx, w, ldw, K, dx, ldx_out, dw, ldw_out, dbias, dz, ldz, part, st)
+             : backward<ACT_F16>(g, x, ldx, w, ldw, K, dx, ldx_out, dw, ldw_out, dbias, dz, ldz, part, st);
+}
+
+}  // namespace moe

@@ -326,6 +326,78 @@ moe_status check_gate(moe_dtype lt, int64_t ld, int T, int E, int k) {
   return MOE_OK;
 }
 
+// options of the balance loss, checked (NULL: softmax, one sequence, no mask)
+moe_status check_balance_opts(const moe_balance_opts* o, moe::BalanceDev* b) {
+  *b = moe::BalanceDev{moe::GATE_SOFTMAX, 1, nullptr, nullptr};
+  if (!o) return MOE_OK;
+  if (o->score != MOE_SCORE_SOFTMAX && o->score != MOE_SCORE_SIGMOID) return MOE_ERR_OPTION;
+  if (o->seqs < 1 || o->seqs > MOE_BALANCE_MAX_SEQS || (o->seqs != 1 && !o->offsets)) return MOE_ERR_OPTION;
+  if (!aligned4(o->offsets)) return MOE_ERR_ALIGN;
+  b->score = o->score == MOE_SCORE_SIGMOID ? moe::GATE_SIGMOID : moe::GATE_SOFTMAX;
+  b->S = o->seqs;
+  b->offsets = o->offsets;
+  b->mask = o->mask;
+  return MOE_OK;
+}
+
+constexpr int64_t kMaxElements = int64_t(1) << 40;  // of a matrix that moe_linear reads or writes
+
+// sizes of a dense product; what is read of it is checked by the callers
+moe_status check_dense(const moe_dense* d, moe_dtype dt, int T) {
+  if (!d) return MOE_ERR_NULL;
+  if (!half_type(dt)) return MOE_ERR_DTYPE;
+  if (T < 0 || T > MOE_GATE_MAX_TOKENS || d->K < 8 || d->K % 8 != 0 || d->K > MOE_LINEAR_MAX_COLUMNS || d->N < 1 ||
+      d->N > MOE_LINEAR_MAX_COLUMNS)
+    return MOE_ERR_SHAPE;
+  if ((int64_t)T * d->N > kMaxElements || (int64_t)T * d->K > kMaxElements || (int64_t)d->N * d->K > kMaxElements)
+    return MOE_ERR_SHAPE;
+  if (d->act < MOE_ACT_NONE || d->act > MOE_ACT_SWIGLU) return MOE_ERR_OPTION;
+  if (d->act == MOE_ACT_SWIGLU && d->N % 2 != 0) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+// an operand of the matrix cores: 16-byte pieces of rows
+moe_status check_operand(const void* p, int64_t ld, int K) {
+  if (!p) return MOE_ERR_NULL;
+  if (ld < K || ld % 8 != 0 || ld > MOE_LINEAR_MAX_COLUMNS) return MOE_ERR_SHAPE;
+  return aligned16(p) ? MOE_OK : MOE_ERR_ALIGN;
+}
+
+moe_status check_matrix(const void* p, moe_dtype dt, int64_t ld, int64_t columns) {
+  if (ld < columns || ld > MOE_LINEAR_MAX_COLUMNS) return MOE_ERR_SHAPE;
+  return aligned_to(p, dt) ? MOE_OK : MOE_ERR_ALIGN;
+}
+
+// rows of type dt that start 16-byte aligned
+bool rows16(const void* p, moe_dtype dt, int64_t ld) {
+  return aligned16(p) && ld % (dt == MOE_F32 ? 4 : 8) == 0;
+}
+
+struct LinearGradLayout {
+  size_t dz, sums, part, total;
+  int64_t ldz;
+  int rows, blocks;
+};
+
+LinearGradLayout linear_grad_layout(int64_t T, int64_t N, int64_t K) {
+  LinearGradLayout L{};
+  L.ldz = (N + 7) / 8 * 8;
+  L.rows = T <= 16384 ? 16 : moe::LINEAR_DZ_ROWS;
+  L.blocks = (int)((T + L.rows - 1) / L.rows);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    size_t r = at;
+    at += align_up(bytes);
+    return r;
+  };
+  L.dz = take((size_t)(T * L.ldz * 2));
+  L.sums = take((size_t)((int64_t)L.blocks * N * 4));
+  // the two products run one after the other
+  L.part = take((size_t)std::max(moe::linear_part_bytes(T, K, N), moe::linear_part_bytes(N, K, T)));
+  L.total = at;
+  return L;
+}
+
 // the selection launches: static top-k, or the adaptive pass (two launches
 // with scratch for the per-token entropies, one without)
 // (clear_word: see launch_topk)
@@ -890,6 +962,197 @@ moe_status moe_lora_add(const void* x, moe_dtype dt, int64_t ldx, int32_t T, con
     HIP_TRY(moe::launch_lora(x, (int)dt, ldx, T, ad, ids, base, ld_base, out, ld_out, out_dt == MOE_F32, props.num_cu,
                              st));
     plan_step("lora", st);
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S) {
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || S < 1) return 0;
+  return align_up((size_t)moe::balance_ws_bytes(T, E, S));
+}
+
+moe_status moe_balance_loss(const void* logits, moe_dtype lt, int64_t ld, int32_t T, int32_t E, int32_t k,
+                            const int32_t* topk_idx, const moe_balance_opts* opts, float* loss, float* z, float* prob,
+                            int32_t* counts, int32_t* tokens, void* ws, size_t ws_bytes, void* stream) {
+  try {
+    moe_status s = check_gate(lt, ld, T, E, k);
+    if (s != MOE_OK) return s;
+    moe::BalanceDev b;
+    if ((s = check_balance_opts(opts, &b)) != MOE_OK) return s;
+    if (z && b.score != moe::GATE_SOFTMAX) return MOE_ERR_OPTION;
+    if (!loss || !counts || !tokens || (T != 0 && (!logits || !topk_idx))) return MOE_ERR_NULL;
+    if (!aligned_to(logits, lt) || !aligned4(topk_idx) || !aligned4(loss) || !aligned4(z) || !aligned4(prob) ||
+        !aligned4(counts) || !aligned4(tokens))
+      return MOE_ERR_ALIGN;
+    if (T != 0) {
+      if (!ws || ws_bytes < moe_balance_workspace_size(T, E, b.S)) return MOE_ERR_WORKSPACE;
+      if (!aligned16(ws)) return MOE_ERR_ALIGN;
+    }
+    DevProps props;
+    if ((s = device_props(&props)) != MOE_OK) return s;
+    hipStream_t st = (hipStream_t)stream;
+    plan_begin(st);
+    HIP_TRY(moe::launch_balance(logits, (int)lt, ld, T, E, k, topk_idx, b, loss, z, prob, counts, tokens, ws, st));
+    plan_step("balance", st);
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, int64_t ld, int32_t T, int32_t E, int32_t k,
+                                     const moe_balance_opts* opts, const int32_t* counts, const int32_t* tokens,
+                                     const float* grad_loss, const float* grad_z, void* grad_logits, int64_t ld_grad,
+                                     void* stream) {
+  try {
+    moe_status s = check_gate(lt, ld, T, E, k);
+    if (s != MOE_OK) return s;
+    if (ld_grad < E) return MOE_ERR_SHAPE;
+    moe::BalanceDev b;
+    if ((s = check_balance_opts(opts, &b)) != MOE_OK) return s;
+    if (grad_z && b.score != moe::GATE_SOFTMAX) return MOE_ERR_OPTION;
+    if (T == 0) return MOE_OK;
+    if (!logits || !counts || !tokens || !grad_logits) return MOE_ERR_NULL;
+    if (!aligned_to(logits, lt) || !aligned_to(grad_logits, lt) || !aligned4(counts) || !aligned4(tokens) ||
+        !aligned4(grad_loss) || !aligned4(grad_z))
+      return MOE_ERR_ALIGN;
+    DevProps props;
+    if ((s = device_props(&props)) != MOE_OK) return s;
+    hipStream_t st = (hipStream_t)stream;
+    plan_begin(st);
+    HIP_TRY(moe::launch_balance_backward(logits, (int)lt, ld, T, E, k, b, counts, tokens, grad_loss, grad_z,
+                                         grad_logits, ld_grad, st));
+    plan_step("balance_backward", st);
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+size_t moe_linear_workspace_size(int32_t T, int32_t N, int32_t K) {
+  if (T < 0 || N < 1 || K < 1) return 0;
+  return align_up((size_t)moe::linear_part_bytes(T, N, K));
+}
+
+moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const moe_dense* dense,
+                      const void* residual, int64_t ld_residual, const float* row_scale, void* preact,
+                      int64_t ld_preact, void* out, int64_t ld_out, moe_dtype out_dt, void* ws, size_t ws_bytes,
+                      void* stream) {
+  try {
+    moe_status s = check_dense(dense, dt, T);
+    if (s != MOE_OK) return s;
+    if (out_dt != dt && out_dt != MOE_F32) return MOE_ERR_DTYPE;
+    const int N = dense->N, K = dense->K, C = dense->act == MOE_ACT_SWIGLU ? N / 2 : N;
+    const moe_dtype bias_dt = (moe_dtype)dense->bias_dt;
+    if (dense->bias && bias_dt != dt && bias_dt != MOE_F32) return MOE_ERR_DTYPE;
+    if ((s = check_operand(dense->w, dense->ldw, K)) != MOE_OK) return s;
+    if (dense->bias && !aligned_to(dense->bias, bias_dt)) return MOE_ERR_ALIGN;
+    if (T == 0) return MOE_OK;
+    if ((s = check_operand(x, ldx, K)) != MOE_OK) return s;
+    if (!out) return MOE_ERR_NULL;
+    if ((s = check_matrix(out, out_dt, ld_out, C)) != MOE_OK) return s;
+    if (residual && (s = check_matrix(residual, out_dt, ld_residual, C)) != MOE_OK) return s;
+    if (residual == out && ld_residual != ld_out) return MOE_ERR_SHAPE;  // in place: the same rows
+    if (preact && (s = check_matrix(preact, dt, ld_preact, N)) != MOE_OK) return s;
+    if (!aligned4(row_scale)) return MOE_ERR_ALIGN;
+    const size_t need = moe_linear_workspace_size(T, N, K);
+    if (need) {
+      if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+      if (!aligned16(ws)) return MOE_ERR_ALIGN;
+    }
+    DevProps props;
+    if ((s = device_props(&props)) != MOE_OK) return s;
+    moe::LinearEpi e{};
+    e.bias = dense->bias;
+    e.bias_f32 = bias_dt == MOE_F32;
+    e.res = residual;
+    e.row_scale = row_scale;
+    e.out = out;
+    e.pre = preact;
+    e.ldr = ld_residual;
+    e.ldo = ld_out;
+    e.ldp = ld_preact;
+    e.C = C;
+    e.act = dense->act;
+    e.out_f32 = out_dt == MOE_F32;
+    e.vec = rows16(out, out_dt, ld_out) && (!residual || rows16(residual, out_dt, ld_residual)) &&
+            (!preact || (rows16(preact, dt, ld_preact) && (C == N || C % 8 == 0)));
+    hipStream_t st = (hipStream_t)stream;
+    plan_begin(st);
+    HIP_TRY(moe::launch_linear(x, (int)dt, ldx, T, dense->w, dense->ldw, N, K, e, (float*)ws, st));
+    plan_step("linear", st);
+    return MOE_OK;
+  } catch (...) {
+    return MOE_ERR_INTERNAL;
+  }
+}
+
+size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t K) {
+  if (T < 0 || N < 1 || K < 1) return 0;
+  return linear_grad_layout(T, N, K).total;
+}
+
+moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_grad, const void* x, moe_dtype dt,
+                               int64_t ldx, int32_t T, const moe_dense* dense, const void* preact, int64_t ld_preact,
+                               const float* row_scale, void* grad_x, int64_t ld_grad_x, void* grad_w,
+                               int64_t ld_grad_w, float* grad_bias, float* grad_row_scale, void* ws, size_t ws_bytes,
+                               void* stream) {
+  try {
+    moe_status s = check_dense(dense, dt, T);
+    if (s != MOE_OK) return s;
+    if (grad_dt != dt && grad_dt != MOE_F32) return MOE_ERR_DTYPE;
+    const int N = dense->N, K = dense->K, C = dense->act == MOE_ACT_SWIGLU ? N / 2 : N;
+    if (grad_x) {
+      if ((s = check_operand(dense->w, dense->ldw, K)) != MOE_OK) return s;
+      if ((s = check_matrix(grad_x, dt, ld_grad_x, K)) != MOE_OK) return s;
+    }
+    if (grad_w && (s = check_matrix(grad_w, dt, ld_grad_w, K)) != MOE_OK) return s;
+    if (!aligned4(grad_bias) || !aligned4(grad_row_scale) || !aligned4(row_scale)) return MOE_ERR_ALIGN;
+    if (T != 0) {
+      if (!grad) return MOE_ERR_NULL;
+      if ((s = check_matrix(grad, grad_dt, ld_grad, C)) != MOE_OK) return s;
+      if (grad_w && (s = check_operand(x, ldx, K)) != MOE_OK) return s;
+      if (!preact && (dense->act != MOE_ACT_NONE || grad_row_scale)) return MOE_ERR_NULL;
+      if (preact && (s = check_matrix(preact, dt, ld_preact, N)) != MOE_OK) return s;
+    }
+    const LinearGradLayout L = linear_grad_layout(T, N, K);
+    if (L.total) {
+      if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+      if (!aligned16(ws)) return MOE_ERR_ALIGN;
+    }
+    DevProps props;
+    if ((s = device_props(&props)) != MOE_OK) return s;
+    uint8_t* W = (uint8_t*)ws;
+    // the gradient itself is dz where nothing changes it and its rows are operands
+    const bool direct = dense->act == MOE_ACT_NONE && !row_scale && grad_dt == dt && N % 8 == 0 &&
+                        T != 0 && rows16(grad, dt, ld_grad);
+    moe::LinearGrad g{};
+    g.g = grad;
+    g.g_f32 = grad_dt == MOE_F32;
+    g.ldg = ld_grad;
+    g.z = dense->act != MOE_ACT_NONE || grad_row_scale ? preact : nullptr;
+    g.ldz_in = ld_preact;
+    g.rs = row_scale;
+    g.dz = direct || !(grad_x || grad_w) || T == 0 ? nullptr : (uint16_t*)(W + L.dz);
+    g.ldz = L.ldz;
+    g.drs = grad_row_scale;
+    g.part = grad_bias ? (float*)(W + L.sums) : nullptr;
+    g.T = T;
+    g.C = C;
+    g.N = N;
+    g.act = dense->act;
+    g.rows = L.rows;
+    g.blocks = L.blocks;
+    g.vec = rows16(grad, grad_dt, ld_grad) && (!g.z || rows16(preact, dt, ld_preact)) && (C == N || C % 8 == 0);
+    const uint16_t* dz = direct ? (const uint16_t*)grad : (const uint16_t*)(W + L.dz);
+    hipStream_t st = (hipStream_t)stream;
+    plan_begin(st);
+    HIP_TRY(moe::launch_linear_backward(g, (int)dt, x, ldx, dense->w, dense->ldw, K, T ? grad_x : nullptr, ld_grad_x,
+                                        grad_w, ld_grad_w, grad_bias, dz, direct ? ld_grad : L.ldz,
+                                        (float*)(W + L.part), st));
+    plan_step("linear_backward", st);
     return MOE_OK;
   } catch (...) {
     return MOE_ERR_INTERNAL;
