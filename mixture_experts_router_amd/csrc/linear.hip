@@ -233,26 +233,31 @@ struct Operand {
 
 template <bool TR, int R, int NI>
 struct Loader {
-  // R rows (m) of 64 k; NI load instructions of this wave
-  uint32_t off[NI];
-  int kc[NI];  // k-contiguous: first k of the lane's piece
+  uint32_t off[NI];  // byte offsets of this wave's NI load instructions
+  int kc[NI];        // first k (TR: the k row) of the lane's piece
   const uint16_t* base;
+  const uint16_t* base2;  // GATED: the up rows
   int64_t ld;
-  uint32_t range;
-  int wide;  // m values left from the tile's first
 
-  __device__ __forceinline__ void init(const Operand& o, int m0, int q0, int lane) {
+  // which piece of k row kr holds logical piece 0: the four rows of a transposed read apart by 32 bytes
+  static __device__ __forceinline__ int swizzle(int kr) {
+    return (((kr & 3) << 1) | (((kr >> 3) & 1) << 3)) & (R / 8 - 1);
+  }
+  // GATED: tile rows run over 32 gate rows from m0 and the 32 up rows `up` further, by turns
+  template <bool GATED>
+  __device__ __forceinline__ void init(const Operand& o, int m0, int up, int q0, int lane) {
     ld = o.ld;
-    const int left = o.n - m0;
-    wide = left;
+    const int left = (GATED ? up : o.n) - m0;
     if constexpr (!TR) {
       base = o.p + (int64_t)m0 * ld;
+      base2 = o.p + ((int64_t)m0 + up) * ld;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int r = 8 * (q0 + i) + lane / 8;
         const int piece = (lane & 7) ^ ((r / 2) & 7);
+        const int row = GATED ? 32 * (r / 64) + r % 32 : r;
         kc[i] = 8 * piece;
-        off[i] = r < left ? (uint32_t)((int64_t)r * ld * 2) + (uint32_t)piece * 16u : OUT_OF_RANGE;
+        off[i] = row < left ? (uint32_t)((int64_t)row * ld * 2) + (uint32_t)piece * 16u : OUT_OF_RANGE;
       }
     } else {
       base = o.p + m0;
@@ -267,25 +272,17 @@ struct Loader {
       }
     }
   }
-  // which piece of k row kr holds logical piece 0: the four rows of a transposed read apart by 32 bytes
-  static __device__ __forceinline__ int swizzle(int kr) {
-    constexpr int PPR = R / 8;
-    return (((kr & 3) << 1) | (((kr >> 3) & 1) << 3)) & (PPR - 1);
-  }
-  // k0: first k of the step, kend: end of the workgroup's share
+  // the step of k0 .. k0 + 63 up to kend (none of it: zeros, without memory traffic)
+  template <bool GATED>
   __device__ __forceinline__ void issue(int k0, int kend, int q0, uint8_t* lds) const {
-    if constexpr (!TR) {
-      const rsrc_t r = make_rsrc(base, OUT_OF_RANGE);
-      const int kl = kend - k0;
+    const int kl = kend - k0;
+    const uint32_t range = kl > 0 ? OUT_OF_RANGE : 0u;
+    const uint32_t soff = TR ? 0u : (uint32_t)k0 * 2u;
+    const rsrc_t r = make_rsrc(TR ? base + (int64_t)k0 * ld : base, range);
+    const rsrc_t r2 = make_rsrc(GATED ? base2 : base, range);
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-        dma16(r, kc[i] < kl ? off[i] : OUT_OF_RANGE, (uint32_t)k0 * 2u, lds + (q0 + i) * 1024);
-    } else {
-      const rsrc_t r = make_rsrc(base + (int64_t)k0 * ld, OUT_OF_RANGE);
-      const int kl = kend - k0;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) dma16(r, kc[i] < kl ? off[i] : OUT_OF_RANGE, 0u, lds + (q0 + i) * 1024);
-    }
+    for (int i = 0; i < NI; ++i)
+      dma16(GATED && ((q0 + i) / 4) % 2 ? r2 : r, kc[i] < kl ? off[i] : OUT_OF_RANGE, soff, lds + (q0 + i) * 1024);
   }
   // fragment of 32 m (from m) and 16 k (step j of the stage): lane l holds m + l % 32, k = 16 j + 8 (l / 32) + 0..7
   static __device__ __forceinline__ s16x8 read(const uint8_t* lds, int m, int j, int lane) {
@@ -325,11 +322,25 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
   constexpr int NIA = BM / 8 / WAVES, NIB = BN / 8 / WAVES, LOADS = NIA + NIB;
   static_assert(NIA >= 1 && NIB >= 1, "every wave loads");
   static_assert(!GATED || NSUB == 2, "one gate and one up block a wave");
-  static_assert(NS * STAGE <= 160 * 1024, "LDS");
+  static_assert(NS >= 2 && NS <= 4 && NS * STAGE <= 160 * 1024, "LDS");
   // epilogue: each wave passes 32 rows of its columns through its own part of the stages
   constexpr int ROWF = 32 * NSUB + 4;  // floats a row, with padding
-  static_assert(WAVES * 32 * ROWF * 4 <= NS * STAGE, "epilogue rows");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[NS * STAGE];
+  constexpr int ROWS_BYTES = 32 * ROWF * 4;
+  constexpr int PER_STAGE = STAGE / ROWS_BYTES;  // waves that fit in a stage
+  static_assert(PER_STAGE * NS >= WAVES, "epilogue rows");
+  // one array per stage: distinct objects let the compiler see that reading a
+  // stage does not wait on loads still landing in the others
+  __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE], st1[STAGE], st2[NS > 2 ? STAGE : 16],
+      st3[NS > 3 ? STAGE : 16];
+  auto stage = [&](auto S_) __attribute__((always_inline)) -> uint8_t* {
+    constexpr int S = decltype(S_)::value;
+    if constexpr (S == 0) return st0;
+    else if constexpr (S == 1) return st1;
+    else if constexpr (S == 2) return st2;
+    else return st3;
+  };
+  typedef Loader<TA, BM, NIA> LA;
+  typedef Loader<TB, BN, NIB> LB;
 
   const int lane = lane_id(), wave = wave_id();
   const int wm = wave / WN, wn = wave % WN;
@@ -350,28 +361,12 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
   const int c0 = nt * (GATED ? BN / 2 : BN);  // first output column
 
   const int k_lo = split * prm.k_split, k_hi = min(prm.K, k_lo + prm.k_split);
-  const int steps = (k_hi - k_lo + 63) / 64;
+  const int steps = (k_hi - k_lo + 63) / 64;  // not positive: all sums 0
 
-  Loader<TA, BM, NIA> la;
-  Loader<TB, BN, NIB> lb;
-  la.init(prm.a, m0, wave * NIA, lane);
-  if constexpr (!GATED) {
-    lb.init(prm.b, c0, wave * NIB, lane);
-  } else {
-    // tile row 64 w + r: gate row c0 + 32 w + r (r < 32), else up row
-    lb.ld = prm.b.ld;
-    lb.base = prm.b.p;
-#pragma unroll
-    for (int i = 0; i < NIB; ++i) {
-      const int r = 8 * (wave * NIB + i) + lane / 8;
-      const int piece = (lane & 7) ^ ((r / 2) & 7);
-      const int col = c0 + 32 * (r / 64) + r % 32;
-      lb.kc[i] = 8 * piece;
-      lb.off[i] = 0u;
-      if (col >= prm.e.C) lb.kc[i] = 0x7FFFFFFF;
-      lb.off[i] = (uint32_t)((int64_t)(32 * (r / 64) + r % 32) * lb.ld * 2) + (uint32_t)piece * 16u;
-    }
-  }
+  LA la;
+  LB lb;
+  la.template init<false>(prm.a, m0, 0, wave * NIA, lane);
+  lb.template init<GATED>(prm.b, c0, prm.e.C, wave * NIB, lane);
 
   f32x16 acc[MS][NSUB];
 #pragma unroll
@@ -381,59 +376,79 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.0f;
 
-  auto issue = [&](int s, int step) __attribute__((always_inline)) {
-    const int k0 = k_lo + 64 * min(step, steps - 1);
-    uint8_t* st = lds + s * STAGE;
-    la.issue(k0, k_hi, wave * NIA, st);
-    if constexpr (!GATED) {
-      lb.issue(k0, k_hi, wave * NIB, st + A_BYTES);
-    } else {
-      // gate and up rows through two descriptors: instruction i of this wave covers eight rows of one kind
+  auto issue = [&](auto S_, int step) __attribute__((always_inline)) {
+    const int k0 = k_lo + 64 * step;
+    uint8_t* st = stage(S_);
+    la.template issue<false>(k0, k_hi, wave * NIA, st);
+    lb.template issue<GATED>(k0, k_hi, wave * NIB, st + A_BYTES);
+  };
+  auto fragments = [&](const uint8_t* st, int j, s16x8 (&af)[MS], s16x8 (&bf)[NSUB]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < NIB; ++i) {
-        const int q = wave * NIB + i;
-        const int64_t row = (int64_t)c0 + ((q / 4) & 1 ? prm.e.C : 0);
-        const rsrc_t r = make_rsrc(lb.base + row * lb.ld, OUT_OF_RANGE);
-        dma16(r, lb.kc[i] < k_hi - k0 ? lb.off[i] : OUT_OF_RANGE, (uint32_t)k0 * 2u, st + A_BYTES + q * 1024);
-      }
-    }
+    for (int ni = 0; ni < NSUB; ++ni) bf[ni] = LB::read(st + A_BYTES, (wn * NSUB + ni) * 32, j, lane);
+#pragma unroll
+    for (int mi = 0; mi < MS; ++mi) af[mi] = LA::read(st, (wm * MS + mi) * 32, j, lane);
+  };
+  auto multiply = [&](const s16x8 (&af)[MS], const s16x8 (&bf)[NSUB]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int mi = 0; mi < MS; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NSUB; ++ni) acc[mi][ni] = mfma32<DT>(af[mi], bf[ni], acc[mi][ni]);
   };
 
+  // Fragments are read one k-step of 16 ahead of the MFMAs.  Before the last
+  // of a stage's four, its reads are complete: one wait for the next stage's
+  // loads and one barrier, after which the stage is refilled NS steps ahead and
+  // the next stage's first fragments are read under the last MFMAs.
   if (steps > 0) {
-#pragma unroll
-    for (int s = 0; s < NS - 1; ++s) {
-      issue(s, s);
+    s16x8 af[2][MS], bf[2][NSUB];
+    for_each<0, NS>([&](auto S_) __attribute__((always_inline)) {
+      issue(S_, decltype(S_)::value);
       __builtin_amdgcn_sched_barrier(0);
-    }
-    int s = 0;
-    for (int step = 0; step < steps; ++step) {
-      wait_vmcnt<(NS - 2) * LOADS>();  // this wave's loads of the step have landed
-      __builtin_amdgcn_s_barrier();    // every wave's have; the stage before is free
-      issue(s == 0 ? NS - 1 : s - 1, step + NS - 1);
-      __builtin_amdgcn_sched_barrier(0);
-      const uint8_t* st = lds + s * STAGE;
+      return true;
+    });
+    wait_vmcnt<(NS - 1) * LOADS>();
+    __builtin_amdgcn_s_barrier();
+    fragments(st0, 0, af[0], bf[0]);
+    auto step = [&](auto S_, int i) __attribute__((always_inline)) {
+      constexpr int S = decltype(S_)::value, N = (S + 1) % NS;
+      const uint8_t* st = stage(S_);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s16x8 af[MS], bf[NSUB];
-#pragma unroll
-        for (int mi = 0; mi < MS; ++mi) af[mi] = Loader<TA, BM, NIA>::read(st, (wm * MS + mi) * 32, j, lane);
-#pragma unroll
-        for (int ni = 0; ni < NSUB; ++ni)
-          bf[ni] = Loader<TB, BN, NIB>::read(st + A_BYTES, (wn * NSUB + ni) * 32, j, lane);
-#pragma unroll
-        for (int mi = 0; mi < MS; ++mi)
-#pragma unroll
-          for (int ni = 0; ni < NSUB; ++ni) acc[mi][ni] = mfma32<DT>(af[mi], bf[ni], acc[mi][ni]);
+      for (int j = 0; j < 3; ++j) {
+        fragments(st, j + 1, af[(j + 1) & 1], bf[(j + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(af[j & 1], bf[j & 1]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      s = s + 1 == NS ? 0 : s + 1;
-    }
+      wait_vmcnt<(NS - 2) * LOADS>();       // this wave's loads of the next step have landed
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // and its reads of this stage (lgkmcnt 0)
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      issue(S_, i + NS);
+      fragments(stage(IC<N>{}), 0, af[0], bf[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(af[1], bf[1]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    int i = 0;
+    for (; i + NS <= steps; i += NS)
+      for_each<0, NS>([&](auto S_) __attribute__((always_inline)) {
+        step(S_, i + decltype(S_)::value);
+        return true;
+      });
+    for_each<0, NS - 1>([&](auto S_) __attribute__((always_inline)) {
+      if (i + decltype(S_)::value >= steps) return false;
+      step(S_, i + decltype(S_)::value);
+      return true;
+    });
   }
   wait_vmcnt<0>();  // no load into LDS lands after this
   __syncthreads();
 
   // ---- epilogue: register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
   const int M = prm.a.n;
-  float* rows = (float*)lds + wave * (32 * ROWF);
+  const int place = wave / PER_STAGE;
+  float* rows = (float*)((place == 0 ? st0 : place == 1 ? st1 : place == 2 ? st2 : st3) +
+                         wave % PER_STAGE * ROWS_BYTES);
   const int hh = lane / 32, col = lane % 32;
   constexpr int LPR = GATED ? 4 : 4 * NSUB;  // lanes a row, eight columns each
 #pragma unroll
@@ -598,14 +613,16 @@ __global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restric
 // -------------------------------------------------------------- launchers --
 
 struct Plan {
-  int bm, bn, splits;
+  int tile;  // rows and columns of a tile
+  int splits;
 };
 
 // The tile and the split of k of a product M x N over K
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  Plan p{128, 128, 1};
-  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  Plan p{128, 1};
   const int64_t steps = (K + 63) / 64;
+  if (((M + 255) / 256) * ((N + 255) / 256) >= 160) return Plan{256, 1};
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
   // fewer tiles than CUs: shares of k of at least eight steps
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), steps / 8));
   return p;
@@ -625,15 +642,17 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   const int64_t steps = (K + 63) / 64;
   prm.splits = p.splits;
   prm.k_split = (int)((steps + p.splits - 1) / p.splits) * 64;
-  prm.m_tiles = (a.n + 127) / 128;
+  prm.m_tiles = (a.n + p.tile - 1) / p.tile;
   const int C = split ? N : e.C;
   prm.e.C = C;
-  const int cols = GATED && !split ? 64 : 128;
+  const int cols = GATED && !split ? p.tile / 2 : p.tile;
   prm.n_tiles = (C + cols - 1) / cols;
   prm.group_m = std::min(prm.m_tiles, 8);
   const int64_t total = (int64_t)prm.m_tiles * prm.n_tiles * prm.splits;
   prm.per_xcd = (int)((total + NUM_XCD - 1) / NUM_XCD);
   const dim3 grid((unsigned)(prm.per_xcd * NUM_XCD));
+  if (p.tile == 256)
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 2>, grid, 512, 0, st, prm);
   if (!split) return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
   hipError_t r = launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
   if (r != hipSuccess) return r;
