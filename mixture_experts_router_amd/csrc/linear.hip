@@ -219,8 +219,7 @@ __device__ __forceinline__ void finish8(const LinearEpi& e, int64_t t, int n, fl
 // 16-byte pieces XORed with the row so that a wave's 16-byte reads meet no bank
 // twice); one whose m (n) is contiguous stages 64 rows of BM (BN) values and is
 // read with ds_read_b64_tr_b16, which transposes 4 x 16 blocks on the way into
-// the registers.  There the pieces are XORed so that the four k rows of a read
-// lie in different banks.
+// the registers.
 //
 // Offsets: a descriptor starts at the tile's first element (64-bit), so that
 // offsets within it stay below 2^31; rows, columns and k past the operand's end
@@ -239,9 +238,12 @@ struct Loader {
   const uint16_t* base2;  // GATED: the up rows
   int64_t ld;
 
-  // which piece of k row kr holds logical piece 0: the four rows of a transposed read apart by 32 bytes
+  // Piece p of k row kr lies at place p ^ swizzle(kr): 32 lanes of a transposed
+  // read take 64 bytes of four consecutive rows, which must lie in different
+  // quarters of the 256 bytes of banks (rows of 192 values are 384 bytes, so
+  // every other row is half way round already).
   static __device__ __forceinline__ int swizzle(int kr) {
-    return (((kr & 3) << 1) | (((kr >> 3) & 1) << 3)) & (R / 8 - 1);
+    return R % 128 == 0 ? (kr & 3) << 2 : ((kr >> 1) & 1) << 2;
   }
   // GATED: tile rows run over 32 gate rows from m0 and the 32 up rows `up` further, by turns
   template <bool GATED>
@@ -517,114 +519,141 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
 
 // ------------------------------------------------------- gradient of z ----
 //
-// A workgroup takes `rows` rows; a thread eight columns at a time.  dz (rounded
-// to the operands' 16 bits: the matrix cores' input) is the operand of both
-// products; the sums of bias and row_scale use it unrounded.  Columns from C up
-// to ldz are zero.  Column sums go to part[block][N], joined in order.
+// A workgroup takes g.rows rows and 8 g.across columns (gated: of each half), a
+// thread eight columns of every (256 / g.across)-th row.  dz (rounded to the
+// operands' 16 bits: the matrix cores' input) is the operand of both products;
+// the sums of bias and row_scale use it unrounded and go to
+// part[row block][N] and row_part[column block][T], joined in order.  The last
+// column block writes zeros up to ldz.
 template <int DT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
-  __shared__ float row_sum[4][64];
-  const int lane = lane_id(), wave = wave_id();
+  __shared__ float sums[256][17];
+  __shared__ float row_sum[LINEAR_DZ_ROWS][4];
+  const int tid = threadIdx.x, across = g.across;
   const bool gated = g.act == LIN_SWIGLU;
   const int64_t t0 = (int64_t)blockIdx.x * g.rows;
   const int rows = (int)min((int64_t)g.rows, g.T - t0);
-  if (g.drs)
-    for (int i = threadIdx.x; i < 256; i += 256) row_sum[i / 64][i % 64] = 0.0f;
-  __syncthreads();
-  for (int base = 0; base < g.C; base += 2048) {
-    const int n = base + 8 * (int)threadIdx.x;
-    const int left = g.C - n;
-    const bool on = left > 0;
-    const bool vec = g.vec && left >= 8;
-    float cs[8], cu[8];
+  const int n = 8 * ((int)blockIdx.y * across + tid % across);
+  const int left = g.C - n;
+  const bool vec = g.vec && left >= 8;
+  float cs[8], cu[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) cs[j] = cu[j] = 0.0f;
-    for (int r = 0; r < rows; ++r) {
-      const int64_t t = t0 + r;
-      float d[8], d2[8], dot = 0.0f;
+  for (int j = 0; j < 8; ++j) cs[j] = cu[j] = 0.0f;
+#pragma unroll 2
+  for (int r = tid / across; r < rows; r += 256 / across) {
+    const int64_t t = t0 + r;
+    float dot = 0.0f;
+    if (left > 0) {
+      float d[8], d2[8], z[8], u[8];  // columns past the end: all 0
+      load8<DT>(g.g, g.g_f32, t * g.ldg + n, left, vec, d);
+      if (g.z) load8<DT>(g.z, false, t * g.ldz_in + n, left, vec, z);
+      if (gated) load8<DT>(g.z, false, t * g.ldz_in + g.C + n, left, vec, u);
+      const float rs = g.rs ? g.rs[t] : 1.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = d2[j] = 0.0f;
-      if (on) {
-        load8<DT>(g.g, g.g_f32, t * g.ldg + n, left, vec, d);
-        const float rs = g.rs ? g.rs[t] : 1.0f;
-        float z[8], u[8];  // columns past the end: all 0
-        if (g.z) load8<DT>(g.z, false, t * g.ldz_in + n, left, vec, z);
-        if (gated) load8<DT>(g.z, false, t * g.ldz_in + g.C + n, left, vec, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float gv = g.rs ? d[j] * rs : d[j];
-          float a = 0.0f, slope = 1.0f;
-          if (g.z) a = activate_slope(gated ? LIN_SILU : g.act, z[j], slope);
-          if (gated) {
-            dot += d[j] * (a * u[j]);
-            d2[j] = gv * a;
-            slope *= u[j];
-          } else {
-            dot += d[j] * a;
-          }
-          d[j] = gv * slope;
+      for (int j = 0; j < 8; ++j) {
+        const float gv = g.rs ? d[j] * rs : d[j];
+        float a = 0.0f, slope = 1.0f;
+        if (g.z) a = activate_slope(gated ? LIN_SILU : g.act, z[j], slope);
+        d2[j] = 0.0f;
+        if (gated) {
+          dot += d[j] * (a * u[j]);
+          d2[j] = gv * a;
+          slope *= u[j];
+        } else {
+          dot += d[j] * a;
         }
-        if (g.dz) {
-          store8<DT>(g.dz, false, t * g.ldz + n, left, vec, d);
-          if (gated) store8<DT>(g.dz, false, t * g.ldz + g.C + n, left, vec, d2);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          cs[j] += d[j];
-          cu[j] += d2[j];
-        }
+        d[j] = gv * slope;
+        cs[j] += d[j];
+        cu[j] += d2[j];
       }
-      if (g.drs) {
-        const float s = wave_sum(dot);
-        if (lane == 0) row_sum[wave][r] += s;
+      if (g.dz) {
+        store8<DT>(g.dz, false, t * g.ldz + n, left, vec, d);
+        if (gated) store8<DT>(g.dz, false, t * g.ldz + g.C + n, left, vec, d2);
       }
     }
-    if (g.part && on) {
-      float* p = g.part + (int64_t)blockIdx.x * g.N;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < left) {
-          p[n + j] = cs[j];
-          if (gated) p[g.C + n + j] = cu[j];
-        }
+    if (g.row_part) {  // the threads of a row: 64 at a time of one wave, or fewer
+      for (int o = 1; o < min(across, 64); o <<= 1) dot += lane_read_f(dot, lane_id() ^ o);
+      if (tid % min(across, 64) == 0) row_sum[r][tid % across / 64] = dot;
     }
   }
-  // the padding of dz rows
-  if (g.dz) {
+  if (g.dz && blockIdx.y + 1 == gridDim.y) {
     const int pad = (int)(g.ldz - g.N);
-    for (int i = threadIdx.x; i < rows * pad; i += 256)
-      ((uint16_t*)g.dz)[(t0 + i / pad) * g.ldz + g.N + i % pad] = 0;
+    for (int i = tid; i < rows * pad; i += 256) g.dz[(t0 + i / pad) * g.ldz + g.N + i % pad] = 0;
+  }
+  if (g.part) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sums[tid][j] = cs[j];
+      sums[tid][8 + j] = cu[j];
+    }
   }
   __syncthreads();
-  if (g.drs)
-    for (int r = threadIdx.x; r < rows; r += 256)
-      g.drs[t0 + r] = ((row_sum[0][r] + row_sum[1][r]) + row_sum[2][r]) + row_sum[3][r];
+  if (g.part) {
+    float* p = g.part + (int64_t)blockIdx.x * g.N;
+    for (int i = tid; i < across * 16; i += 256) {
+      const int c = i / 16, j = i % 16;
+      const int m = 8 * ((int)blockIdx.y * across + c) + j % 8;
+      float v = 0.0f;
+      for (int q = c; q < 256; q += across) v += sums[q][j];
+      if (m < g.C && (j < 8 || gated)) p[j < 8 ? m : g.C + m] = v;
+    }
+  }
+  if (g.row_part)
+    for (int r = tid; r < rows; r += 256) {
+      float v = row_sum[r][0];
+      for (int q = 1; q < (across + 63) / 64; ++q) v += row_sum[r][q];
+      g.row_part[(int64_t)blockIdx.y * g.T + t0 + r] = v;
+    }
 }
 
-__global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restrict__ part, int blocks, int N,
-                                                          float* __restrict__ out) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
-  float s = 0.0f;
-  for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * N + n];
-  out[n] = s;
+// out[i] = sum over b of part[b][n], in an order of its own: 16 groups of every
+// 16th b, then the groups.  A workgroup 64 of the n.
+__global__ __launch_bounds__(1024) void linear_sums_kernel(const float* __restrict__ part, int blocks, int64_t n,
+                                                           float* __restrict__ out) {
+  __shared__ float sums[16][64];
+  const int group = threadIdx.x / 64, lane = lane_id();
+  const int64_t i = (int64_t)blockIdx.x * 64 + lane;
+  float v = 0.0f;
+  if (i < n) {
+#pragma unroll 8
+    for (int b = group; b < blocks; b += 16) v += part[(int64_t)b * n + i];
+  }
+  sums[group][lane] = v;
+  __syncthreads();
+  if (group == 0 && i < n) {
+#pragma unroll
+    for (int q = 1; q < 16; ++q) v += sums[q][lane];
+    out[i] = v;
+  }
 }
 
 // -------------------------------------------------------------- launchers --
 
+constexpr int CUS = 256;
+
 struct Plan {
-  int tile;  // rows and columns of a tile
+  int bm, bn;  // rows and columns of a tile
   int splits;
 };
 
-// The tile and the split of k of a product M x N over K
+// The tile and the split of k of a product M x N over K: the least time of the
+// CU with the most tiles, a tile costing its area by how near its waves come to
+// the matrix cores' rate (the smaller the wave's share, the more LDS bytes an
+// MFMA needs).
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
-  Plan p{128, 1};
   const int64_t steps = (K + 63) / 64;
-  if (((M + 255) / 256) * ((N + 255) / 256) >= 160) return Plan{256, 1};
-  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  if (M < 1 || N < 1) return Plan{128, 128, 1};
+  auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  auto cost = [&](int bm, int bn, double each) { return (double)((tiles(bm, bn) + CUS - 1) / CUS) * bm * bn * each; };
+  Plan p{128, 128, 1};
+  double best = cost(128, 128, 1.6);
+  if (steps > 4 && cost(192, 256, 1.1) < best) {
+    p = Plan{192, 256, 1};
+    best = cost(192, 256, 1.1);
+  }
+  if (steps > 4 && cost(256, 256, 1.0) < best) p = Plan{256, 256, 1};
   // fewer tiles than CUs: shares of k of at least eight steps
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), steps / 8));
+  if (p.bm == 128) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(CUS / tiles(128, 128), steps / 8));
   return p;
 }
 
@@ -642,18 +671,24 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   const int64_t steps = (K + 63) / 64;
   prm.splits = p.splits;
   prm.k_split = (int)((steps + p.splits - 1) / p.splits) * 64;
-  prm.m_tiles = (a.n + p.tile - 1) / p.tile;
+  prm.m_tiles = (a.n + p.bm - 1) / p.bm;
   const int C = split ? N : e.C;
   prm.e.C = C;
-  const int cols = GATED && !split ? p.tile / 2 : p.tile;
+  const int cols = GATED && !split ? p.bn / 2 : p.bn;
   prm.n_tiles = (C + cols - 1) / cols;
   prm.group_m = std::min(prm.m_tiles, 8);
   const int64_t total = (int64_t)prm.m_tiles * prm.n_tiles * prm.splits;
   prm.per_xcd = (int)((total + NUM_XCD - 1) / NUM_XCD);
   const dim3 grid((unsigned)(prm.per_xcd * NUM_XCD));
-  if (p.tile == 256)
+  if (p.bm == 256)
     return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 2>, grid, 512, 0, st, prm);
-  if (!split) return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
+  if (p.bm == 192)
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 2>, grid, 512, 0, st, prm);
+  if (!split) {
+    if (steps <= 4)  // two workgroups a CU
+      return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2>, grid, 256, 0, st, prm);
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
+  }
   hipError_t r = launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
   if (r != hipSuccess) return r;
   const int64_t threads = (int64_t)a.n * ((e.C + 7) / 8);
@@ -681,18 +716,23 @@ LinearEpi plain_out(void* out, int64_t ld, int C) {
 
 template <int DT>
 hipError_t backward(const LinearGrad& g, const void* x, int64_t ldx, const void* w, int64_t ldw, int K, void* dx,
-                    int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias, const uint16_t* dz, int64_t ldz,
-                    float* part, hipStream_t st) {
-  if (g.dz || g.part || g.drs) {
-    if (g.T) {
-      const hipError_t r = launch_kernel(linear_dz_kernel<DT>, (unsigned)g.blocks, 256, 0, st, g);
-      if (r != hipSuccess) return r;
-    }
-    if (dbias) {
-      const hipError_t r2 = launch_kernel(linear_bias_kernel, (unsigned)((g.N + 255) / 256), 256, 0, st, g.part,
-                                          g.blocks, g.N, dbias);
-      if (r2 != hipSuccess) return r2;
-    }
+                    int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias, float* drs, const uint16_t* dz,
+                    int64_t ldz, float* part, hipStream_t st) {
+  if (g.T && (g.dz || g.part || g.row_part)) {
+    const hipError_t r = launch_kernel(linear_dz_kernel<DT>, dim3((unsigned)g.blocks, (unsigned)g.column_blocks), 256, 0,
+                                       st, g);
+    if (r != hipSuccess) return r;
+  }
+  auto sums = [&](const float* p, int blocks, int64_t n, float* out) {
+    return launch_kernel(linear_sums_kernel, (unsigned)((n + 63) / 64), 1024, 0, st, p, blocks, n, out);
+  };
+  if (dbias) {
+    const hipError_t r = sums(g.part, g.blocks, g.N, dbias);
+    if (r != hipSuccess) return r;
+  }
+  if (g.T && drs) {
+    const hipError_t r = sums(g.row_part, g.column_blocks, g.T, drs);
+    if (r != hipSuccess) return r;
   }
   if (dx) {
     const Operand a{dz, ldz, (int)g.T}, b{(const uint16_t*)w, ldw, K};
@@ -721,11 +761,11 @@ hipError_t launch_linear(const void* x, int dt, int64_t ldx, int T, const void* 
 }
 
 hipError_t launch_linear_backward(const LinearGrad& g, int dt, const void* x, int64_t ldx, const void* w, int64_t ldw,
-                                  int K, void* dx, int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias,
+                                  int K, void* dx, int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias, float* drs,
                                   const uint16_t* dz, int64_t ldz, float* part, hipStream_t st) {
   return dt == ACT_BF16
-             ? backward<ACT_BF16>(g, x, ldx, w, ldw, K, dx, ldx_out, dw, ldw_out, dbias, dz, ldz, part, st)
-             : backward<ACT_F16>(g, x, ldx, w, ldw, K, dx, ldx_out, dw, ldw_out, dbias, dz, ldz, part, st);
+             ? backward<ACT_BF16>(g, x, ldx, w, ldw, K, dx, ldx_out, dw, ldw_out, dbias, drs, dz, ldz, part, st)
+             : backward<ACT_F16>(g, x, ldx, w, ldw, K, dx, ldx_out, dw, ldw_out, dbias, drs, dz, ldz, part, st);
 }
 
 }  // namespace moe

@@ -374,16 +374,21 @@ bool rows16(const void* p, moe_dtype dt, int64_t ld) {
 }
 
 struct LinearGradLayout {
-  size_t dz, sums, part, total;
+  size_t dz, sums, row_sums, part, total;
   int64_t ldz;
-  int rows, blocks;
+  int rows, blocks, across, column_blocks;
 };
 
-LinearGradLayout linear_grad_layout(int64_t T, int64_t N, int64_t K) {
+// N: rows of W; a gated product has half as many columns, and fewer blocks of them than is reserved
+LinearGradLayout linear_grad_layout(int64_t T, int64_t N, int64_t K, int64_t C) {
   LinearGradLayout L{};
   L.ldz = (N + 7) / 8 * 8;
+  // 16 rows a workgroup, so that a few thousand fill the CUs, and at most 64 threads (512 columns) across
   L.rows = T <= 16384 ? 16 : moe::LINEAR_DZ_ROWS;
   L.blocks = (int)((T + L.rows - 1) / L.rows);
+  L.across = 1;
+  while (L.across < 64 && L.across * 8 < C) L.across *= 2;
+  L.column_blocks = (int)((C + 8 * L.across - 1) / (8 * L.across));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     size_t r = at;
@@ -392,6 +397,7 @@ LinearGradLayout linear_grad_layout(int64_t T, int64_t N, int64_t K) {
   };
   L.dz = take((size_t)(T * L.ldz * 2));
   L.sums = take((size_t)((int64_t)L.blocks * N * 4));
+  L.row_sums = take((size_t)((N + 511) / 512 * T * 4));
   // the two products run one after the other
   L.part = take((size_t)std::max(moe::linear_part_bytes(T, K, N), moe::linear_part_bytes(N, K, T)));
   L.total = at;
@@ -1091,7 +1097,7 @@ moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const
 
 size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t K) {
   if (T < 0 || N < 1 || K < 1) return 0;
-  return linear_grad_layout(T, N, K).total;
+  return linear_grad_layout(T, N, K, N).total;
 }
 
 moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_grad, const void* x, moe_dtype dt,
@@ -1117,7 +1123,7 @@ moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_g
       if (!preact && (dense->act != MOE_ACT_NONE || grad_row_scale)) return MOE_ERR_NULL;
       if (preact && (s = check_matrix(preact, dt, ld_preact, N)) != MOE_OK) return s;
     }
-    const LinearGradLayout L = linear_grad_layout(T, N, K);
+    const LinearGradLayout L = linear_grad_layout(T, N, K, C);
     if (L.total) {
       if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
       if (!aligned16(ws)) return MOE_ERR_ALIGN;
@@ -1137,20 +1143,22 @@ moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_g
     g.rs = row_scale;
     g.dz = direct || !(grad_x || grad_w) || T == 0 ? nullptr : (uint16_t*)(W + L.dz);
     g.ldz = L.ldz;
-    g.drs = grad_row_scale;
     g.part = grad_bias ? (float*)(W + L.sums) : nullptr;
+    g.row_part = grad_row_scale ? (float*)(W + L.row_sums) : nullptr;
     g.T = T;
     g.C = C;
     g.N = N;
     g.act = dense->act;
     g.rows = L.rows;
     g.blocks = L.blocks;
+    g.across = L.across;
+    g.column_blocks = L.column_blocks;
     g.vec = rows16(grad, grad_dt, ld_grad) && (!g.z || rows16(preact, dt, ld_preact)) && (C == N || C % 8 == 0);
     const uint16_t* dz = direct ? (const uint16_t*)grad : (const uint16_t*)(W + L.dz);
     hipStream_t st = (hipStream_t)stream;
     plan_begin(st);
     HIP_TRY(moe::launch_linear_backward(g, (int)dt, x, ldx, dense->w, dense->ldw, K, T ? grad_x : nullptr, ld_grad_x,
-                                        grad_w, ld_grad_w, grad_bias, dz, direct ? ld_grad : L.ldz,
+                                        grad_w, ld_grad_w, grad_bias, grad_row_scale, dz, direct ? ld_grad : L.ldz,
                                         (float*)(W + L.part), st));
     plan_step("linear_backward", st);
     return MOE_OK;
