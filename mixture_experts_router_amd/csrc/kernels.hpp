@@ -201,6 +201,7 @@ struct LinearEpi {
   int C, act;
   bool bias_f32, out_f32;
   bool vec;  // every row of res, out and pre starts 16-byte aligned (gated: the up half of pre too)
+  bool bias_vec;  // bias is 16-byte aligned (gated: its up half too)
 };
 
 // dz = row_scale g act'(z), and the sums of bias and row_scale

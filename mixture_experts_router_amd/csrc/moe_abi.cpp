@@ -1085,6 +1085,7 @@ moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const
     e.out_f32 = out_dt == MOE_F32;
     e.vec = rows16(out, out_dt, ld_out) && (!residual || rows16(residual, out_dt, ld_residual)) &&
             (!preact || (rows16(preact, dt, ld_preact) && (C == N || C % 8 == 0)));
+    e.bias_vec = aligned16(dense->bias) && (C == N || C % 8 == 0);
     hipStream_t st = (hipStream_t)stream;
     plan_begin(st);
     HIP_TRY(moe::launch_linear(x, (int)dt, ldx, T, dense->w, dense->ldw, N, K, e, (float*)ws, st));
