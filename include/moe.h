@@ -544,7 +544,7 @@ typedef struct {
  *   topk_idx  int32 [T, k]
  *   loss fp32 [S], z fp32 [S] (or NULL; MOE_ERR_OPTION with sigmoid scores), prob
  *   fp32 [S, E] (or NULL), counts int32 [S, E], tokens int32 [S] (the n): out
- *   ws        moe_balance_workspace_size(T, E, S) bytes, 16-byte aligned
+ *   ws        moe_balance_workspace_size(T, E, S) bytes (may be 0), 16-byte aligned
  * T == 0 writes zeros (with offsets: they are read).
  */
 size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S);

@@ -467,6 +467,13 @@ def _new(like: torch.Tensor, rows: int, columns: int, dtype):
     return like.new_empty((rows, columns), dtype=dtype)
 
 
+def _vector(like: torch.Tensor, n: int, dtype):
+    """A tensor [n] beside `like`, which is on the current GPU."""
+    if _empty_cuda is not None:
+        return _empty_cuda((n,), (1,), dtype)
+    return like.new_empty(n, dtype=dtype)
+
+
 def _here(t: torch.Tensor, stream) -> bool:
     """Whether `t` is on the current GPU and no other stream is asked for."""
     dev = t.get_device()
@@ -835,16 +842,17 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, score: str = "softm
     dev = logits.get_device()
     pi = _operand(idx, "idx", dev, torch.int32, (T, k))
     o, S = _balance_opts(dev, T, score, offsets, mask)
-    loss = logits.new_empty(S, dtype=torch.float32)
-    z = logits.new_empty(S, dtype=torch.float32) if score == "softmax" else None
+    loss = _vector(logits, S, torch.float32)
+    z = _vector(logits, S, torch.float32) if score == "softmax" else None
     prob = _new(logits, S, E, torch.float32)
     counts = _new(logits, S, E, torch.int32)
-    tokens = logits.new_empty(S, dtype=torch.int32)
+    tokens = _vector(logits, S, torch.int32)
     need = lib().moe_balance_workspace_size(T, E, S)
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=logits.device)
+    ws = _vector(logits, need, torch.uint8) if need else None
     _check(lib().moe_balance_loss(logits.data_ptr(), code, ld, T, E, k, pi, o, loss.data_ptr(),
                                   None if z is None else z.data_ptr(), prob.data_ptr(), counts.data_ptr(),
-                                  tokens.data_ptr(), ws.data_ptr(), ws.numel(), _current(dev)), "moe_balance_loss")
+                                  tokens.data_ptr(), None if ws is None else ws.data_ptr(), need, _current(dev)),
+           "moe_balance_loss")
     r = dict(loss=loss, prob=prob, counts=counts, tokens=tokens)
     if z is not None:
         r["z"] = z
@@ -991,7 +999,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
         ldo = _out_rows(out, "out", dev, odt, (T, C))
     z = _new(x, T, N, dtype) if want_preact else None
     need = lib().moe_linear_workspace_size(T, N, K)
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    ws = _vector(x, need, torch.uint8) if need else None
     _check(lib().moe_linear(x.data_ptr(), code, ldx, T, CDense(w.data_ptr(), ldw, pb, bcode, N, K, kind), pr, ldr, ps,
                             None if z is None else z.data_ptr(), N, out.data_ptr(), ldo, _TYPES[odt],
                             None if ws is None else ws.data_ptr(), need, _current(dev)), "moe_linear")
@@ -1035,10 +1043,10 @@ def linear_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, act
     r = {}
     for n in want:
         r[n] = (_new(x, T, K, dtype) if n == "x" else _new(x, N, K, dtype) if n == "w" else
-                torch.empty(N if n == "bias" else T, dtype=torch.float32, device=x.device))
+                _vector(x, N if n == "bias" else T, torch.float32))
     at = lambda n: r[n].data_ptr() if n in r else None  # noqa: E731
     need = lib().moe_linear_backward_workspace_size(T, N, K)
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    ws = _vector(x, max(need, 256), torch.uint8)
     _check(lib().moe_linear_backward(grad.data_ptr(), gcode, ldg, x.data_ptr(), code, ldx, T,
                                      CDense(w.data_ptr(), ldw, None, code, N, K, kind), pz, ldz, ps, at("x"), K,
                                      at("w"), K, at("bias"), at("row_scale"), ws.data_ptr(), ws.numel(),

@@ -22,17 +22,23 @@ namespace moe {
 namespace {
 
 constexpr float SCORE_EPS = 1e-20f;
-constexpr int PART_THREADS = 512;  // 32 tokens at a time, sixteen lanes a token
-constexpr int JOIN_THREADS = 1024;
 
 // Sums of one chunk and sequence: prob sums, counts (each E rounded up to 4), z sum, tokens
 __host__ __device__ constexpr int slot_words(int E) { return 2 * ((E + 3) / 4 * 4) + 4; }
 
-// tokens of a chunk: at most 1024 chunks
+// tokens of a chunk: at most 512 chunks, two workgroups a CU
 int chunk_tokens(int T) {
-  const int64_t c = ((int64_t)T + 1023) / 1024;
+  const int64_t c = ((int64_t)T + 511) / 512;
   return (int)((c + 31) / 32 * 32);
 }
+
+// One launch, a workgroup a sequence, where that is at most a few rounds of 64
+// tokens: nothing is known of the sequences here but their number and T.
+bool whole_sequences(int T, int S) { return T <= 512 || (T <= 2048 && S >= 4); }
+
+// exp(x): the hardware's exponential of x / ln 2, whose rounding is the larger
+// part of the error, |x| 2^-24 (expf takes twice the instructions)
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 template <int LT>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
@@ -86,10 +92,12 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t at, int E, 
   }
 }
 
-// Probabilities of a row in place of its logits; the softmax's lse (0 for a
-// row that masks everything), or with sigmoid scores 1 - s in q
-template <int NB, bool SOFTMAX>
-__device__ __forceinline__ float probabilities(f32x4 (&l)[NB], f32x4 (&q)[NB]) {
+// Scores of a row in place of its logits, without their sum's division: the
+// exponentials over their maximum, or the sigmoids (GRAD: 1 - s in q).  inv:
+// what makes them probabilities.  Returns the softmax's lse (0 for a row that
+// masks everything).  A masked expert's score is 0 also beside NaN.
+template <int NB, bool SOFTMAX, bool GRAD>
+__device__ __forceinline__ float scores(f32x4 (&l)[NB], f32x4 (&q)[NB], float& inv) {
   float sum = 0.0f;
   if constexpr (SOFTMAX) {
     float m = -INFINITY;
@@ -100,16 +108,12 @@ __device__ __forceinline__ float probabilities(f32x4 (&l)[NB], f32x4 (&q)[NB]) {
     for (int c = 0; c < NB; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float e = l[c][j] == -INFINITY ? 0.0f : expf(l[c][j] - m);
+        const float e = l[c][j] == -INFINITY ? 0.0f : exp_fast(l[c][j] - m);
         l[c][j] = e;
         sum += e;
       }
     sum = sum16(sum);
-    const float inv = 1.0f / sum;
-#pragma unroll
-    for (int c = 0; c < NB; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) l[c][j] = l[c][j] != 0.0f ? l[c][j] * inv : 0.0f;
+    inv = 1.0f / sum;
     return sum == 0.0f ? 0.0f : m + logf(sum);
   } else {
 #pragma unroll
@@ -117,17 +121,13 @@ __device__ __forceinline__ float probabilities(f32x4 (&l)[NB], f32x4 (&q)[NB]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float v = l[c][j];
-        const float s = 1.0f / (1.0f + expf(-v));
-        q[c][j] = 1.0f / (1.0f + expf(v));
+        const float s = __builtin_amdgcn_rcpf(1.0f + exp_fast(-v));  // exactly 0 at -inf
+        if constexpr (GRAD) q[c][j] = __builtin_amdgcn_rcpf(1.0f + exp_fast(v));
         l[c][j] = s;
         sum += s;
       }
     sum = sum16(sum) + SCORE_EPS;
-    const float inv = 1.0f / sum;
-#pragma unroll
-    for (int c = 0; c < NB; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) l[c][j] = l[c][j] != 0.0f ? l[c][j] * inv : 0.0f;
+    inv = 1.0f / sum;
     return 0.0f;
   }
 }
@@ -143,87 +143,164 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_
   return lo;
 }
 
+// What a workgroup sums of consecutive tokens
+template <int WAVES>
+struct Sums {
+  float prob[WAVES][256];
+  int hist[256];
+  float z[WAVES];
+  int n[WAVES];
+};
+
+// The tokens [from, to): sums of the probabilities by wave, counts, z and live
+// tokens.  Sixteen lanes a token, the next token's logits loaded before the
+// present one's are used.  Ends with a barrier.
+template <int NB, int LT, bool SOFTMAX, int WAVES>
+__device__ __forceinline__ void sum_tokens(const void* logits, int64_t ld, int vec, int E, int k, const int32_t* idx,
+                                           const uint8_t* mask, int64_t from, int64_t to, Sums<WAVES>& out) {
+  constexpr int THREADS = 64 * WAVES, ROWS = 4 * WAVES;
+  const int tid = threadIdx.x, lane = lane_id(), wave = wave_id(), i16 = lane % 16;
+  if (tid < 256) out.hist[tid] = 0;
+  int64_t t = from + tid / 16;
+  bool live = t < to && (!mask || mask[t] != 0);
+  f32x4 p[NB], q[NB], next[NB];
+  load_row<LT, NB>(logits, t * ld, E, vec, live, i16, next);
+  __syncthreads();
+  for (int64_t i = from * k + tid; i < to * k; i += THREADS) {
+    const int e = idx[i];
+    if (e >= 0 && e < E && (!mask || mask[i / k] != 0)) atomicAdd(&out.hist[e], 1);
+  }
+  f32x4 acc[NB];
+#pragma unroll
+  for (int c = 0; c < NB; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float za = 0.0f;
+  int n = 0;
+  for (int64_t t0 = from; t0 < to; t0 += ROWS) {
+    n += live;
+#pragma unroll
+    for (int c = 0; c < NB; ++c) p[c] = next[c];
+    t += ROWS;
+    live = t < to && (!mask || mask[t] != 0);
+    load_row<LT, NB>(logits, t * ld, E, vec, live, i16, next);
+    float inv;
+    const float lse = scores<NB, SOFTMAX, false>(p, q, inv);
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[c][j] += p[c][j] != 0.0f ? p[c][j] * inv : 0.0f;
+    za += lse * lse;
+  }
+  // the four rows of a wave
+#pragma unroll
+  for (int c = 0; c < NB; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v = acc[c][j];
+      v += lane_read_f(v, lane ^ 16);
+      v += lane_read_f(v, lane ^ 32);
+      if (lane < 16) out.prob[wave][64 * c + 4 * i16 + j] = v;
+    }
+  za += lane_read_f(za, lane ^ 16);
+  za += lane_read_f(za, lane ^ 32);
+  n += __shfl_xor(n, 16, WAVE);
+  n += __shfl_xor(n, 32, WAVE);
+  if (lane == 0) {
+    out.z[wave] = za;
+    out.n[wave] = n;
+  }
+  __syncthreads();
+}
+
+struct BalanceOut {
+  float* loss;
+  float* z;
+  float* prob;
+  int32_t* counts;
+  int32_t* tokens;
+};
+
+// Results of sequence s from its sums: thread e has expert e's (0 past E).
+// Every thread calls it; means and the loss's sum in 64 bits.
+__device__ __forceinline__ void finish_sequence(const BalanceOut& o, int s, int E, int k, float prob, int count,
+                                                double z, int n, double (&part)[4]) {
+  const int tid = threadIdx.x;
+  if (tid < 256) {
+    double d = 0.0;
+    if (tid < E) {
+      const double mean = n ? (double)prob / n : 0.0;
+      if (o.prob) o.prob[(int64_t)s * E + tid] = (float)mean;
+      o.counts[(int64_t)s * E + tid] = count;
+      d = count ? (double)count * mean : 0.0;
+    }
+    for (int i = 1; i < 64; i <<= 1) d += __shfl_xor(d, i, WAVE);
+    if (tid % 64 == 0) part[tid / 64] = d;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    o.loss[s] = n ? (float)((((part[0] + part[1]) + part[2]) + part[3]) * E / ((double)k * n)) : 0.0f;
+    if (o.z) o.z[s] = n ? (float)(z / n) : 0.0f;
+    o.tokens[s] = n;
+  }
+}
+
+// A workgroup a sequence
+template <int NB, int LT, bool SOFTMAX>
+__global__ __launch_bounds__(1024) void balance_whole_kernel(const void* __restrict__ logits, int64_t ld, int vec,
+                                                             int T, int E, int k, const int32_t* __restrict__ idx,
+                                                             BalanceDev b, BalanceOut o) {
+  __shared__ Sums<16> sums;
+  __shared__ double part[4];
+  const int s = blockIdx.x, tid = threadIdx.x;
+  int64_t from = 0, to = T;
+  if (b.offsets) {
+    from = max((int64_t)0, (int64_t)b.offsets[s]);
+    to = min((int64_t)T, (int64_t)b.offsets[s + 1]);
+  }
+  sum_tokens<NB, LT, SOFTMAX, 16>(logits, ld, vec, E, k, idx, b.mask, from, to, sums);
+  float prob = 0.0f;
+  double z = 0.0;
+  int n = 0;
+  if (tid < E)
+    for (int w = 0; w < 16; ++w) prob += sums.prob[w][tid];
+  for (int w = 0; w < 16; ++w) {
+    z += sums.z[w];
+    n += sums.n[w];
+  }
+  finish_sequence(o, s, E, k, prob, tid < E ? sums.hist[tid] : 0, z, n, part);
+}
+
 // A workgroup sums the chunk [lo, hi) of tokens, each sequence in it into a
 // slot of its own: chunk c and sequence s meet at most once on the way
 // through both, so c + s names the slot.
 template <int NB, int LT, bool SOFTMAX>
-__global__ __launch_bounds__(PART_THREADS) void balance_part_kernel(const void* __restrict__ logits, int64_t ld,
-                                                                    int vec, int T, int E, int k,
-                                                                    const int32_t* __restrict__ idx, BalanceDev b,
-                                                                    int chunk, float* __restrict__ slots) {
-  __shared__ float psum[PART_THREADS / 64][256];
-  __shared__ int hist[256];
-  __shared__ float zsum[PART_THREADS / 64];
-  __shared__ int nsum[PART_THREADS / 64];
-  const int tid = threadIdx.x, lane = lane_id(), wave = wave_id(), i16 = lane % 16;
+__global__ __launch_bounds__(512) void balance_part_kernel(const void* __restrict__ logits, int64_t ld, int vec, int T,
+                                                           int E, int k, const int32_t* __restrict__ idx, BalanceDev b,
+                                                           int chunk, float* __restrict__ slots) {
+  __shared__ Sums<8> sums;
+  const int tid = threadIdx.x;
   const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min((int64_t)T, lo + chunk);
   const int words = slot_words(E), padded = (E + 3) / 4 * 4;
-
   int s = b.offsets ? sequence_of(b.offsets, b.S, lo) : 0;
   for (; s < b.S; ++s) {
     const int64_t from = b.offsets ? max(lo, (int64_t)b.offsets[s]) : lo;
     const int64_t to = b.offsets ? min(hi, (int64_t)b.offsets[s + 1]) : hi;
     if (from >= hi) break;
     if (from >= to) continue;
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-
-    f32x4 acc[NB];
-#pragma unroll
-    for (int c = 0; c < NB; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float za = 0.0f;
-    int n = 0;
-    for (int64_t t0 = from; t0 < to; t0 += PART_THREADS / 16) {
-      const int64_t t = t0 + tid / 16;
-      const bool live = t < to && (!b.mask || b.mask[t] != 0);
-      f32x4 p[NB], q[NB];
-      load_row<LT, NB>(logits, t * ld, E, vec, live, i16, p);
-      const float lse = probabilities<NB, SOFTMAX>(p, q);
-#pragma unroll
-      for (int c = 0; c < NB; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[c][j] += p[c][j];
-      za += lse * lse;
-      n += live;
-    }
-    for (int64_t i = from * k + tid; i < to * k; i += PART_THREADS) {
-      const int e = idx[i];
-      if (e >= 0 && e < E && (!b.mask || b.mask[i / k] != 0)) atomicAdd(&hist[e], 1);
-    }
-
-    // the four rows of a wave, then the waves in order
-#pragma unroll
-    for (int c = 0; c < NB; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float v = acc[c][j];
-        v += lane_read_f(v, lane ^ 16);
-        v += lane_read_f(v, lane ^ 32);
-        if (lane < 16) psum[wave][64 * c + 4 * i16 + j] = v;
-      }
-    za += lane_read_f(za, lane ^ 16);
-    za += lane_read_f(za, lane ^ 32);
-    n += __shfl_xor(n, 16, WAVE);
-    n += __shfl_xor(n, 32, WAVE);
-    if (lane == 0) {
-      zsum[wave] = za;
-      nsum[wave] = n;
-    }
-    __syncthreads();
+    sum_tokens<NB, LT, SOFTMAX, 8>(logits, ld, vec, E, k, idx, b.mask, from, to, sums);
     float* slot = slots + ((int64_t)blockIdx.x + s) * words;
-    if (tid < E) {
+    if (tid < padded) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < PART_THREADS / 64; ++w) v += psum[w][tid];
+      for (int w = 0; w < 8; ++w) v += sums.prob[w][tid];
       slot[tid] = v;
-      ((int*)slot)[padded + tid] = hist[tid];
+      ((int*)slot)[padded + tid] = sums.hist[tid];
     }
     if (tid == 0) {
       float v = 0.0f;
       int m = 0;
-      for (int w = 0; w < PART_THREADS / 64; ++w) {
-        v += zsum[w];
-        m += nsum[w];
+      for (int w = 0; w < 8; ++w) {
+        v += sums.z[w];
+        m += sums.n[w];
       }
       slot[2 * padded] = v;
       ((int*)slot)[2 * padded + 1] = m;
@@ -232,18 +309,16 @@ __global__ __launch_bounds__(PART_THREADS) void balance_part_kernel(const void* 
   }
 }
 
-// A workgroup a sequence: its slots in order, then the loss
-__global__ __launch_bounds__(JOIN_THREADS) void balance_join_kernel(const float* __restrict__ slots, int T, int E,
-                                                                    int k, BalanceDev b, int chunk,
-                                                                    float* __restrict__ loss, float* __restrict__ z,
-                                                                    float* __restrict__ prob,
-                                                                    int32_t* __restrict__ counts,
-                                                                    int32_t* __restrict__ tokens) {
-  __shared__ float psum[4][256];
-  __shared__ int csum[4][256];
-  __shared__ double dsum[4];
-  __shared__ int n_all;
-  const int s = blockIdx.x, tid = threadIdx.x, e = tid % 256, g = tid / 256;
+// A workgroup a sequence: its slots in order of the sixteen waves' shares, four
+// experts a lane
+__global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restrict__ slots, int T, int E, int k,
+                                                            BalanceDev b, int chunk, BalanceOut o) {
+  __shared__ f32x4 psum[16][64];
+  __shared__ int csum[16][256];
+  __shared__ double zsum[16];
+  __shared__ int nsum[16];
+  __shared__ double part[4];
+  const int s = blockIdx.x, tid = threadIdx.x, lane = lane_id(), wave = wave_id();
   const int words = slot_words(E), padded = (E + 3) / 4 * 4;
   int64_t from = 0, to = T;
   if (b.offsets) {
@@ -251,119 +326,146 @@ __global__ __launch_bounds__(JOIN_THREADS) void balance_join_kernel(const float*
     to = min((int64_t)T, (int64_t)b.offsets[s + 1]);
   }
   const int64_t c0 = from / chunk, c1 = from < to ? (to - 1) / chunk + 1 : c0;
-  float v = 0.0f;
-  int c = 0;
-  if (e < E)
-    for (int64_t i = c0 + g; i < c1; i += 4) {
-      const float* slot = slots + (i + s) * words;
-      v += slot[e];
-      c += ((const int*)slot)[padded + e];
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  int c[4] = {0, 0, 0, 0};
+  if (4 * lane < E) {
+#pragma unroll 8
+    for (int64_t i = c0 + wave; i < c1; i += 16) {
+      const float* slot = slots + (i + s) * words + 4 * lane;
+      const f32x4 a = *(const f32x4*)slot;
+      const u32x4 h = *(const u32x4*)(slot + padded);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] += a[j];
+        c[j] += (int)h[j];
+      }
     }
-  psum[g][e] = v;
-  csum[g][e] = c;
+  }
+  psum[wave][lane] = v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) csum[wave][4 * lane + j] = c[j];
   double zs = 0.0;
   int n = 0;
-  if (tid < 64) {
-    for (int64_t i = c0 + tid; i < c1; i += 64) {
-      const float* slot = slots + (i + s) * words;
-      zs += slot[2 * padded];
-      n += ((const int*)slot)[2 * padded + 1];
-    }
-    for (int o = 1; o < 64; o <<= 1) {
-      zs += __shfl_xor(zs, o, WAVE);
-      n += __shfl_xor(n, o, WAVE);
-    }
-    if (tid == 0) {
-      tokens[s] = n;
-      if (z) z[s] = n ? (float)(zs / n) : 0.0f;
-    }
+  for (int64_t i = c0 + tid; i < c1; i += 1024) {
+    const float* slot = slots + (i + s) * words + 2 * padded;
+    zs += slot[0];
+    n += ((const int*)slot)[1];
   }
-  if (tid == 0) n_all = n;
-  __syncthreads();
-  n = n_all;
-  double d = 0.0;
-  if (tid < 256) {
-    const float total = ((psum[0][tid] + psum[1][tid]) + psum[2][tid]) + psum[3][tid];
-    const int cnt = csum[0][tid] + csum[1][tid] + csum[2][tid] + csum[3][tid];
-    if (tid < E) {
-      const double mean = n ? (double)total / n : 0.0;
-      if (prob) prob[(int64_t)s * E + tid] = (float)mean;
-      counts[(int64_t)s * E + tid] = cnt;
-      d = cnt ? (double)cnt * mean : 0.0;
-    }
-    for (int o = 1; o < 64; o <<= 1) d += __shfl_xor(d, o, WAVE);
-    if (tid % 64 == 0) dsum[tid / 64] = d;
+  for (int i = 1; i < 64; i <<= 1) {
+    zs += __shfl_xor(zs, i, WAVE);
+    n += __shfl_xor(n, i, WAVE);
+  }
+  if (lane == 0) {
+    zsum[wave] = zs;
+    nsum[wave] = n;
   }
   __syncthreads();
-  if (tid == 0) loss[s] = n ? (float)((((dsum[0] + dsum[1]) + dsum[2]) + dsum[3]) * E / ((double)k * n)) : 0.0f;
+  float prob = 0.0f;
+  int count = 0;
+  zs = 0.0;
+  n = 0;
+  if (tid < E)
+    for (int w = 0; w < 16; ++w) {
+      prob += ((const float*)psum[w])[tid];
+      count += csum[w][tid];
+    }
+  for (int w = 0; w < 16; ++w) {
+    zs += zsum[w];
+    n += nsum[w];
+  }
+  finish_sequence(o, s, E, k, prob, count, zs, n, part);
 }
 
+// The gradient.  A workgroup takes `rows` tokens, sixteen at a time and the next
+// ones' logits loaded before; a row of lanes keeps its sequence's slopes while
+// its tokens stay in it.  Bound by the logits read and the gradient written.
 template <int NB, int LT, bool SOFTMAX>
 __global__ __launch_bounds__(256) void balance_backward_kernel(const void* __restrict__ logits, int64_t ld, int vec,
-                                                               int T, int E, int k, BalanceDev b,
+                                                               int T, int E, int k, BalanceDev b, int rows,
                                                                const int32_t* __restrict__ counts,
                                                                const int32_t* __restrict__ tokens,
                                                                const float* __restrict__ grad_loss,
                                                                const float* __restrict__ grad_z,
                                                                void* __restrict__ out, int64_t ldo, int vec_out) {
   const int lane = lane_id(), i16 = lane % 16;
-  const int64_t t = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
-  if (t >= T) return;
-  int s = 0;
-  bool live = !b.mask || b.mask[t] != 0;
-  if (b.offsets && live) {
-    s = sequence_of(b.offsets, b.S, t);
-    live = s < b.S && b.offsets[s] <= t;
-  }
-  int n = 0;
-  if (live) n = tokens[s];
-  live = live && n > 0;
-  f32x4 p[NB], q[NB], g[NB];
-  load_row<LT, NB>(logits, t * ld, E, vec, live, i16, p);
-  const float nf = (float)n;
-  const float slope = live && grad_loss ? grad_loss[s] * ((float)E / ((float)k * nf * nf)) : 0.0f;
+  int64_t t = (int64_t)blockIdx.x * rows + threadIdx.x / 16;
+  const int64_t end = min((int64_t)T, (int64_t)(blockIdx.x + 1) * rows);
+  f32x4 p[NB], q[NB], g[NB], next[NB];
+  bool on = t < end && (!b.mask || b.mask[t] != 0);
+  load_row<LT, NB>(logits, t * ld, E, vec, on, i16, next);
+  int s = -1;
+  int64_t s_from = 0, s_to = b.offsets ? 0 : T;  // tokens of the sequence whose slopes are held
+  float slope = 0.0f, zslope = 0.0f;
+  if (!b.offsets) s = 0;
+  bool fresh = !b.offsets;
+  for (; t < end; t += 16) {
+    const bool was = on;
 #pragma unroll
-  for (int c = 0; c < NB; ++c)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int x = 64 * c + 4 * i16 + j;
-      g[c][j] = live && x < E ? slope * (float)counts[(int64_t)s * E + x] : 0.0f;
+    for (int c = 0; c < NB; ++c) p[c] = next[c];
+    const int64_t t2 = t + 16;
+    on = t2 < end && (!b.mask || b.mask[t2] != 0);
+    load_row<LT, NB>(logits, t2 * ld, E, vec, on, i16, next);
+    if (b.offsets && (t >= s_to || s < 0)) {
+      s = sequence_of(b.offsets, b.S, t);
+      s_from = s < b.S ? b.offsets[s] : (int64_t)T;
+      s_to = s < b.S ? b.offsets[s + 1] : (int64_t)T;
+      fresh = true;
     }
-  const float lse = probabilities<NB, SOFTMAX>(p, q);
-  float dot = 0.0f;
+    if (fresh) {
+      const int n = s < b.S ? tokens[s] : 0;
+      const float nf = (float)n;
+      slope = n > 0 && grad_loss ? grad_loss[s] * ((float)E / ((float)k * nf * nf)) : 0.0f;
+      zslope = SOFTMAX && n > 0 && grad_z ? grad_z[s] * (2.0f / nf) : 0.0f;
 #pragma unroll
-  for (int c = 0; c < NB; ++c)
+      for (int c = 0; c < NB; ++c)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dot += g[c][j] * p[c][j];
-  dot = sum16(dot);
-  const float add = SOFTMAX && live && grad_z ? grad_z[s] * (2.0f / nf) * lse - dot : -dot;
-#pragma unroll
-  for (int c = 0; c < NB; ++c) {
-    const int x = 64 * c + 4 * i16;
-    if (x >= E) continue;
-    f32x4 v;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float d = p[c][j] * (g[c][j] + add);
-      if (!SOFTMAX) d *= q[c][j];
-      v[j] = live && p[c][j] != 0.0f ? d : 0.0f;
-    }
-    if (vec_out) {
-      if constexpr (LT == GATE_F32) {
-        __builtin_nontemporal_store(v, (f32x4*)((float*)out + t * ldo + x));
-      } else {
-        u32x2 o;
-        o.x = (uint32_t)f32_to_act_bits(v.x, LT) | (uint32_t)f32_to_act_bits(v.y, LT) << 16;
-        o.y = (uint32_t)f32_to_act_bits(v.z, LT) | (uint32_t)f32_to_act_bits(v.w, LT) << 16;
-        __builtin_nontemporal_store(o, (u32x2*)((uint16_t*)out + t * ldo + x));
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (x + j < E) {
-          if constexpr (LT == GATE_F32) ((float*)out)[t * ldo + x + j] = v[j];
-          else ((uint16_t*)out)[t * ldo + x + j] = f32_to_act_bits(v[j], LT);
+        for (int j = 0; j < 4; ++j) {
+          const int x = 64 * c + 4 * i16 + j;
+          g[c][j] = n > 0 && x < E ? slope * (float)counts[(int64_t)s * E + x] : 0.0f;
         }
+      fresh = false;
+    }
+    const bool live = was && t >= s_from && t < s_to;
+    float inv;
+    const float lse = scores<NB, SOFTMAX, true>(p, q, inv);
+    float dot = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[c][j] = p[c][j] != 0.0f ? p[c][j] * inv : 0.0f;
+        dot += g[c][j] * p[c][j];
+      }
+    dot = sum16(dot);
+    const float add = zslope * lse - dot;
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+      const int x = 64 * c + 4 * i16;
+      if (x >= E) continue;
+      f32x4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float d = p[c][j] * (g[c][j] + add);
+        if (!SOFTMAX) d *= q[c][j];
+        v[j] = live && p[c][j] != 0.0f ? d : 0.0f;
+      }
+      if (vec_out) {
+        if constexpr (LT == GATE_F32) {
+          __builtin_nontemporal_store(v, (f32x4*)((float*)out + t * ldo + x));
+        } else {
+          u32x2 o;
+          o.x = (uint32_t)f32_to_act_bits(v.x, LT) | (uint32_t)f32_to_act_bits(v.y, LT) << 16;
+          o.y = (uint32_t)f32_to_act_bits(v.z, LT) | (uint32_t)f32_to_act_bits(v.w, LT) << 16;
+          __builtin_nontemporal_store(o, (u32x2*)((uint16_t*)out + t * ldo + x));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (x + j < E) {
+            if constexpr (LT == GATE_F32) ((float*)out)[t * ldo + x + j] = v[j];
+            else ((uint16_t*)out)[t * ldo + x + j] = f32_to_act_bits(v[j], LT);
+          }
+      }
     }
   }
 }
@@ -394,7 +496,7 @@ hipError_t dispatch(int E, int lt, int score, F&& go) {
 }  // namespace
 
 int64_t balance_ws_bytes(int T, int E, int S) {
-  if (T == 0) return 0;
+  if (whole_sequences(T, S)) return 0;
   const int chunk = chunk_tokens(T);
   return (((int64_t)T + chunk - 1) / chunk + S) * slot_words(E) * 4;
 }
@@ -402,30 +504,34 @@ int64_t balance_ws_bytes(int T, int E, int S) {
 hipError_t launch_balance(const void* logits, int lt, int64_t ld, int T, int E, int k, const int32_t* idx,
                           const BalanceDev& b, float* loss, float* z, float* prob, int32_t* counts, int32_t* tokens,
                           void* ws, hipStream_t st) {
-  const int chunk = T ? chunk_tokens(T) : 1;
-  if (T) {
-    const int vec = rows_vec(logits, lt, E, ld);
-    const hipError_t r = dispatch(E, lt, b.score, [&](auto nb, auto l, auto softmax) {
-      constexpr int NB = decltype(nb)::value, LT = decltype(l)::value;
-      constexpr bool SM = decltype(softmax)::value;
-      return launch_kernel(balance_part_kernel<NB, LT, SM>, (unsigned)((T + chunk - 1) / chunk), PART_THREADS, 0, st,
-                           logits, ld, vec, T, E, k, idx, b, chunk, (float*)ws);
-    });
-    if (r != hipSuccess) return r;
-  }
-  return launch_kernel(balance_join_kernel, (unsigned)b.S, JOIN_THREADS, 0, st, (const float*)ws, T, E, k, b, chunk,
-                       loss, z, prob, counts, tokens);
+  const int vec = rows_vec(logits, lt, E, ld);
+  const BalanceOut o{loss, z, prob, counts, tokens};
+  const bool whole = whole_sequences(T, b.S);
+  const int chunk = whole ? 1 : chunk_tokens(T);
+  const hipError_t r = dispatch(E, lt, b.score, [&](auto nb, auto l, auto softmax) {
+    constexpr int NB = decltype(nb)::value, LT = decltype(l)::value;
+    constexpr bool SM = decltype(softmax)::value;
+    if (whole)
+      return launch_kernel(balance_whole_kernel<NB, LT, SM>, (unsigned)b.S, 1024, 0, st, logits, ld, vec, T, E, k, idx,
+                           b, o);
+    return launch_kernel(balance_part_kernel<NB, LT, SM>, (unsigned)((T + (int64_t)chunk - 1) / chunk), 512, 0, st,
+                         logits, ld, vec, T, E, k, idx, b, chunk, (float*)ws);
+  });
+  if (r != hipSuccess || whole) return r;
+  return launch_kernel(balance_join_kernel, (unsigned)b.S, 1024, 0, st, (const float*)ws, T, E, k, b, chunk, o);
 }
 
 hipError_t launch_balance_backward(const void* logits, int lt, int64_t ld, int T, int E, int k, const BalanceDev& b,
                                    const int32_t* counts, const int32_t* tokens, const float* grad_loss,
                                    const float* grad_z, void* out, int64_t ldo, hipStream_t st) {
   const int vec = rows_vec(logits, lt, E, ld), vec_out = rows_vec(out, lt, E, ldo);
+  // 16 tokens a workgroup until there are four workgroups a CU, then up to 64
+  const int rows = (int)std::min<int64_t>(64, std::max<int64_t>(16, ((int64_t)T / 1024 + 15) / 16 * 16));
   return dispatch(E, lt, b.score, [&](auto nb, auto l, auto softmax) {
     constexpr int NB = decltype(nb)::value, LT = decltype(l)::value;
     constexpr bool SM = decltype(softmax)::value;
-    return launch_kernel(balance_backward_kernel<NB, LT, SM>, (unsigned)(((int64_t)T + 15) / 16), 256, 0, st, logits,
-                         ld, vec, T, E, k, b, counts, tokens, grad_loss, grad_z, out, ldo, vec_out);
+    return launch_kernel(balance_backward_kernel<NB, LT, SM>, (unsigned)(((int64_t)T + rows - 1) / rows), 256, 0, st,
+                         logits, ld, vec, T, E, k, b, rows, counts, tokens, grad_loss, grad_z, out, ldo, vec_out);
   });
 }
 

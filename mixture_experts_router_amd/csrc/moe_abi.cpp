@@ -992,8 +992,9 @@ moe_status moe_balance_loss(const void* logits, moe_dtype lt, int64_t ld, int32_
     if (!aligned_to(logits, lt) || !aligned4(topk_idx) || !aligned4(loss) || !aligned4(z) || !aligned4(prob) ||
         !aligned4(counts) || !aligned4(tokens))
       return MOE_ERR_ALIGN;
-    if (T != 0) {
-      if (!ws || ws_bytes < moe_balance_workspace_size(T, E, b.S)) return MOE_ERR_WORKSPACE;
+    const size_t need = moe_balance_workspace_size(T, E, b.S);
+    if (need) {
+      if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
       if (!aligned16(ws)) return MOE_ERR_ALIGN;
     }
     DevProps props;

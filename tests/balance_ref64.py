@@ -1,10 +1,11 @@
 """The balance loss, the experts' counts and the gradient in 64 bits, sequence by sequence, with bounds of the kernels'
 fp32 error.
 
-U = 2^-24.  A probability: the exponent's difference is off by at most U |l - m| (|l - m| <= 20 in the tests, smaller
-probabilities weigh nothing), expf and the division a few U, its sum of E <= 256 positive terms at most 24 U (sixteen
-a lane, then four steps): 64 U of p in all.  A sum over tokens of positive terms adds U for each step of its order: at
-most T / 32 + 300.  log and the logsumexp: 64 U from the sum, and 3 U |lse| from its own roundings.
+U = 2^-24.  A probability: the exponent's difference, and its product with 1 / ln 2, are off by at most U |l - m| each
+(|l - m| <= 20 in the tests, smaller probabilities weigh nothing), the exponential and the division by 2 U each, its
+sum of E <= 256 positive terms by 24 U (sixteen a lane, then four steps) beside its terms' own 42 U, weighted by p: 128 U
+of p in all.  A sum over tokens of positive terms adds U for each step of its order: at
+most T / 32 + 300.  log and the logsumexp: 66 U from the sum, and 3 U |lse| from its own roundings.
 """
 import numpy as np
 
@@ -48,7 +49,7 @@ def balance(l, idx, score, offsets=None, mask=None):
     r = dict(loss=np.zeros(S), z=np.zeros(S), prob=np.zeros((S, E)), counts=np.zeros((S, E), np.int32),
              tokens=np.zeros(S, np.int32))
     b = dict(loss=np.zeros(S), z=np.zeros(S), prob=np.zeros((S, E)))
-    steps = (T / 32 + 300 + 64) * U
+    steps = (T / 32 + 300 + 128) * U
     for s, at in enumerate(rows):
         n = len(at)
         if not n:
@@ -61,7 +62,7 @@ def balance(l, idx, score, offsets=None, mask=None):
         r["z"][s] = (lse * lse).mean()
         b["prob"][s] = steps * r["prob"][s] + 2.0 ** -149
         b["loss"][s] = (steps + 4 * U) * r["loss"][s]
-        b["z"][s] = steps * r["z"][s] + (2 * np.abs(lse) * (64 * U + 3 * U * np.abs(lse))).mean()
+        b["z"][s] = steps * r["z"][s] + (2 * np.abs(lse) * (66 * U + 3 * U * np.abs(lse))).mean()
     return r, b
 
 
@@ -79,7 +80,7 @@ def gradient(l, counts, tokens, grad_loss, grad_z, k, score, dtype, offsets=None
         dot = (np.where(p != 0, g * p, 0.0)).sum(1, keepdims=True)
         v = np.where(p != 0, p * (g - dot + zt) * rest, 0.0)
         out[at] = v
-        # p and every term of the bracket to 64 U and the rounding of each step; the sum of 256 products 24 U more
+        # p and every term of the bracket to 128 U and the rounding of each step; the sum of 256 products 24 U more
         mag = p * (np.abs(g) + (np.abs(g) * p).sum(1, keepdims=True) + np.abs(zt)) * rest
-        bound[at] = 200 * U * mag + HALF[dtype] * np.abs(v) + TINY[dtype]
+        bound[at] = 300 * U * mag + HALF[dtype] * np.abs(v) + TINY[dtype]
     return out, bound

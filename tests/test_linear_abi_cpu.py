@@ -42,8 +42,8 @@ BOTH = [
 @pytest.mark.parametrize("kw,status", BOTH + [
     (dict(idx=None), "MOE_ERR_NULL"), (dict(loss=None), "MOE_ERR_NULL"), (dict(idx=P + 2), "MOE_ERR_ALIGN"),
     (dict(loss=P + 2), "MOE_ERR_ALIGN"), (dict(z=P + 2), "MOE_ERR_ALIGN"), (dict(prob=P + 2), "MOE_ERR_ALIGN"),
-    (dict(o=bopts(score=1), z=P), "MOE_ERR_OPTION"), (dict(ws=None), "MOE_ERR_WORKSPACE"),
-    (dict(n=0), "MOE_ERR_WORKSPACE"), (dict(ws=P + 8), "MOE_ERR_ALIGN")])
+    (dict(o=bopts(score=1), z=P), "MOE_ERR_OPTION"), (dict(T=3000, ws=None), "MOE_ERR_WORKSPACE"),
+    (dict(T=3000, n=0), "MOE_ERR_WORKSPACE"), (dict(T=3000, ws=P + 8), "MOE_ERR_ALIGN")])
 def test_balance_loss_refuses(kw, status):
     assert moe.STATUS[balance(**kw)] == status
 
@@ -60,9 +60,9 @@ def test_balance_workspace():
     size = moe.lib().moe_balance_workspace_size
     assert size(0, 32, 1) == 0 and size(-1, 32, 1) == 0 and size(4, 0, 1) == 0 and size(4, 257, 1) == 0
     assert size(4, 32, 0) == 0
-    need = size(1000, 32, 5)
-    assert moe.STATUS[balance(T=1000, o=bopts(seqs=5, offsets=P), n=need - 1)] == "MOE_ERR_WORKSPACE"
-    assert moe.STATUS[balance(T=1000, o=bopts(seqs=5, offsets=P), n=need)] == "MOE_ERR_DEVICE"
+    need = size(3000, 32, 5)
+    assert moe.STATUS[balance(T=3000, o=bopts(seqs=5, offsets=P), n=need - 1)] == "MOE_ERR_WORKSPACE"
+    assert moe.STATUS[balance(T=3000, o=bopts(seqs=5, offsets=P), n=need)] == "MOE_ERR_DEVICE"
     # about a thousand chunks at most
     assert size(1 << 25, 256, 1) <= 1100 * (2 * 256 + 4) * 4
 
