@@ -36,9 +36,10 @@ int chunk_tokens(int T) {
 // tokens: nothing is known of the sequences here but their number and T.
 bool whole_sequences(int T, int S) { return T <= 512 || (T <= 2048 && S >= 4); }
 
-// exp(x): the hardware's exponential of x / ln 2, whose rounding is the larger
-// part of the error, |x| 2^-24 (expf takes twice the instructions)
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.69314718055994531f;
+
+// a b, and 0 where a or b is 0 whatever the other is (v_mul_legacy_f32)
+__device__ float mul0(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
 
 template <int LT>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
@@ -94,8 +95,11 @@ __device__ __forceinline__ void load_row(const void* logits, int64_t at, int E, 
 
 // Scores of a row in place of its logits, without their sum's division: the
 // exponentials over their maximum, or the sigmoids (GRAD: 1 - s in q).  inv:
-// what makes them probabilities.  Returns the softmax's lse (0 for a row that
-// masks everything).  A masked expert's score is 0 also beside NaN.
+// what makes them probabilities, by mul0: a masked expert's are 0 also beside
+// NaN.  Returns the softmax's lse (0 for a row that masks everything).
+//
+// The hardware's exponential and logarithm to base 2, after the maximum is taken
+// off (l may be any float): (l - m) log2(e) is off by about |l - m| 2^-23.
 template <int NB, bool SOFTMAX, bool GRAD>
 __device__ __forceinline__ float scores(f32x4 (&l)[NB], f32x4 (&q)[NB], float& inv) {
   float sum = 0.0f;
@@ -104,30 +108,31 @@ __device__ __forceinline__ float scores(f32x4 (&l)[NB], f32x4 (&q)[NB], float& i
 #pragma unroll
     for (int c = 0; c < NB; ++c) m = fmaxf(m, fmaxf(fmaxf(l[c].x, l[c].y), fmaxf(l[c].z, l[c].w)));
     m = max16(m);
+    const bool none = m == -INFINITY;
+    m = none ? 0.0f : m;
 #pragma unroll
     for (int c = 0; c < NB; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float e = l[c][j] == -INFINITY ? 0.0f : exp_fast(l[c][j] - m);
-        l[c][j] = e;
-        sum += e;
+        l[c][j] = __builtin_amdgcn_exp2f((l[c][j] - m) * LOG2E);
+        sum += l[c][j];
       }
     sum = sum16(sum);
-    inv = 1.0f / sum;
-    return sum == 0.0f ? 0.0f : m + logf(sum);
+    inv = __builtin_amdgcn_rcpf(sum);
+    return none ? 0.0f : m + __builtin_amdgcn_logf(sum) * LN2;
   } else {
 #pragma unroll
     for (int c = 0; c < NB; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float v = l[c][j];
-        const float s = __builtin_amdgcn_rcpf(1.0f + exp_fast(-v));  // exactly 0 at -inf
-        if constexpr (GRAD) q[c][j] = __builtin_amdgcn_rcpf(1.0f + exp_fast(v));
+        const float v = l[c][j] * LOG2E;
+        const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v));  // exactly 0 at -inf
+        if constexpr (GRAD) q[c][j] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v));
         l[c][j] = s;
         sum += s;
       }
     sum = sum16(sum) + SCORE_EPS;
-    inv = 1.0f / sum;
+    inv = __builtin_amdgcn_rcpf(sum);
     return 0.0f;
   }
 }
@@ -187,7 +192,7 @@ __device__ __forceinline__ void sum_tokens(const void* logits, int64_t ld, int v
 #pragma unroll
     for (int c = 0; c < NB; ++c)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[c][j] += p[c][j] != 0.0f ? p[c][j] * inv : 0.0f;
+      for (int j = 0; j < 4; ++j) acc[c][j] += mul0(p[c][j], inv);
     za += lse * lse;
   }
   // the four rows of a wave
@@ -433,8 +438,8 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const void* __res
     for (int c = 0; c < NB; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        p[c][j] = p[c][j] != 0.0f ? p[c][j] * inv : 0.0f;
-        dot += g[c][j] * p[c][j];
+        p[c][j] = mul0(p[c][j], inv);
+        dot = __builtin_fmaf(g[c][j], p[c][j], dot);
       }
     dot = sum16(dot);
     const float add = zslope * lse - dot;
@@ -445,9 +450,9 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const void* __res
       f32x4 v;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float d = p[c][j] * (g[c][j] + add);
-        if (!SOFTMAX) d *= q[c][j];
-        v[j] = live && p[c][j] != 0.0f ? d : 0.0f;
+        float d = mul0(p[c][j], g[c][j] + add);
+        if (!SOFTMAX) d = mul0(d, q[c][j]);
+        v[j] = live ? d : 0.0f;
       }
       if (vec_out) {
         if constexpr (LT == GATE_F32) {

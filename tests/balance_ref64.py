@@ -2,7 +2,7 @@
 fp32 error.
 
 U = 2^-24.  A probability: the exponent's difference, and its product with 1 / ln 2, are off by at most U |l - m| each
-(|l - m| <= 20 in the tests, smaller probabilities weigh nothing), the exponential and the division by 2 U each, its
+(|l - m| <= 20 in the tests, smaller probabilities weigh nothing), the exponential and the reciprocal by 2 U each, its
 sum of E <= 256 positive terms by 24 U (sixteen a lane, then four steps) beside its terms' own 42 U, weighted by p: 128 U
 of p in all.  A sum over tokens of positive terms adds U for each step of its order: at
 most T / 32 + 300.  log and the logsumexp: 66 U from the sum, and 3 U |lse| from its own roundings.
