@@ -32,9 +32,11 @@ int chunk_tokens(int T) {
   return (int)((c + 31) / 32 * 32);
 }
 
-// One launch, a workgroup a sequence, where that is at most a few rounds of 64
-// tokens: nothing is known of the sequences here but their number and T.
-bool whole_sequences(int T, int S) { return T <= 512 || (T <= 2048 && S >= 4); }
+// One launch, a workgroup a sequence, for few tokens: 512 x 32 in 7.2 us of
+// kernels and 9.2 us a call, against 3.6 and 3.8 us and 13.1 us a call in two.
+// More tokens need more CUs (1237 x 160 in nine sequences: 17.1 us against 12.3
+// and 4.0).
+bool whole_sequences(int T) { return T <= 512; }
 
 constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.69314718055994531f;
 
@@ -144,6 +146,21 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_
     const int mid = (int)(((unsigned)lo + (unsigned)hi) / 2u);
     if (offsets[mid + 1] > t) hi = mid;
     else lo = mid + 1;
+  }
+  return lo;
+}
+
+// The same for a token that the whole wave asks for: 64 probes at a time
+__device__ __forceinline__ int sequence_of_wave(const int32_t* offsets, int S, int64_t t) {
+  int lo = 0, span = S;
+  while (span > 0) {
+    const int step = (span + 63) / 64;
+    const int at = lo + lane_id() * step;
+    const int before = (int)__builtin_popcountll(__ballot(at < lo + span && offsets[min(at, S - 1) + 1] <= t));
+    if (before == 0) break;
+    const int end = lo + span;
+    lo += (before - 1) * step + 1;
+    span = min(step - 1, end - lo);
   }
   return lo;
 }
@@ -276,7 +293,8 @@ __global__ __launch_bounds__(1024) void balance_whole_kernel(const void* __restr
 
 // A workgroup sums the chunk [lo, hi) of tokens, each sequence in it into a
 // slot of its own: chunk c and sequence s meet at most once on the way
-// through both, so c + s names the slot.
+// through both, so c + s names the slot.  The gridDim.y workgroups of a chunk
+// take its sequences by turns (a sequence is a chain of latencies, some 4 us).
 template <int NB, int LT, bool SOFTMAX>
 __global__ __launch_bounds__(512) void balance_part_kernel(const void* __restrict__ logits, int64_t ld, int vec, int T,
                                                            int E, int k, const int32_t* __restrict__ idx, BalanceDev b,
@@ -285,8 +303,8 @@ __global__ __launch_bounds__(512) void balance_part_kernel(const void* __restric
   const int tid = threadIdx.x;
   const int64_t lo = (int64_t)blockIdx.x * chunk, hi = min((int64_t)T, lo + chunk);
   const int words = slot_words(E), padded = (E + 3) / 4 * 4;
-  int s = b.offsets ? sequence_of(b.offsets, b.S, lo) : 0;
-  for (; s < b.S; ++s) {
+  int s = b.offsets ? sequence_of_wave(b.offsets, b.S, lo) : 0;
+  for (s += blockIdx.y; s < b.S; s += gridDim.y) {
     const int64_t from = b.offsets ? max(lo, (int64_t)b.offsets[s]) : lo;
     const int64_t to = b.offsets ? min(hi, (int64_t)b.offsets[s + 1]) : hi;
     if (from >= hi) break;
@@ -501,7 +519,7 @@ hipError_t dispatch(int E, int lt, int score, F&& go) {
 }  // namespace
 
 int64_t balance_ws_bytes(int T, int E, int S) {
-  if (whole_sequences(T, S)) return 0;
+  if (whole_sequences(T)) return 0;
   const int chunk = chunk_tokens(T);
   return (((int64_t)T + chunk - 1) / chunk + S) * slot_words(E) * 4;
 }
@@ -511,16 +529,17 @@ hipError_t launch_balance(const void* logits, int lt, int64_t ld, int T, int E, 
                           void* ws, hipStream_t st) {
   const int vec = rows_vec(logits, lt, E, ld);
   const BalanceOut o{loss, z, prob, counts, tokens};
-  const bool whole = whole_sequences(T, b.S);
+  const bool whole = whole_sequences(T);
   const int chunk = whole ? 1 : chunk_tokens(T);
+  const unsigned chunks = (unsigned)((T + (int64_t)chunk - 1) / chunk);
+  const unsigned turns = whole ? 1u : std::max(1u, std::min({512u / chunks, (unsigned)b.S, 8u}));
   const hipError_t r = dispatch(E, lt, b.score, [&](auto nb, auto l, auto softmax) {
     constexpr int NB = decltype(nb)::value, LT = decltype(l)::value;
     constexpr bool SM = decltype(softmax)::value;
     if (whole)
       return launch_kernel(balance_whole_kernel<NB, LT, SM>, (unsigned)b.S, 1024, 0, st, logits, ld, vec, T, E, k, idx,
                            b, o);
-    return launch_kernel(balance_part_kernel<NB, LT, SM>, (unsigned)((T + (int64_t)chunk - 1) / chunk), 512, 0, st,
-                         logits, ld, vec, T, E, k, idx, b, chunk, (float*)ws);
+    return launch_kernel(balance_part_kernel<NB, LT, SM>, dim3(chunks, turns), 512, 0, st, logits, ld, vec, T, E, k, idx, b, chunk, (float*)ws);
   });
   if (r != hipSuccess || whole) return r;
   return launch_kernel(balance_join_kernel, (unsigned)b.S, 1024, 0, st, (const float*)ws, T, E, k, b, chunk, o);
