@@ -222,6 +222,8 @@ constexpr int LINEAR_DZ_ROWS = 64;
 
 // bytes of the partial sums of a product [M, N] over K (0: none)
 int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K);
+// the same for launch_linear
+int64_t linear_forward_bytes(int64_t T, int64_t N, int64_t K);
 hipError_t launch_linear(const void* x, int dt, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K,
                          const LinearEpi& e, float* part, hipStream_t st);
 // dz: g.dz, or the gradient itself where that is dz (rows ldz apart, ldz % 8 == 0, N values and zeros up to the next

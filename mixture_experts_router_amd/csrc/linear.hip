@@ -353,10 +353,14 @@ struct TileParams {
   LinearEpi e;
 };
 
-// GATED: the wave's second column block holds the up columns of its first
-template <int DT, bool TA, bool TB, bool GATED, int BM, int BN, int WM, int WN, int NS>
-__global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams prm) {
-  constexpr int WAVES = WM * WN;
+// GATED: the wave's second column block holds the up columns of its first.
+// KS 2: two waves share a block of C, each half of every stage's k-steps, and
+// add up at the end (a second wave on the SIMD where the tile has only four
+// blocks).
+template <int DT, bool TA, bool TB, bool GATED, int BM, int BN, int WM, int WN, int KS, int NS>
+__global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileParams prm) {
+  constexpr int WAVES = WM * WN * KS;
+  constexpr int JW = 4 / KS;  // MFMA k-steps of a stage and wave
   constexpr int MS = BM / WM / 32, NSUB = BN / WN / 32;
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
   constexpr int NIA = BM / 8 / WAVES, NIB = BN / 8 / WAVES, LOADS = NIA + NIB;
@@ -383,7 +387,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
   typedef Loader<TB, BN, NIB> LB;
 
   const int lane = lane_id(), wave = wave_id();
-  const int wm = wave / WN, wn = wave % WN;
+  const int wm = wave / WN % WM, wn = wave % WN, kh = wave / (WM * WN);
 
   // ---- the tile: XCD x takes a contiguous range of the tiles, which run over
   // the row tiles of a group, then column tiles, then groups, then splits
@@ -436,7 +440,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
   };
 
   // Fragments are read one k-step of 16 ahead of the MFMAs.  Before the last
-  // of a stage's four, its reads are complete: one wait for the next stage's
+  // of a stage's, its reads are complete: one wait for the next stage's
   // loads and one barrier, after which the stage is refilled NS steps ahead and
   // the next stage's first fragments are read under the last MFMAs.
   if (steps > 0) {
@@ -448,13 +452,13 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
     });
     wait_vmcnt<(NS - 1) * LOADS>();
     __builtin_amdgcn_s_barrier();
-    fragments(st0, 0, af[0], bf[0]);
+    fragments(st0, kh * JW, af[0], bf[0]);
     auto step = [&](auto S_, int i) __attribute__((always_inline)) {
       constexpr int S = decltype(S_)::value, N = (S + 1) % NS;
       const uint8_t* st = stage(S_);
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        fragments(st, j + 1, af[(j + 1) & 1], bf[(j + 1) & 1]);
+      for (int j = 0; j < JW - 1; ++j) {
+        fragments(st, kh * JW + j + 1, af[(j + 1) & 1], bf[(j + 1) & 1]);
         __builtin_amdgcn_sched_barrier(0);
         multiply(af[j & 1], bf[j & 1]);
         __builtin_amdgcn_sched_barrier(0);
@@ -464,7 +468,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
       issue(S_, i + NS);
-      fragments(stage(IC<N>{}), 0, af[0], bf[0]);
+      fragments(stage(IC<N>{}), kh * JW, af[0], bf[0]);
       __builtin_amdgcn_sched_barrier(0);
       multiply(af[1], bf[1]);
       __builtin_amdgcn_sched_barrier(0);
@@ -484,6 +488,43 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
   wait_vmcnt<0>();  // no load into LDS lands after this
   __syncthreads();
 
+  // ---- KS 2: each wave of a pair passes the row blocks that the other finishes
+  constexpr int MO = MS / KS;  // row blocks that a wave finishes: kh MO ..
+  static_assert(MS % KS == 0, "whole row blocks");
+  if constexpr (KS == 2) {
+    constexpr int TILE = NSUB * 4096;  // bytes of a 32-row block's accumulators
+    constexpr int FIT = STAGE / TILE;
+    static_assert(FIT * NS >= WAVES * MO, "accumulators");
+    auto at = [&](int w, int mo) __attribute__((always_inline)) {
+      const int i = w * MO + mo, p = i / FIT;
+      return (f32x4*)((p == 0 ? st0 : p == 1 ? st1 : p == 2 ? st2 : st3) + i % FIT * TILE);
+    };
+#pragma unroll
+    for (int mo = 0; mo < MO; ++mo)
+#pragma unroll
+      for (int ni = 0; ni < NSUB; ++ni)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = kh == 0 ? acc[MO + mo][ni][4 * q + j] : acc[mo][ni][4 * q + j];
+          at(wave, mo)[(ni * 4 + q) * 64 + lane] = v;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int mo = 0; mo < MO; ++mo)
+#pragma unroll
+      for (int ni = 0; ni < NSUB; ++ni)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 v = at(wave ^ (WM * WN), mo)[(ni * 4 + q) * 64 + lane];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // the first half of k, then the second
+            acc[mo][ni][4 * q + j] = kh == 0 ? acc[mo][ni][4 * q + j] + v[j] : v[j] + acc[MO + mo][ni][4 * q + j];
+        }
+    __syncthreads();
+  }
+
   // ---- epilogue: register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
   const int M = prm.a.n;
   const int place = wave / PER_STAGE;
@@ -492,7 +533,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
   const int hh = lane / 32, col = lane % 32;
   constexpr int LPR = GATED ? 4 : 4 * NSUB;  // lanes a row, eight columns each
 #pragma unroll
-  for (int mi = 0; mi < MS; ++mi) {
+  for (int mi = 0; mi < MO; ++mi) {
 #pragma unroll
     for (int ni = 0; ni < NSUB; ++ni)
 #pragma unroll
@@ -500,7 +541,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
         rows[(8 * (r / 4) + 4 * hh + r % 4) * ROWF + ni * 32 + col] = acc[mi][ni][r];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int t0 = m0 + (wm * MS + mi) * 32;
+    const int t0 = m0 + (wm * MS + kh * MO + mi) * 32;
 #pragma unroll 1
     for (int r = lane / LPR; r < 32; r += 64 / LPR) {
       const int c = 8 * (lane % LPR);
@@ -527,6 +568,122 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void linear_tile_kernel(TileParams
       }
     }
     __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---------------------------------------------------------- stream kernel --
+//
+// Few tokens or few columns: a workgroup computes 16 G columns of 16 H tokens,
+// its eight waves taking every eighth 64 of k (a wave's operands are used by no
+// other, so they go from memory to registers; no barrier before the end).  W is
+// the MFMA's row operand, so a lane ends with four consecutive columns of one
+// token.  A lane's 32 bytes of a row are two 16-byte loads, one for each of the
+// unit's two MFMAs (k is summed in that order, whatever it is called), and the
+// next unit's loads are under way while one is multiplied.  The waves' sums go
+// through LDS.  Bound by the bytes of W (one token), or by what the L2 gives a
+// CU: 16 (G + H) rows for 256 G H products.
+// GATED: groups G / 2 .. G - 1 are the up columns of the first G / 2.
+struct StreamParams {
+  const uint16_t* x;
+  const uint16_t* w;
+  int64_t ldx, ldw;
+  int T, N, K, t_tiles;
+  LinearEpi e;
+};
+
+template <int DT, bool GATED, int G, int H>
+__global__ __launch_bounds__(512, G * H > 4 ? 2 : 4) void linear_stream_kernel(StreamParams prm) {
+  constexpr int WAVES = 8;
+  constexpr int OG = GATED ? G / 2 : G;  // groups of output columns
+  __shared__ f32x4 sums[WAVES][G * H][64];
+  const int lane = lane_id(), wave = wave_id(), r = lane % 16, g = lane / 16;
+  // tokens fastest: the workgroups that run at a time share their rows of W
+  const int tt = (int)blockIdx.x % prm.t_tiles, ct = (int)blockIdx.x / prm.t_tiles;
+  const int t0 = tt * 16 * H, c0 = ct * 16 * OG;
+  const rsrc_t rx = make_rsrc(prm.x + (int64_t)t0 * prm.ldx, OUT_OF_RANGE);
+  const rsrc_t rw = make_rsrc(prm.w + (int64_t)c0 * prm.ldw, OUT_OF_RANGE);
+  const rsrc_t ru = make_rsrc(prm.w + ((int64_t)prm.e.C + c0) * prm.ldw, OUT_OF_RANGE);
+  uint32_t xo[H], wo[G];
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    xo[h] = t0 + 16 * h + r < prm.T ? (uint32_t)((16 * h + r) * prm.ldx * 2) + (uint32_t)g * 16u : OUT_OF_RANGE;
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const int c = 16 * (i % OG) + r;
+    wo[i] = c0 + c < prm.e.C ? (uint32_t)(c * prm.ldw * 2) + (uint32_t)g * 16u : OUT_OF_RANGE;
+  }
+  struct Unit {
+    u32x4 w[G][2], x[H][2];
+  };
+  auto load = [&](Unit& v, int u) __attribute__((always_inline)) {
+    const int k = 64 * u + 8 * g;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const bool in = k + 32 * b < prm.K;
+      const int at = 128 * u + 64 * b;
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+        v.w[i][b] = __builtin_amdgcn_raw_buffer_load_b128(GATED && i >= OG ? ru : rw,
+                                                          (int)(in ? wo[i] + at : OUT_OF_RANGE), 0, 0);
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        v.x[h][b] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(in ? xo[h] + at : OUT_OF_RANGE), 0, 0);
+    }
+  };
+  f32x4 acc[G][H];
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int h = 0; h < H; ++h) acc[i][h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const Unit& v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+#pragma unroll
+        for (int h = 0; h < H; ++h) acc[i][h] = mfma16<DT>(v.w[i][b], v.x[h][b], acc[i][h]);
+  };
+  // units past the last are zeros without memory traffic
+  const int units = (prm.K + 63) / 64;
+  Unit a, b;
+  load(a, wave);
+  for (int u = wave; u < units; u += 2 * WAVES) {
+    load(b, u + WAVES);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(a);
+    load(a, u + 2 * WAVES);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(b);
+  }
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int h = 0; h < H; ++h) sums[wave][i * H + h][lane] = acc[i][h];
+  __syncthreads();
+  // a thread eight columns of a token: lanes 32 q + t and 32 q + 16 + t of a group hold columns 8 q .. 8 q + 7
+  for (int o = threadIdx.x; o < OG * 2 * 16 * H; o += 512) {
+    const int q = o % (2 * OG), t = o / (2 * OG);
+    const int i = q / 2, at = 32 * (q % 2) + t % 16, h = t / 16;
+    auto total = [&](int grp, float (&v)[8]) __attribute__((always_inline)) {
+      f32x4 lo = sums[0][grp * H + h][at], hi = sums[0][grp * H + h][at + 16];
+#pragma unroll
+      for (int wv = 1; wv < WAVES; ++wv) {
+        lo += sums[wv][grp * H + h][at];
+        hi += sums[wv][grp * H + h][at + 16];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = lo[j];
+        v[4 + j] = hi[j];
+      }
+    };
+    const int n = c0 + 16 * i + 8 * (q % 2);
+    if (t0 + t < prm.T && n < prm.e.C) {
+      float z[8], u[8];
+      total(i, z);
+      if constexpr (GATED) total(OG + i, u);
+      finish8<DT, GATED>(prm.e, t0 + t, n, z, u);
+    }
   }
 }
 
@@ -711,6 +868,7 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   prm.part = part;
   const Plan p = plan_of(a.n, N, K);
   const bool split = p.splits > 1;
+  if (split && !part) return hipErrorInvalidValue;
   const int64_t steps = (K + 63) / 64;
   prm.splits = p.splits;
   prm.k_split = (int)((steps + p.splits - 1) / p.splits) * 64;
@@ -724,26 +882,59 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   prm.per_xcd = (int)((total + NUM_XCD - 1) / NUM_XCD);
   const dim3 grid((unsigned)(prm.per_xcd * NUM_XCD));
   if (p.bm == 256)
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 2>, grid, 512, 0, st, prm);
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 1, 2>, grid, 512, 0, st, prm);
   if (p.bm == 192)
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 2>, grid, 512, 0, st, prm);
-  if (!split) {
-    if (steps <= 4)  // two workgroups a CU
-      return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2>, grid, 256, 0, st, prm);
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
-  }
-  hipError_t r = launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 4>, grid, 256, 0, st, prm);
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 1, 2>, grid, 512, 0, st, prm);
+  if (!split && steps <= 4)  // two workgroups a CU
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 1, 2>, grid, 256, 0, st, prm);
+  if (!split)
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
+  hipError_t r = launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
   if (r != hipSuccess) return r;
   const int64_t threads = (int64_t)a.n * ((e.C + 7) / 8);
   return launch_kernel(linear_join_kernel<DT>, (unsigned)((threads + 255) / 256), 256, 0, st, part, p.splits, a.n, N,
                        e);
 }
 
+// Groups of 16 columns and 16 tokens of a workgroup of the stream kernel
+struct StreamPlan {
+  int g, h;  // g 0: the tile kernel instead
+};
+
+// A workgroup loads 16 (G + H) rows; at about 9 TB/s (what the L2s give it in
+// this pattern) up to 100 MB take less than the tile kernel's 14 us for few rows
+// and its join: 16 x 4096 to 4096 10.4 against 14.8 us, 32 tokens 14.2 against
+// 14.9, 64 tokens (2816) 18.0 against 14.9; 777 x 4096 to 64 9.9 against 13.4.
+StreamPlan stream_plan(int64_t T, int64_t N, int64_t K, bool gated) {
+  const int g = gated ? 2 : 1;
+  auto bytes = [&](int h) {
+    return ((T + 16 * h - 1) / (16 * h)) * ((N + 16 * g - 1) / (16 * g)) * (16 * g + std::min<int64_t>(T, 16 * h)) * 2 * K;
+  };
+  const int h = T > 16 && bytes(2) < bytes(1) && ((T + 31) / 32) * ((N + 16 * g - 1) / (16 * g)) >= CUS ? 2 : 1;
+  return T <= 16 || bytes(h) <= (100 << 20) ? StreamPlan{g, h} : StreamPlan{0, 0};
+}
+
+template <int DT, bool GATED>
+hipError_t launch_stream(const StreamPlan& p, const void* x, int64_t ldx, int T, const void* w, int64_t ldw, int N,
+                         int K, const LinearEpi& e, hipStream_t st) {
+  StreamParams prm{(const uint16_t*)x, (const uint16_t*)w, ldx, ldw, T, N, K, (T + 16 * p.h - 1) / (16 * p.h), e};
+  const int cols = GATED ? 8 * p.g : 16 * p.g;
+  const unsigned grid = (unsigned)((int64_t)prm.t_tiles * ((e.C + cols - 1) / cols));
+  auto go = [&](auto kern) { return launch_kernel(kern, grid, 512, 0, st, prm); };
+  return p.h == 2 ? go(linear_stream_kernel<DT, GATED, GATED ? 2 : 1, 2>)
+                  : go(linear_stream_kernel<DT, GATED, GATED ? 2 : 1, 1>);
+}
+
 template <int DT>
 hipError_t forward(const void* x, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K, const LinearEpi& e,
                    float* part, hipStream_t st) {
+  const bool gated = e.act == LIN_SWIGLU;
+  const StreamPlan p = stream_plan(T, N, K, gated);
+  if (p.g)
+    return gated ? launch_stream<DT, true>(p, x, ldx, T, w, ldw, N, K, e, st)
+                 : launch_stream<DT, false>(p, x, ldx, T, w, ldw, N, K, e, st);
   const Operand a{(const uint16_t*)x, ldx, T}, b{(const uint16_t*)w, ldw, N};
-  if (e.act == LIN_SWIGLU) return launch_tile<DT, false, false, true>(a, b, N, K, e, part, st);
+  if (gated) return launch_tile<DT, false, false, true>(a, b, N, K, e, part, st);
   return launch_tile<DT, false, false, false>(a, b, N, K, e, part, st);
 }
 
@@ -791,6 +982,12 @@ hipError_t backward(const LinearGrad& g, const void* x, int64_t ldx, const void*
 }
 
 }  // namespace
+
+int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K);
+int64_t linear_forward_bytes(int64_t T, int64_t N, int64_t K) {
+  // gated and not: the larger
+  return stream_plan(T, N, K, false).g && stream_plan(T, N, K, true).g ? 0 : linear_part_bytes(T, N, K);
+}
 
 int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K) {
   const Plan p = plan_of(M, N, K);

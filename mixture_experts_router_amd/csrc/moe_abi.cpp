@@ -1040,7 +1040,7 @@ moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, int64_t l
 
 size_t moe_linear_workspace_size(int32_t T, int32_t N, int32_t K) {
   if (T < 0 || N < 1 || K < 1) return 0;
-  return align_up((size_t)moe::linear_part_bytes(T, N, K));
+  return align_up((size_t)moe::linear_forward_bytes(T, N, K));
 }
 
 moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const moe_dense* dense,
