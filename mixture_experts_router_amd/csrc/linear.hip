@@ -275,6 +275,9 @@ struct Loader {
   const uint16_t* base;
   const uint16_t* base2;  // GATED: the up rows
   int64_t ld;
+  u32x4 buf, buf2;
+  uint32_t soff;
+  int left;
 
   // Piece p of k row kr lies at place p ^ swizzle(kr): 32 lanes of a transposed
   // read take 64 bytes of four consecutive rows, which must lie in different
@@ -287,7 +290,7 @@ struct Loader {
   template <bool GATED>
   __device__ __forceinline__ void init(const Operand& o, int m0, int up, int q0, int lane) {
     ld = o.ld;
-    const int left = (GATED ? up : o.n) - m0;
+    const int wide = (GATED ? up : o.n) - m0;
     if constexpr (!TR) {
       base = o.p + (int64_t)m0 * ld;
       base2 = o.p + ((int64_t)m0 + up) * ld;
@@ -297,7 +300,7 @@ struct Loader {
         const int piece = (lane & 7) ^ ((r / 2) & 7);
         const int row = GATED ? 32 * (r / 64) + r % 32 : r;
         kc[i] = 8 * piece;
-        off[i] = row < left ? (uint32_t)((int64_t)row * ld * 2) + (uint32_t)piece * 16u : OUT_OF_RANGE;
+        off[i] = row < wide ? (uint32_t)((int64_t)row * ld * 2) + (uint32_t)piece * 16u : OUT_OF_RANGE;
       }
     } else {
       base = o.p + m0;
@@ -308,21 +311,23 @@ struct Loader {
         const int kr = at / PPR;
         const int piece = (at % PPR) ^ swizzle(kr);
         kc[i] = kr;
-        off[i] = 8 * piece < left ? (uint32_t)((int64_t)kr * ld * 2) + (uint32_t)piece * 16u : OUT_OF_RANGE;
+        off[i] = 8 * piece < wide ? (uint32_t)((int64_t)kr * ld * 2) + (uint32_t)piece * 16u : OUT_OF_RANGE;
       }
     }
   }
-  // the step of k0 .. k0 + 63 up to kend (none of it: zeros, without memory traffic)
+  // The loads of the step k0 .. k0 + 63 up to kend (none of it: zeros, without
+  // memory traffic): their buffers, then load instruction i
   template <bool GATED>
-  __device__ __forceinline__ void issue(int k0, int kend, int q0, uint32_t lds) const {
-    const int kl = kend - k0;
-    const uint32_t range = kl > 0 ? OUT_OF_RANGE : 0u;
-    const uint32_t soff = TR ? 0u : (uint32_t)k0 * 2u;
-    const u32x4 r = buffer_of(TR ? base + (int64_t)k0 * ld : base, range);
-    const u32x4 r2 = buffer_of(GATED ? base2 : base, range);
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      dma16(GATED && ((q0 + i) / 4) % 2 ? r2 : r, kc[i] < kl ? off[i] : OUT_OF_RANGE, soff, lds + (q0 + i) * 1024);
+  __device__ __forceinline__ void begin(int k0, int kend) {
+    left = kend - k0;
+    const uint32_t range = left > 0 ? OUT_OF_RANGE : 0u;
+    soff = TR ? 0u : (uint32_t)k0 * 2u;
+    buf = buffer_of(TR ? base + (int64_t)k0 * ld : base, range);
+    buf2 = buffer_of(GATED ? base2 : base, range);
+  }
+  template <bool GATED>
+  __device__ __forceinline__ void issue(int i, int q0, uint32_t lds) const {
+    dma16(GATED && ((q0 + i) / 4) % 2 ? buf2 : buf, kc[i] < left ? off[i] : OUT_OF_RANGE, soff, lds + (q0 + i) * 1024);
   }
   // fragment of 32 m (from m) and 16 k (step j of the stage): lane l holds m + l % 32, k = 16 j + 8 (l / 32) + 0..7
   static __device__ __forceinline__ s16x8 read(const uint8_t* lds, int m, int j, int lane) {
@@ -420,11 +425,15 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.0f;
 
-  auto issue = [&](auto S_, int step) __attribute__((always_inline)) {
+  auto begin = [&](int step) __attribute__((always_inline)) {
     const int k0 = k_lo + 64 * step;
+    la.template begin<false>(k0, k_hi);
+    lb.template begin<GATED>(k0, k_hi);
+  };
+  auto issue = [&](auto S_, int i) __attribute__((always_inline)) {  // load i of the step, into stage S
     const uint32_t st = lds_address(stage(S_));
-    la.template issue<false>(k0, k_hi, wave * NIA, st);
-    lb.template issue<GATED>(k0, k_hi, wave * NIB, st + A_BYTES);
+    if (i < NIA) la.template issue<false>(i, wave * NIA, st);
+    else lb.template issue<GATED>(i - NIA, wave * NIB, st + A_BYTES);
   };
   auto fragments = [&](const uint8_t* st, int j, s16x8 (&af)[MS], s16x8 (&bf)[NSUB]) __attribute__((always_inline)) {
 #pragma unroll
@@ -446,7 +455,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
   if (steps > 0) {
     s16x8 af[2][MS], bf[2][NSUB];
     for_each<0, NS>([&](auto S_) __attribute__((always_inline)) {
-      issue(S_, decltype(S_)::value);
+      begin(decltype(S_)::value);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) issue(S_, i);
       __builtin_amdgcn_sched_barrier(0);
       return true;
     });
@@ -467,11 +478,19 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
       __builtin_amdgcn_s_waitcnt(0xC07F);   // and its reads of this stage (lgkmcnt 0)
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
-      issue(S_, i + NS);
+      begin(i + NS);
       fragments(stage(IC<N>{}), kh * JW, af[0], bf[0]);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(af[1], bf[1]);
-      __builtin_amdgcn_sched_barrier(0);
+      // the last MFMAs and the loads by turns, so that neither waits for the other
+      constexpr int MMAS = MS * NSUB;
+#pragma unroll
+      for (int m = 0; m < MMAS; ++m) {
+        acc[m / NSUB][m % NSUB] = mfma32<DT>(af[1][m / NSUB], bf[1][m % NSUB], acc[m / NSUB][m % NSUB]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int l = m * LOADS / MMAS; l < (m + 1) * LOADS / MMAS; ++l) issue(S_, l);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     };
     int i = 0;
     for (; i + NS <= steps; i += NS)
