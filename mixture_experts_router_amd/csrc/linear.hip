@@ -16,22 +16,11 @@ namespace {
 typedef __bf16 bf16;
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int NUM_XCD = 8;  // workgroups go round-robin over 8 XCDs, each with its own L2
 constexpr uint32_t OUT_OF_RANGE = 0x80000000u;  // a byte offset past every descriptor: the load gives zeros
-
-template <int DT>
-__device__ __forceinline__ f32x16 mfma32(s16x8 a, s16x8 b, f32x16 c) {
-  if constexpr (DT == ACT_BF16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
-                                                  0);
-}
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -279,12 +268,12 @@ struct Loader {
   uint32_t soff;
   int left;
 
-  // Piece p of k row kr lies at place p ^ swizzle(kr): 32 lanes of a transposed
-  // read take 64 bytes of four consecutive rows, which must lie in different
-  // quarters of the 256 bytes of banks (rows of 192 values are 384 bytes, so
-  // every other row is half way round already).
+  // Piece p of k row kr lies at place p ^ swizzle(kr).  32 lanes of a transposed
+  // read take 32 bytes of eight rows, kr .. kr + 3 and kr + 8 .. kr + 11, which
+  // must lie in different eighths of the 256 bytes of banks (rows of 192 values
+  // are 384 bytes, so every other row is half way round already).
   static __device__ __forceinline__ int swizzle(int kr) {
-    return R % 128 == 0 ? (kr & 3) << 2 : ((kr >> 1) & 1) << 2;
+    return (R % 128 == 0 ? (kr & 3) << 2 : ((kr >> 1) & 1) << 2) ^ (((kr >> 3) & 1) << 1);
   }
   // GATED: tile rows run over 32 gate rows from m0 and the 32 up rows `up` further, by turns
   template <bool GATED>
@@ -329,22 +318,24 @@ struct Loader {
   __device__ __forceinline__ void issue(int i, int q0, uint32_t lds) const {
     dma16(GATED && ((q0 + i) / 4) % 2 ? buf2 : buf, kc[i] < left ? off[i] : OUT_OF_RANGE, soff, lds + (q0 + i) * 1024);
   }
-  // fragment of 32 m (from m) and 16 k (step j of the stage): lane l holds m + l % 32, k = 16 j + 8 (l / 32) + 0..7
-  static __device__ __forceinline__ s16x8 read(const uint8_t* lds, int m, int j, int lane) {
+  // fragment of 16 m (from m) and 32 k (half j of the stage): lane l holds m + l % 16, k = 32 j + 8 (l / 16) + 0..7
+  static __device__ __forceinline__ u32x4 read(const uint8_t* lds, int m, int j, int lane) {
     if constexpr (!TR) {
-      const int row = m + lane % 32;
-      const int piece = (2 * j + lane / 32) ^ ((row / 2) & 7);
-      return *(const s16x8*)(lds + (row * 128 + (piece << 4)));
+      const int row = m + lane % 16;
+      const int piece = (4 * j + lane / 16) ^ ((row / 2) & 7);
+      return *(const u32x4*)(lds + (row * 128 + (piece << 4)));
     } else {
-      // lane i of a 16-lane group reads 4 values of row i / 4 and gets column i of the group's 4 x 16 block
-      const int col = m + 16 * ((lane / 16) & 1) + 4 * (lane & 3);
-      const int kr = 16 * j + 8 * (lane / 32) + ((lane & 15) >> 2);
-      auto half = [&](int kk) __attribute__((always_inline)) {
-        const int at = kk * (R * 2) + (((col >> 3) ^ swizzle(kk)) << 4) + (col & 7) * 2;
-        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at));
+      // Lane i of a 16-lane group reads 4 values of row i / 4 and gets column i of
+      // the group's 4 x 16 block.  The swizzle is the same for all of a lane's
+      // rows, so a fragment's address is one exclusive or and one sum.
+      const int kr = 8 * (lane / 16) + ((lane & 15) >> 2);
+      const int at = kr * (R * 2) + (lane & 3) * 8 + ((m * 2) ^ (swizzle(kr) << 4));
+      auto half = [&](int off) __attribute__((always_inline)) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + (at + off)));
       };
-      const s16x4 a = half(kr), b = half(kr + 4);
-      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+      const int k = j * (32 * R * 2);
+      const s16x4 a = half(k), b = half(k + 4 * R * 2);
+      return __builtin_bit_cast(u32x4, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
 };
@@ -365,8 +356,9 @@ struct TileParams {
 template <int DT, bool TA, bool TB, bool GATED, int BM, int BN, int WM, int WN, int KS, int NS>
 __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileParams prm) {
   constexpr int WAVES = WM * WN * KS;
-  constexpr int JW = 4 / KS;  // MFMA k-steps of a stage and wave
-  constexpr int MS = BM / WM / 32, NSUB = BN / WN / 32;
+  constexpr int JW = 2 / KS;  // MFMA k-steps of a stage and wave
+  constexpr int MS = BM / WM / 32, NSUB = BN / WN / 32;  // blocks of 32 rows and columns of a wave
+  constexpr int MB = 2 * MS, NB = 2 * NSUB, MH = MB / 2;  // fragments of 16
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
   constexpr int NIA = BM / 8 / WAVES, NIB = BN / 8 / WAVES, LOADS = NIA + NIB;
   static_assert(NIA >= 1 && NIB >= 1, "every wave loads");
@@ -417,13 +409,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
   la.template init<false>(prm.a, m0, 0, wave * NIA, lane);
   lb.template init<GATED>(prm.b, c0, prm.e.C, wave * NIB, lane);
 
-  f32x16 acc[MS][NSUB];
+  f32x4 acc[MB][NB];
 #pragma unroll
-  for (int mi = 0; mi < MS; ++mi)
+  for (int mi = 0; mi < MB; ++mi)
 #pragma unroll
-    for (int ni = 0; ni < NSUB; ++ni)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.0f;
+    for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   auto begin = [&](int step) __attribute__((always_inline)) {
     const int k0 = k_lo + 64 * step;
@@ -435,25 +425,25 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
     if (i < NIA) la.template issue<false>(i, wave * NIA, st);
     else lb.template issue<GATED>(i - NIA, wave * NIB, st + A_BYTES);
   };
-  auto fragments = [&](const uint8_t* st, int j, s16x8 (&af)[MS], s16x8 (&bf)[NSUB]) __attribute__((always_inline)) {
+  // half h of the wave's rows, and its columns, at k-step j
+  auto read_a = [&](const uint8_t* st, int j, int h, u32x4 (&af)[MH]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int ni = 0; ni < NSUB; ++ni) bf[ni] = LB::read(st + A_BYTES, (wn * NSUB + ni) * 32, j, lane);
-#pragma unroll
-    for (int mi = 0; mi < MS; ++mi) af[mi] = LA::read(st, (wm * MS + mi) * 32, j, lane);
+    for (int mi = 0; mi < MH; ++mi) af[mi] = LA::read(st, (wm * MB + h * MH + mi) * 16, kh * JW + j, lane);
   };
-  auto multiply = [&](const s16x8 (&af)[MS], const s16x8 (&bf)[NSUB]) __attribute__((always_inline)) {
+  auto read_b = [&](const uint8_t* st, int j, u32x4 (&bf)[NB]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int mi = 0; mi < MS; ++mi)
-#pragma unroll
-      for (int ni = 0; ni < NSUB; ++ni) acc[mi][ni] = mfma32<DT>(af[mi], bf[ni], acc[mi][ni]);
+    for (int ni = 0; ni < NB; ++ni) bf[ni] = LB::read(st + A_BYTES, (wn * NB + ni) * 16, kh * JW + j, lane);
   };
 
-  // Fragments are read one k-step of 16 ahead of the MFMAs.  Before the last
-  // of a stage's, its reads are complete: one wait for the next stage's
-  // loads and one barrier, after which the stage is refilled NS steps ahead and
-  // the next stage's first fragments are read under the last MFMAs.
+  // A k-step's MFMAs run in two halves of the wave's rows; a half's fragments
+  // are read one half ahead.  Before the last half of a stage its reads are
+  // complete: one wait for the next stage's loads and one barrier, after which
+  // the next stage's first fragments are read, and the loads that refill this
+  // stage NS steps ahead go out between the last MFMAs, so that neither waits
+  // for the other.  16 x 16 x 32 products: 8% faster than 32 x 32 x 16 at 8192^3,
+  // where the card's power sets the clock (four waves of 128 x 128 gained nothing).
   if (steps > 0) {
-    s16x8 af[2][MS], bf[2][NSUB];
+    u32x4 af[2][MH], bf[2][NB];
     for_each<0, NS>([&](auto S_) __attribute__((always_inline)) {
       begin(decltype(S_)::value);
 #pragma unroll
@@ -463,34 +453,45 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
     });
     wait_vmcnt<(NS - 1) * LOADS>();
     __builtin_amdgcn_s_barrier();
-    fragments(st0, kh * JW, af[0], bf[0]);
+    read_b(st0, 0, bf[0]);
+    read_a(st0, 0, 0, af[0]);
     auto step = [&](auto S_, int i) __attribute__((always_inline)) {
       constexpr int S = decltype(S_)::value, N = (S + 1) % NS;
+      constexpr int B0 = KS == 1 ? 0 : S & 1;  // the columns' registers of the first k-step
+      static_assert(KS == 1 || NS % 2 == 0, "registers by turns");
       const uint8_t* st = stage(S_);
+      constexpr int HALVES = 2 * JW;
+      for_each<0, HALVES>([&](auto H_) __attribute__((always_inline)) {
+        constexpr int hf = decltype(H_)::value, j = hf / 2, B = (B0 + j) & 1;
+        constexpr bool last = hf == HALVES - 1;
+        if constexpr (!last) {
+          if constexpr (hf % 2 == 1) read_b(st, j + 1, bf[B ^ 1]);
+          read_a(st, (hf + 1) / 2, (hf + 1) % 2, af[(hf + 1) & 1]);
+        } else {
+          wait_vmcnt<(NS - 2) * LOADS>();      // this wave's loads of the next step have landed
+          __builtin_amdgcn_s_waitcnt(0xC07F);  // and its reads of this stage (lgkmcnt 0)
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+          begin(i + NS);
+          read_b(stage(IC<N>{}), 0, bf[B ^ 1]);
+          read_a(stage(IC<N>{}), 0, 0, af[0]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int MMAS = MH * NB;
 #pragma unroll
-      for (int j = 0; j < JW - 1; ++j) {
-        fragments(st, kh * JW + j + 1, af[(j + 1) & 1], bf[(j + 1) & 1]);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(af[j & 1], bf[j & 1]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      wait_vmcnt<(NS - 2) * LOADS>();       // this wave's loads of the next step have landed
-      __builtin_amdgcn_s_waitcnt(0xC07F);   // and its reads of this stage (lgkmcnt 0)
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      begin(i + NS);
-      fragments(stage(IC<N>{}), kh * JW, af[0], bf[0]);
-      __builtin_amdgcn_sched_barrier(0);
-      // the last MFMAs and the loads by turns, so that neither waits for the other
-      constexpr int MMAS = MS * NSUB;
+        for (int m = 0; m < MMAS; ++m) {
+          f32x4& c = acc[(hf % 2) * MH + m / NB][m % NB];
+          c = mfma16<DT>(af[hf & 1][m / NB], bf[B][m % NB], c);
+          if constexpr (last) {
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int m = 0; m < MMAS; ++m) {
-        acc[m / NSUB][m % NSUB] = mfma32<DT>(af[1][m / NSUB], bf[1][m % NSUB], acc[m / NSUB][m % NSUB]);
+            for (int l = m * LOADS / MMAS; l < (m + 1) * LOADS / MMAS; ++l) issue(S_, l);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int l = m * LOADS / MMAS; l < (m + 1) * LOADS / MMAS; ++l) issue(S_, l);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+        return true;
+      });
     };
     int i = 0;
     for (; i + NS <= steps; i += NS)
@@ -518,46 +519,39 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
       const int i = w * MO + mo, p = i / FIT;
       return (f32x4*)((p == 0 ? st0 : p == 1 ? st1 : p == 2 ? st2 : st3) + i % FIT * TILE);
     };
+    constexpr int FRAGS = 2 * NB;  // fragments of a 32-row block
 #pragma unroll
     for (int mo = 0; mo < MO; ++mo)
 #pragma unroll
-      for (int ni = 0; ni < NSUB; ++ni)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          f32x4 v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = kh == 0 ? acc[MO + mo][ni][4 * q + j] : acc[mo][ni][4 * q + j];
-          at(wave, mo)[(ni * 4 + q) * 64 + lane] = v;
-        }
+      for (int q = 0; q < FRAGS; ++q)
+        at(wave, mo)[q * 64 + lane] = kh == 0 ? acc[2 * (MO + mo) + q / NB][q % NB] : acc[2 * mo + q / NB][q % NB];
     __syncthreads();
 #pragma unroll
     for (int mo = 0; mo < MO; ++mo)
 #pragma unroll
-      for (int ni = 0; ni < NSUB; ++ni)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4 v = at(wave ^ (WM * WN), mo)[(ni * 4 + q) * 64 + lane];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)  // the first half of k, then the second
-            acc[mo][ni][4 * q + j] = kh == 0 ? acc[mo][ni][4 * q + j] + v[j] : v[j] + acc[MO + mo][ni][4 * q + j];
-        }
+      for (int q = 0; q < FRAGS; ++q) {
+        const f32x4 v = at(wave ^ (WM * WN), mo)[q * 64 + lane];
+        f32x4& c = acc[2 * mo + q / NB][q % NB];
+        c = kh == 0 ? c + v : v + acc[2 * (MO + mo) + q / NB][q % NB];  // the first half of k, then the second
+      }
     __syncthreads();
   }
 
-  // ---- epilogue: register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+  // ---- epilogue: register r of lane l holds row 4 (l / 16) + r, column l % 16 of a fragment
   const int M = prm.a.n;
   const int place = wave / PER_STAGE;
   float* rows = (float*)((place == 0 ? st0 : place == 1 ? st1 : place == 2 ? st2 : st3) +
                          wave % PER_STAGE * ROWS_BYTES);
-  const int hh = lane / 32, col = lane % 32;
   constexpr int LPR = GATED ? 4 : 4 * NSUB;  // lanes a row, eight columns each
 #pragma unroll
   for (int mi = 0; mi < MO; ++mi) {
 #pragma unroll
-    for (int ni = 0; ni < NSUB; ++ni)
+    for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        rows[(8 * (r / 4) + 4 * hh + r % 4) * ROWF + ni * 32 + col] = acc[mi][ni][r];
+      for (int ni = 0; ni < NB; ++ni)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          rows[(16 * a + 4 * (lane / 16) + r) * ROWF + ni * 16 + lane % 16] = acc[2 * mi + a][ni][r];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const int t0 = m0 + (wm * MS + kh * MO + mi) * 32;
