@@ -76,9 +76,33 @@ __device__ __forceinline__ void for_each(F&& f) {
 
 // ------------------------------------------------------------ activations --
 //
-// Exponentials are expf's (not the shorter hardware form): outputs may be fp32.
+// The hardware's exponential (base 2) and reciprocal: exp is off by |z| 2^-24
+// beside two units in the last place, where the value or its complement has
+// shrunk by as much, so no activation is off by more than a few 2^-24.
 
-__device__ __forceinline__ float sigmoid_(float v) { return 1.0f / (1.0f + expf(-v)); }
+constexpr float LOG2E = 1.44269504088896341f;
+
+__device__ __forceinline__ float sigmoid_(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * v));
+}
+
+// The normal distribution Phi(z) = erfc(-z / sqrt 2) / 2, and exp(-z^2 / 2).
+// erfc(x) = exp(-x^2) F(t) / (1 + 2 x) for x >= 0 with t = (x - 3.75) / (x + 3.75)
+// (Shepherd and Laframboise, "Chebyshev approximation of (1 + 2x) exp(x^2) erfc x
+// in 0 <= x < infinity", 1981); F here a polynomial fitted to 1.3e-8.  Phi is off
+// by 3 2^-24 at most (erfcf: the epilogue of 777 x 2816 4 us longer).
+__device__ __forceinline__ float normal_(float z, float& e) {
+  constexpr float F[] = {1.23751259f, -0.140240654f, 0.00358627038f, 0.082278423f, -0.108814269f, 0.0922907665f, -0.0586468577f, 0.0284092519f, -0.00984449498f, 0.00167591218f, 0.000396307616f, -0.000224116753f};
+  const float x = 0.70710678118654752f * fabsf(z);
+  e = __builtin_amdgcn_exp2f(-LOG2E * (x * x));
+  const float y = fminf(x, 40.0f);  // e is 0 there (or NaN, as z)
+  const float t = (y - 3.75f) * __builtin_amdgcn_rcpf(y + 3.75f);
+  float f = F[11];
+#pragma unroll
+  for (int i = 10; i >= 0; --i) f = __builtin_fmaf(f, t, F[i]);
+  const float tail = 0.5f * (e * f) * __builtin_amdgcn_rcpf(__builtin_fmaf(2.0f, y, 1.0f));
+  return z > 0.0f ? 1.0f - tail : tail;
+}
 
 // act(z) and its slope
 __device__ __forceinline__ float activate_slope(int act, float z, float& slope) {
@@ -92,8 +116,9 @@ __device__ __forceinline__ float activate_slope(int act, float z, float& slope) 
       return z * s;
     }
     case LIN_GELU: {
-      const float c = 0.5f * erfcf(-0.70710678118654752f * z);
-      slope = c + z * (0.39894228040143268f * expf(-0.5f * z * z));
+      float e;
+      const float c = normal_(z, e);
+      slope = e != 0.0f ? c + z * (0.39894228040143268f * e) : c;
       return z * c;
     }
     case LIN_SIGMOID: {
@@ -219,8 +244,7 @@ __device__ __forceinline__ void finish8(const LinearEpi& e, int64_t t, int n, fl
     switch (e.act) {
       case LIN_RELU: each([](float v) { return v > 0.0f ? v : (v != v ? v : 0.0f); }); break;
       case LIN_SILU: each([](float v) { return v * sigmoid_(v); }); break;
-      // (1 + erf(v)) = erfc(-v), without cancellation
-      case LIN_GELU: each([](float v) { return 0.5f * v * erfcf(-0.70710678118654752f * v); }); break;
+      case LIN_GELU: each([](float v) { float e; return v * normal_(v, e); }); break;
       default: each([](float v) { return sigmoid_(v); }); break;
     }
   }
@@ -850,23 +874,30 @@ struct Plan {
 };
 
 // The tile and the split of k of a product M x N over K: the least time of the
-// CU with the most tiles, a tile costing its area by how near its waves come to
-// the matrix cores' rate (the smaller the wave's share, the more LDS bytes an
-// MFMA needs).
+// CU with the most tiles, a tile costing its area by what its shape was measured
+// to take an element and step, over the 256 x 256 tile's (1.6 us a step): the
+// smaller a wave's share, the more LDS bytes an MFMA needs.
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int64_t steps = (K + 63) / 64;
   if (M < 1 || N < 1) return Plan{128, 128, 1};
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  auto cost = [&](int bm, int bn, double each) { return (double)((tiles(bm, bn) + CUS - 1) / CUS) * bm * bn * each; };
   Plan p{128, 128, 1};
-  double best = cost(128, 128, 1.6);
-  if (steps > 4 && cost(192, 256, 1.1) < best) {
-    p = Plan{192, 256, 1};
-    best = cost(192, 256, 1.1);
-  }
-  if (steps > 4 && cost(256, 256, 1.0) < best) p = Plan{256, 256, 1};
-  // fewer tiles than CUs: shares of k of at least eight steps
-  if (p.bm == 128) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(CUS / tiles(128, 128), steps / 8));
+  double best = 0.0;
+  auto offer = [&](int bm, int bn, double each) {
+    const double cost = (double)((tiles(bm, bn) + CUS - 1) / CUS) * bm * bn * each;
+    if (best != 0.0 && cost >= best) return;
+    best = cost;
+    p = Plan{bm, bn, 1};
+  };
+  offer(256, 256, 1.0);
+  offer(192, 256, 1.11);
+  offer(128, 256, 1.12);
+  offer(128, 128, 1.2);
+  if (p.bn == 256) return p;
+  // fewer tiles than CUs: shares of k of at least eight steps (four of the smaller tile; 64 x 2816 to 4096: 8.4 us and
+  // 2.9 for the join, against 11.6 and 3.4 with 128-row tiles)
+  if (M <= 64) p = Plan{64, 64, 1};
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(CUS / tiles(p.bm, p.bn), steps / (p.bm == 64 ? 4 : 8)));
   return p;
 }
 
@@ -896,13 +927,18 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   const dim3 grid((unsigned)(prm.per_xcd * NUM_XCD));
   if (p.bm == 256)
     return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 1, 2>, grid, 512, 0, st, prm);
+  if (p.bm == 128 && p.bn == 256)
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 256, 2, 4, 1, 3>, grid, 512, 0, st, prm);
   if (p.bm == 192)
     return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 1, 2>, grid, 512, 0, st, prm);
-  if (!split && steps <= 4)  // two workgroups a CU
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 1, 2>, grid, 256, 0, st, prm);
-  if (!split)
+  if (!split && p.bm == 128)
     return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
-  hipError_t r = launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
+  if constexpr (!GATED) {
+    if (!split) return launch_kernel(linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4>, grid, 256, 0, st, prm);
+  }
+  hipError_t r = p.bm == 64
+                     ? launch_kernel(linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4>, grid, 256, 0, st, prm)
+                     : launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
   if (r != hipSuccess) return r;
   const int64_t threads = (int64_t)a.n * ((e.C + 7) / 8);
   return launch_kernel(linear_join_kernel<DT>, (unsigned)((threads + 255) / 256), 256, 0, st, part, p.splits, a.n, N,
