@@ -139,34 +139,32 @@ __device__ __forceinline__ float half_to_f32(uint32_t bits) {
   return act_to_f32(bits, DT);
 }
 
-// n..n+7 of a row of 16-bit (f32: 32-bit) values, `vec` if whole and aligned
-template <int DT>
-__device__ __forceinline__ void load8(const void* p, bool f32, int64_t at, int left, bool vec, float (&v)[8]) {
+// W = 8 or 1 values from `at` of a row of 16-bit (f32: 32-bit) values, of which
+// `left` exist (the others are 0); vec: all of them, 16-byte aligned
+template <int DT, int W>
+__device__ __forceinline__ void load_n(const void* p, bool f32, int64_t at, int left, bool vec, float (&v)[W]) {
   if (f32) {
     const float* q = (const float*)p + at;
-    if (vec) {
-      const f32x4 a = *(const f32x4*)q, b = *(const f32x4*)(q + 4);
+    if (W == 8 && vec) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = a[j];
-        v[4 + j] = b[j];
+      for (int h = 0; h < W / 4; ++h) {
+        const f32x4 a = *(const f32x4*)(q + 4 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * h + j] = a[j];
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < left ? q[j] : 0.0f;
+      for (int j = 0; j < W; ++j) v[j] = j < left ? q[j] : 0.0f;
     }
   } else {
     const uint16_t* q = (const uint16_t*)p + at;
-    if (vec) {
+    if (W == 8 && vec) {
       const u32x4 a = load16(q);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = half_to_f32<DT>(a[j] & 0xFFFFu);
-        v[2 * j + 1] = half_to_f32<DT>(a[j] >> 16);
-      }
+      for (int j = 0; j < W; ++j) v[j] = half_to_f32<DT>(j % 2 ? a[j / 2] >> 16 : a[j / 2] & 0xFFFFu);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < left ? half_to_f32<DT>(q[j]) : 0.0f;
+      for (int j = 0; j < W; ++j) v[j] = j < left ? half_to_f32<DT>(q[j]) : 0.0f;
     }
   }
 }
@@ -182,64 +180,64 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-template <int DT>
-__device__ __forceinline__ void store8(void* p, bool f32, int64_t at, int left, bool vec, const float (&v)[8]) {
+template <int DT, int W>
+__device__ __forceinline__ void store_n(void* p, bool f32, int64_t at, int left, bool vec, const float (&v)[W]) {
   if (f32) {
     float* q = (float*)p + at;
-    if (vec) {
-      *(f32x4*)q = f32x4{v[0], v[1], v[2], v[3]};
-      *(f32x4*)(q + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    if (W == 8 && vec) {
+#pragma unroll
+      for (int h = 0; h < W / 4; ++h) *(f32x4*)(q + 4 * h) = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < W; ++j)
         if (j < left) q[j] = v[j];
     }
   } else {
     uint16_t* q = (uint16_t*)p + at;
-    if (vec) {
-      u32x4 a;
+    if (W == 8 && vec) {
+      u32x4 a = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a[j] = pack2<DT>(v[2 * j], v[2 * j + 1]);
+      for (int j = 0; j < W / 2; ++j) a[j] = pack2<DT>(v[2 * j], v[2 * j + 1]);
       *(u32x4*)q = a;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < W; ++j)
         if (j < left) q[j] = (uint16_t)pack2<DT>(v[j], 0.0f);
     }
   }
 }
 
-// Eight columns n..n+7 of output row t from their fp32 sums (gated: u the sums
-// of the up columns).  Everything is fp32 up to the one rounding that gives
+// W = 8 or 1 columns from n of output row t from their fp32 sums (gated: u the
+// sums of the up columns).  Everything is fp32 up to the one rounding that gives
 // `out`; the kept z is rounded on its own.  The choices are made once for the
-// eight columns: made for each, they took 25 us of a 4096 x 4096 output.
-template <int DT, bool GATED>
-__device__ __forceinline__ void finish8(const LinearEpi& e, int64_t t, int n, float (&z)[8], float (&u)[8]) {
+// columns: made for each, they took 25 us of a 4096 x 4096 output.
+template <int DT, bool GATED, int W>
+__device__ __forceinline__ void finish(const LinearEpi& e, int64_t t, int n, float (&z)[W], float (&u)[W]) {
   const int left = e.C - n;
-  const bool vec = e.vec && left >= 8;
+  const bool vec = e.vec && left >= W;
   if (e.bias) {
-    const bool bvec = e.bias_vec && left >= 8;
-    float b[8];
-    load8<DT>(e.bias, e.bias_f32, n, left, bvec, b);
+    const bool bvec = e.bias_vec && left >= W;
+    float b[W];
+    load_n<DT, W>(e.bias, e.bias_f32, n, left, bvec, b);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] += b[j];
+    for (int j = 0; j < W; ++j) z[j] += b[j];
     if (GATED) {
-      load8<DT>(e.bias, e.bias_f32, (int64_t)e.C + n, left, bvec, b);
+      load_n<DT, W>(e.bias, e.bias_f32, (int64_t)e.C + n, left, bvec, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] += b[j];
+      for (int j = 0; j < W; ++j) u[j] += b[j];
     }
   }
   if (e.pre) {
-    store8<DT>(e.pre, false, t * e.ldp + n, left, vec, z);
-    if (GATED) store8<DT>(e.pre, false, t * e.ldp + e.C + n, left, vec, u);
+    store_n<DT, W>(e.pre, false, t * e.ldp + n, left, vec, z);
+    if (GATED) store_n<DT, W>(e.pre, false, t * e.ldp + e.C + n, left, vec, u);
   }
   if constexpr (GATED) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] = z[j] * sigmoid_(z[j]) * u[j];
+    for (int j = 0; j < W; ++j) z[j] = z[j] * sigmoid_(z[j]) * u[j];
   } else if (e.act != LIN_NONE) {
     auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = f(z[j]);
+      for (int j = 0; j < W; ++j) z[j] = f(z[j]);
     };
     switch (e.act) {
       case LIN_RELU: each([](float v) { return v > 0.0f ? v : (v != v ? v : 0.0f); }); break;
@@ -251,15 +249,15 @@ __device__ __forceinline__ void finish8(const LinearEpi& e, int64_t t, int n, fl
   if (e.row_scale) {
     const float rs = e.row_scale[t];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] *= rs;
+    for (int j = 0; j < W; ++j) z[j] *= rs;
   }
   if (e.res) {
-    float r[8];
-    load8<DT>(e.res, e.out_f32, t * e.ldr + n, left, vec, r);
+    float r[W];
+    load_n<DT, W>(e.res, e.out_f32, t * e.ldr + n, left, vec, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] += r[j];
+    for (int j = 0; j < W; ++j) z[j] += r[j];
   }
-  store8<DT>(e.out, e.out_f32, t * e.ldo + n, left, vec, z);
+  store_n<DT, W>(e.out, e.out_f32, t * e.ldo + n, left, vec, z);
 }
 
 // ------------------------------------------------------------ tile kernel --
@@ -364,12 +362,15 @@ struct Loader {
   }
 };
 
+// elements between the rows of partial sums
+__host__ __device__ constexpr int64_t part_row(int64_t n) { return (n + 7) / 8 * 8; }
+
 struct TileParams {
   Operand a, b;
   int K;
   int m_tiles, n_tiles, splits, group_m, per_xcd;
   int k_split;   // k of one split, a multiple of 64
-  float* part;   // splits > 1: fp32 sums [splits][M][N]
+  float* part;   // splits > 1: fp32 sums [splits][M][part_row(N)]
   LinearEpi e;
 };
 
@@ -579,29 +580,39 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const int t0 = m0 + (wm * MS + kh * MO + mi) * 32;
+    const int w0 = c0 + wn * (GATED ? 32 : 32 * NSUB);  // the wave's first output column
+    if (prm.splits > 1 || prm.e.vec) {
 #pragma unroll 1
-    for (int r = lane / LPR; r < 32; r += 64 / LPR) {
-      const int c = 8 * (lane % LPR);
-      const int n = c0 + wn * (GATED ? 32 : 32 * NSUB) + c;
-      const float* src = rows + r * ROWF + c;
-      float z[8], u[8];
-      auto eight = [](const float* q, float (&v)[8]) __attribute__((always_inline)) {
-        const f32x4 a = *(const f32x4*)q, b = *(const f32x4*)(q + 4);
+      for (int r = lane / LPR; r < 32; r += 64 / LPR) {
+        const int c = 8 * (lane % LPR);
+        const float* src = rows + r * ROWF + c;
+        float z[8], u[8];
+        auto eight = [](const float* q, float (&v)[8]) __attribute__((always_inline)) {
+          const f32x4 a = *(const f32x4*)q, b = *(const f32x4*)(q + 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = a[j];
-          v[4 + j] = b[j];
+          for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+          }
+        };
+        eight(src, z);
+        if constexpr (GATED) eight(src + 32, u);
+        if (t0 + r < M && w0 + c < prm.e.C) {
+          if (prm.splits > 1)  // whole eights: the rows of `part` are padded
+            store_n<DT, 8>(prm.part, true, ((int64_t)split * M + t0 + r) * part_row(prm.e.C) + w0 + c, 8, true, z);
+          else
+            finish<DT, GATED, 8>(prm.e, t0 + r, w0 + c, z, u);
         }
-      };
-      eight(src, z);
-      if constexpr (GATED) eight(src + 32, u);
-      if (t0 + r < M && n < prm.e.C) {
-        if (prm.splits > 1) {
-          const bool vec = prm.e.C % 4 == 0 && n + 8 <= prm.e.C;
-          store8<DT>(prm.part, true, ((int64_t)split * M + t0 + r) * prm.e.C + n, prm.e.C - n, vec, z);
-        } else {
-          finish8<DT, GATED>(prm.e, t0 + r, n, z, u);
-        }
+      }
+    } else {
+      // rows that do not start aligned: a lane a column, so that a store still covers whole lines
+      constexpr int CW = GATED ? 32 : 32 * NSUB;
+#pragma unroll 1
+      for (int r = lane / CW; r < 32; r += 64 / CW) {
+        const int c = lane % CW;
+        float z[1] = {rows[r * ROWF + c]}, u[1] = {0.0f};
+        if constexpr (GATED) u[0] = rows[r * ROWF + 32 + c];
+        if (t0 + r < M && w0 + c < prm.e.C) finish<DT, GATED, 1>(prm.e, t0 + r, w0 + c, z, u);
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -719,39 +730,41 @@ __global__ __launch_bounds__(512, G * H > 4 ? 2 : 4) void linear_stream_kernel(S
       float z[8], u[8];
       total(i, z);
       if constexpr (GATED) total(OG + i, u);
-      finish8<DT, GATED>(prm.e, t0 + t, n, z, u);
+      finish<DT, GATED, 8>(prm.e, t0 + t, n, z, u);
     }
   }
 }
 
-// The sums of the splits in order, and the epilogue: a thread eight columns of a row
-template <int DT>
+// The sums of the splits in order, and the epilogue: a thread W columns of a row
+// (one where the rows it writes do not start aligned)
+template <int DT, int W>
 __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ part, int splits, int M, int N,
                                                           LinearEpi e) {
-  const int chunks = (e.C + 7) / 8;
+  const int chunks = (e.C + W - 1) / W;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= (int64_t)M * chunks) return;
   const int64_t t = i / chunks;
-  const int n = (int)(i - t * chunks) * 8;
+  const int n = (int)(i - t * chunks) * W;
   const bool gated = e.act == LIN_SWIGLU;
-  const bool vec = N % 4 == 0 && n + 8 <= e.C && (!gated || e.C % 4 == 0);
-  float z[8], u[8];
+  const bool up_vec = e.C % 4 == 0 && n + W <= e.C;
+  float z[W], u[W];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) z[j] = u[j] = 0.0f;
+  for (int j = 0; j < W; ++j) z[j] = u[j] = 0.0f;
+#pragma unroll 4
   for (int s = 0; s < splits; ++s) {
-    const int64_t row = ((int64_t)s * M + t) * N + n;
-    float v[8];
-    load8<DT>(part, true, row, e.C - n, vec, v);
+    const int64_t row = ((int64_t)s * M + t) * part_row(N) + n;
+    float v[W];
+    load_n<DT, W>(part, true, row, W, true, v);  // past the end: the padding, or another half's
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] += v[j];
+    for (int j = 0; j < W; ++j) z[j] += v[j];
     if (gated) {
-      load8<DT>(part, true, row + e.C, e.C - n, vec, v);
+      load_n<DT, W>(part, true, row + e.C, e.C - n, up_vec, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] += v[j];
+      for (int j = 0; j < W; ++j) u[j] += v[j];
     }
   }
-  if (gated) finish8<DT, true>(e, t, n, z, u);
-  else finish8<DT, false>(e, t, n, z, u);
+  if (gated) finish<DT, true, W>(e, t, n, z, u);
+  else finish<DT, false, W>(e, t, n, z, u);
 }
 
 // ------------------------------------------------------- gradient of z ----
@@ -782,9 +795,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
     float dot = 0.0f;
     if (left > 0) {
       float d[8], d2[8], z[8], u[8];  // columns past the end: all 0
-      load8<DT>(g.g, g.g_f32, t * g.ldg + n, left, vec, d);
-      if (g.z) load8<DT>(g.z, false, t * g.ldz_in + n, left, vec, z);
-      if (gated) load8<DT>(g.z, false, t * g.ldz_in + g.C + n, left, vec, u);
+      load_n<DT, 8>(g.g, g.g_f32, t * g.ldg + n, left, vec, d);
+      if (g.z) load_n<DT, 8>(g.z, false, t * g.ldz_in + n, left, vec, z);
+      if (gated) load_n<DT, 8>(g.z, false, t * g.ldz_in + g.C + n, left, vec, u);
       const float rs = g.rs ? g.rs[t] : 1.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -804,8 +817,8 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
         cu[j] += d2[j];
       }
       if (g.dz) {
-        store8<DT>(g.dz, false, t * g.ldz + n, left, vec, d);
-        if (gated) store8<DT>(g.dz, false, t * g.ldz + g.C + n, left, vec, d2);
+        store_n<DT, 8>(g.dz, false, t * g.ldz + n, left, vec, d);
+        if (gated) store_n<DT, 8>(g.dz, false, t * g.ldz + g.C + n, left, vec, d2);
       }
     }
     if (g.row_part) {  // the threads of a row: 64 at a time of one wave, or fewer
@@ -843,8 +856,8 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
     }
 }
 
-// out[i] = sum over b of part[b][n], in an order of its own: 16 groups of every
-// 16th b, then the groups.  A workgroup 64 of the n.
+// out[i] = sum over b of part[b][i]: 16 groups of every 16th b, then the groups.
+// A workgroup 64 of the n.
 __global__ __launch_bounds__(1024) void linear_sums_kernel(const float* __restrict__ part, int blocks, int64_t n,
                                                            float* __restrict__ out) {
   __shared__ float sums[16][64];
@@ -871,33 +884,39 @@ constexpr int CUS = 256;
 struct Plan {
   int bm, bn;  // rows and columns of a tile
   int splits;
+  double us;  // what the product is expected to take
 };
 
-// The tile and the split of k of a product M x N over K: the least time of the
-// CU with the most tiles, a tile costing its area by what its shape was measured
-// to take an element and step, over the 256 x 256 tile's (1.6 us a step): the
-// smaller a wave's share, the more LDS bytes an MFMA needs.
+// The tile and the split of k of a product M x N over K: the least of what the
+// forms are expected to take, rounds of workgroups times (steps of a share times
+// us a step, or the operands' bytes at 5 TB/s, and us to begin and to finish),
+// and the join of the shares.  Measured us a step of 64 k: 256 x 256 1.6, 192 x
+// 256 1.33, 128 x 256 0.95, 128 x 128 0.45 (154 workgroups) to 0.5 (256); 64 x 64
+// 0.25 to 0.45 (512, two a CU).  Results against a fixed tile of 128 in
+// brackets, us: 64 x 2816 to 4096 11.3 (15.1), 777 x 4096 to 2816 30 (30),
+// 2048 x 4096 to 4096 64 (77), 4096 x 11008 to 4096 273 (450).
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  Plan p{128, 128, 1, 0.0};
+  if (M < 1 || N < 1) return p;
   const int64_t steps = (K + 63) / 64;
-  if (M < 1 || N < 1) return Plan{128, 128, 1};
-  auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  Plan p{128, 128, 1};
-  double best = 0.0;
-  auto offer = [&](int bm, int bn, double each) {
-    const double cost = (double)((tiles(bm, bn) + CUS - 1) / CUS) * bm * bn * each;
-    if (best != 0.0 && cost >= best) return;
-    best = cost;
-    p = Plan{bm, bn, 1};
+  const double bytes_us = (double)((M + N) * K) * 2.0 / 5.0e6;
+  auto offer = [&](int bm, int bn, int64_t at_once, double step, double ends, int64_t splits) {
+    const int64_t work = ((M + bm - 1) / bm) * ((N + bn - 1) / bn) * splits;
+    const int64_t share = (steps + splits - 1) / splits;
+    double us = std::max((double)((work + at_once - 1) / at_once) * ((double)share * step + ends), bytes_us + ends);
+    if (splits > 1) us += 3.5 + (double)(splits * M * N) * 4.0 / 2.5e6;
+    if (p.us == 0.0 || us < p.us) p = Plan{bm, bn, (int)splits, us};
   };
-  offer(256, 256, 1.0);
-  offer(192, 256, 1.11);
-  offer(128, 256, 1.12);
-  offer(128, 128, 1.2);
-  if (p.bn == 256) return p;
-  // fewer tiles than CUs: shares of k of at least eight steps (four of the smaller tile; 64 x 2816 to 4096: 8.4 us and
-  // 2.9 for the join, against 11.6 and 3.4 with 128-row tiles)
-  if (M <= 64) p = Plan{64, 64, 1};
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(CUS / tiles(p.bm, p.bn), steps / (p.bm == 64 ? 4 : 8)));
+  offer(256, 256, CUS, 1.6, 6.0, 1);
+  offer(192, 256, CUS, 1.33, 5.5, 1);
+  offer(128, 256, CUS, 0.95, 5.0, 1);
+  const int64_t wide = ((M + 127) / 128) * ((N + 127) / 128), small = ((M + 63) / 64) * ((N + 63) / 64);
+  auto filled = [](int64_t work, int64_t at_once) { return (double)std::min(work, at_once) / (double)at_once; };
+  for (int64_t s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32}) {
+    if (s > 1 && 2 * s > steps) break;  // shares of two steps or more
+    offer(128, 128, CUS, 0.38 + 0.12 * filled(wide * s, CUS), 4.5, s);
+    offer(64, 64, 2 * CUS, 0.2 + 0.25 * filled(small * s, 2 * CUS), 4.0, s);
+  }
   return p;
 }
 
@@ -919,7 +938,8 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   prm.m_tiles = (a.n + p.bm - 1) / p.bm;
   const int C = split ? N : e.C;
   prm.e.C = C;
-  const int cols = GATED && !split ? p.bn / 2 : p.bn;
+  // gated: half of the tile's columns, but for the 64-row tile, which is 64 x 128 then
+  const int cols = GATED && !split && p.bm != 64 ? p.bn / 2 : p.bn;
   prm.n_tiles = (C + cols - 1) / cols;
   prm.group_m = std::min(prm.m_tiles, 8);
   const int64_t total = (int64_t)prm.m_tiles * prm.n_tiles * prm.splits;
@@ -927,22 +947,22 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   const dim3 grid((unsigned)(prm.per_xcd * NUM_XCD));
   if (p.bm == 256)
     return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 1, 2>, grid, 512, 0, st, prm);
-  if (p.bm == 128 && p.bn == 256)
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 256, 2, 4, 1, 3>, grid, 512, 0, st, prm);
   if (p.bm == 192)
     return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 1, 2>, grid, 512, 0, st, prm);
+  if (p.bn == 256)
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 256, 2, 4, 1, 3>, grid, 512, 0, st, prm);
   if (!split && p.bm == 128)
     return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
-  if constexpr (!GATED) {
-    if (!split) return launch_kernel(linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4>, grid, 256, 0, st, prm);
-  }
-  hipError_t r = p.bm == 64
-                     ? launch_kernel(linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4>, grid, 256, 0, st, prm)
-                     : launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
-  if (r != hipSuccess) return r;
-  const int64_t threads = (int64_t)a.n * ((e.C + 7) / 8);
-  return launch_kernel(linear_join_kernel<DT>, (unsigned)((threads + 255) / 256), 256, 0, st, part, p.splits, a.n, N,
-                       e);
+  if (!split && GATED)  // 64 columns of each half
+    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 64, 128, 2, 2, 1, 3>, grid, 256, 0, st, prm);
+  const hipError_t r =
+      p.bm == 64 ? launch_kernel(linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4>, grid, 256, 0, st, prm)
+                 : launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
+  if (r != hipSuccess || !split) return r;
+  const int w = e.vec ? 8 : 1;
+  const int64_t threads = (int64_t)a.n * ((e.C + w - 1) / w);
+  return launch_kernel(e.vec ? linear_join_kernel<DT, 8> : linear_join_kernel<DT, 1>, (unsigned)((threads + 255) / 256),
+                       256, 0, st, part, p.splits, a.n, N, e);
 }
 
 // Groups of 16 columns and 16 tokens of a workgroup of the stream kernel
@@ -950,17 +970,19 @@ struct StreamPlan {
   int g, h;  // g 0: the tile kernel instead
 };
 
-// A workgroup loads 16 (G + H) rows; at about 9 TB/s (what the L2s give it in
-// this pattern) up to 100 MB take less than the tile kernel's 14 us for few rows
-// and its join: 16 x 4096 to 4096 10.4 against 14.8 us, 32 tokens 14.2 against
-// 14.9, 64 tokens (2816) 18.0 against 14.9; 777 x 4096 to 64 9.9 against 13.4.
+// Where it is expected to take less than the tile kernel: a workgroup loads
+// 16 G rows of W and up to 16 H tokens, which the L2s give at about 9 TB/s in
+// this pattern, and a wave's units take 0.5 us each.  (16 x 4096 to 4096 10.4
+// against 14.8 us, 777 x 4096 to 64 9.9 against 13.4; 64 x 2816 to 4096 18.0
+// against 11.5.)
 StreamPlan stream_plan(int64_t T, int64_t N, int64_t K, bool gated) {
   const int g = gated ? 2 : 1;
   auto bytes = [&](int h) {
     return ((T + 16 * h - 1) / (16 * h)) * ((N + 16 * g - 1) / (16 * g)) * (16 * g + std::min<int64_t>(T, 16 * h)) * 2 * K;
   };
   const int h = T > 16 && bytes(2) < bytes(1) && ((T + 31) / 32) * ((N + 16 * g - 1) / (16 * g)) >= CUS ? 2 : 1;
-  return T <= 16 || bytes(h) <= (100 << 20) ? StreamPlan{g, h} : StreamPlan{0, 0};
+  const double us = 2.5 + std::max((double)bytes(h) / 9.0e6, 0.5 * (double)((K + 511) / 512));
+  return us <= plan_of(T, N, K).us ? StreamPlan{g, h} : StreamPlan{0, 0};
 }
 
 template <int DT, bool GATED>
@@ -1009,11 +1031,11 @@ hipError_t backward(const LinearGrad& g, const void* x, int64_t ldx, const void*
   auto sums = [&](const float* p, int blocks, int64_t n, float* out) {
     return launch_kernel(linear_sums_kernel, (unsigned)((n + 63) / 64), 1024, 0, st, p, blocks, n, out);
   };
-  if (dbias) {
+  if (dbias && g.part != dbias) {
     const hipError_t r = sums(g.part, g.blocks, g.N, dbias);
     if (r != hipSuccess) return r;
   }
-  if (g.T && drs) {
+  if (g.T && drs && g.row_part != drs) {
     const hipError_t r = sums(g.row_part, g.column_blocks, g.T, drs);
     if (r != hipSuccess) return r;
   }
@@ -1040,7 +1062,7 @@ int64_t linear_forward_bytes(int64_t T, int64_t N, int64_t K) {
 
 int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K) {
   const Plan p = plan_of(M, N, K);
-  return p.splits > 1 ? (int64_t)p.splits * M * N * 4 : 0;
+  return p.splits > 1 ? (int64_t)p.splits * M * part_row(N) * 4 : 0;
 }
 
 hipError_t launch_linear(const void* x, int dt, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K,

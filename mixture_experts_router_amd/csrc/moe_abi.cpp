@@ -1145,8 +1145,9 @@ moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_g
     g.rs = row_scale;
     g.dz = direct || !(grad_x || grad_w) || T == 0 ? nullptr : (uint16_t*)(W + L.dz);
     g.ldz = L.ldz;
-    g.part = grad_bias ? (float*)(W + L.sums) : nullptr;
-    g.row_part = grad_row_scale ? (float*)(W + L.row_sums) : nullptr;
+    // one block's sums are the result
+    g.part = !grad_bias ? nullptr : L.blocks == 1 ? grad_bias : (float*)(W + L.sums);
+    g.row_part = !grad_row_scale ? nullptr : L.column_blocks == 1 ? grad_row_scale : (float*)(W + L.row_sums);
     g.T = T;
     g.C = C;
     g.N = N;
