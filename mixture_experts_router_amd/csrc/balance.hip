@@ -533,15 +533,18 @@ hipError_t launch_balance(const void* logits, int lt, int64_t ld, int T, int E, 
   const int chunk = whole ? 1 : chunk_tokens(T);
   const unsigned chunks = (unsigned)((T + (int64_t)chunk - 1) / chunk);
   const unsigned turns = whole ? 1u : std::max(1u, std::min({512u / chunks, (unsigned)b.S, 8u}));
+  note_launch(whole ? "balance_whole" : "balance_part");
   const hipError_t r = dispatch(E, lt, b.score, [&](auto nb, auto l, auto softmax) {
     constexpr int NB = decltype(nb)::value, LT = decltype(l)::value;
     constexpr bool SM = decltype(softmax)::value;
     if (whole)
       return launch_kernel(balance_whole_kernel<NB, LT, SM>, (unsigned)b.S, 1024, 0, st, logits, ld, vec, T, E, k, idx,
                            b, o);
-    return launch_kernel(balance_part_kernel<NB, LT, SM>, dim3(chunks, turns), 512, 0, st, logits, ld, vec, T, E, k, idx, b, chunk, (float*)ws);
+    return launch_kernel(balance_part_kernel<NB, LT, SM>, dim3(chunks, turns), 512, 0, st, logits, ld, vec, T, E, k,
+                         idx, b, chunk, (float*)ws);
   });
   if (r != hipSuccess || whole) return r;
+  note_launch("balance_join");
   return launch_kernel(balance_join_kernel, (unsigned)b.S, 1024, 0, st, (const float*)ws, T, E, k, b, chunk, o);
 }
 
@@ -551,6 +554,7 @@ hipError_t launch_balance_backward(const void* logits, int lt, int64_t ld, int T
   const int vec = rows_vec(logits, lt, E, ld), vec_out = rows_vec(out, lt, E, ldo);
   // 16 tokens a workgroup until there are four workgroups a CU, then up to 64
   const int rows = (int)std::min<int64_t>(64, std::max<int64_t>(16, ((int64_t)T / 1024 + 15) / 16 * 16));
+  note_launch("balance_backward");
   return dispatch(E, lt, b.score, [&](auto nb, auto l, auto softmax) {
     constexpr int NB = decltype(nb)::value, LT = decltype(l)::value;
     constexpr bool SM = decltype(softmax)::value;

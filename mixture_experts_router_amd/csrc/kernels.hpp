@@ -21,6 +21,10 @@ __host__ __device__ constexpr int code_bits(int bits) { return bits == NVF4 ? 4 
 // next kernel launch on this thread, if one is pending.
 bool next_launch_events(hipEvent_t* start, hipEvent_t* stop);
 
+// Adds a kernel to the list of moe_debug_last_plan (launch functions of several
+// kernels; the others are named by their caller).
+void note_launch(const char* name);
+
 // Every kernel of the library is launched through here.  With a pending
 // event pair the launch carries it (hipExtLaunchKernelGGL: the events take the
 // kernel's own start/end timestamps); otherwise a plain launch.

@@ -945,22 +945,24 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   const int64_t total = (int64_t)prm.m_tiles * prm.n_tiles * prm.splits;
   prm.per_xcd = (int)((total + NUM_XCD - 1) / NUM_XCD);
   const dim3 grid((unsigned)(prm.per_xcd * NUM_XCD));
-  if (p.bm == 256)
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 1, 2>, grid, 512, 0, st, prm);
-  if (p.bm == 192)
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 1, 2>, grid, 512, 0, st, prm);
-  if (p.bn == 256)
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 256, 2, 4, 1, 3>, grid, 512, 0, st, prm);
-  if (!split && p.bm == 128)
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
-  if (!split && GATED)  // 64 columns of each half
-    return launch_kernel(linear_tile_kernel<DT, TA, TB, GATED, 64, 128, 2, 2, 1, 3>, grid, 256, 0, st, prm);
-  const hipError_t r =
-      p.bm == 64 ? launch_kernel(linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4>, grid, 256, 0, st, prm)
-                 : launch_kernel(linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4>, grid, 512, 0, st, prm);
+  auto go = [&](const char* name, auto kern, unsigned threads) {
+    note_launch(name);
+    return launch_kernel(kern, grid, threads, 0, st, prm);
+  };
+  if (p.bm == 256) return go("linear_256x256", linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 1, 2>, 512);
+  if (p.bm == 192) return go("linear_192x256", linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 1, 2>, 512);
+  if (p.bn == 256) return go("linear_128x256", linear_tile_kernel<DT, TA, TB, GATED, 128, 256, 2, 4, 1, 3>, 512);
+  if (!split && p.bm == 128) return go("linear_128x128", linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2, 4>, 512);
+  if constexpr (GATED) {  // 64 columns of each half
+    if (!split) return go("linear_64x128", linear_tile_kernel<DT, TA, TB, true, 64, 128, 2, 2, 1, 3>, 256);
+  }
+  const hipError_t r = p.bm == 64
+                           ? go("linear_64x64", linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4>, 256)
+                           : go("linear_128x128", linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4>, 512);
   if (r != hipSuccess || !split) return r;
   const int w = e.vec ? 8 : 1;
   const int64_t threads = (int64_t)a.n * ((e.C + w - 1) / w);
+  note_launch("linear_join");
   return launch_kernel(e.vec ? linear_join_kernel<DT, 8> : linear_join_kernel<DT, 1>, (unsigned)((threads + 255) / 256),
                        256, 0, st, part, p.splits, a.n, N, e);
 }
@@ -991,7 +993,10 @@ hipError_t launch_stream(const StreamPlan& p, const void* x, int64_t ldx, int T,
   StreamParams prm{(const uint16_t*)x, (const uint16_t*)w, ldx, ldw, T, N, K, (T + 16 * p.h - 1) / (16 * p.h), e};
   const int cols = GATED ? 8 * p.g : 16 * p.g;
   const unsigned grid = (unsigned)((int64_t)prm.t_tiles * ((e.C + cols - 1) / cols));
-  auto go = [&](auto kern) { return launch_kernel(kern, grid, 512, 0, st, prm); };
+  auto go = [&](auto kern) {
+    note_launch(p.h == 2 ? "linear_stream_2" : "linear_stream_1");
+    return launch_kernel(kern, grid, 512, 0, st, prm);
+  };
   return p.h == 2 ? go(linear_stream_kernel<DT, GATED, GATED ? 2 : 1, 2>)
                   : go(linear_stream_kernel<DT, GATED, GATED ? 2 : 1, 1>);
 }
@@ -1024,11 +1029,13 @@ hipError_t backward(const LinearGrad& g, const void* x, int64_t ldx, const void*
                     int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias, float* drs, const uint16_t* dz,
                     int64_t ldz, float* part, hipStream_t st) {
   if (g.T && (g.dz || g.part || g.row_part)) {
+    note_launch("linear_dz");
     const hipError_t r = launch_kernel(linear_dz_kernel<DT>, dim3((unsigned)g.blocks, (unsigned)g.column_blocks), 256, 0,
                                        st, g);
     if (r != hipSuccess) return r;
   }
   auto sums = [&](const float* p, int blocks, int64_t n, float* out) {
+    note_launch("linear_sums");
     return launch_kernel(linear_sums_kernel, (unsigned)((n + 63) / 64), 1024, 0, st, p, blocks, n, out);
   };
   if (dbias && g.part != dbias) {

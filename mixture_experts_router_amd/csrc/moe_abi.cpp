@@ -65,6 +65,14 @@ void plan_step(const char* name, hipStream_t st) {
   g_prof.plan += name;
 }
 
+}  // namespace
+
+namespace moe {
+void note_launch(const char* name) { plan_step(name, nullptr); }
+}  // namespace moe
+
+namespace {
+
 // ------------------------------------------------------- device properties
 
 struct DevProps {
@@ -1002,7 +1010,6 @@ moe_status moe_balance_loss(const void* logits, moe_dtype lt, int64_t ld, int32_
     hipStream_t st = (hipStream_t)stream;
     plan_begin(st);
     HIP_TRY(moe::launch_balance(logits, (int)lt, ld, T, E, k, topk_idx, b, loss, z, prob, counts, tokens, ws, st));
-    plan_step("balance", st);
     return MOE_OK;
   } catch (...) {
     return MOE_ERR_INTERNAL;
@@ -1031,7 +1038,6 @@ moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, int64_t l
     plan_begin(st);
     HIP_TRY(moe::launch_balance_backward(logits, (int)lt, ld, T, E, k, b, counts, tokens, grad_loss, grad_z,
                                          grad_logits, ld_grad, st));
-    plan_step("balance_backward", st);
     return MOE_OK;
   } catch (...) {
     return MOE_ERR_INTERNAL;
@@ -1090,7 +1096,6 @@ moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const
     hipStream_t st = (hipStream_t)stream;
     plan_begin(st);
     HIP_TRY(moe::launch_linear(x, (int)dt, ldx, T, dense->w, dense->ldw, N, K, e, (float*)ws, st));
-    plan_step("linear", st);
     return MOE_OK;
   } catch (...) {
     return MOE_ERR_INTERNAL;
@@ -1163,7 +1168,6 @@ moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_g
     HIP_TRY(moe::launch_linear_backward(g, (int)dt, x, ldx, dense->w, dense->ldw, K, T ? grad_x : nullptr, ld_grad_x,
                                         grad_w, ld_grad_w, grad_bias, grad_row_scale, dz, direct ? ld_grad : L.ldz,
                                         (float*)(W + L.part), st));
-    plan_step("linear_backward", st);
     return MOE_OK;
   } catch (...) {
     return MOE_ERR_INTERNAL;
