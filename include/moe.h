@@ -579,7 +579,8 @@ moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, int64_t l
  *   bias  [N] of type bias_dt (x's or MOE_F32), or NULL
  * Sums, the activation and the epilogue are fp32; one rounding gives out.
  *   K % 8 == 0; ldw % 8 == 0; w 16-byte aligned; K and N at least 1, all of K, N
- *   and the row distances at most MOE_LINEAR_MAX_COLUMNS
+ *   and the row distances at most MOE_LINEAR_MAX_COLUMNS; T N, T K and N K at most
+ *   2^38
  */
 #define MOE_LINEAR_MAX_COLUMNS (1 << 22)
 typedef enum {

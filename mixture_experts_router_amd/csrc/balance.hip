@@ -145,6 +145,17 @@ __device__ __forceinline__ float scores(f32x4 (&l)[NB], f32x4 (&q)[NB], float& i
   }
 }
 
+// A row whose sum is NaN (a NaN or +inf logit): NaN for every expert that is not
+// masked, also where its exponential had vanished
+template <int LT, int NB>
+__device__ __forceinline__ void spread_nan(const void* logits, int64_t at, int E, int vec, int i16, f32x4 (&p)[NB]) {
+  load_row<LT, NB>(logits, at, E, vec, true, i16, p);
+#pragma unroll
+  for (int c = 0; c < NB; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[c][j] = p[c][j] == -INFINITY ? 0.0f : NAN;
+}
+
 // first sequence that ends after token t: offsets[s] <= t < offsets[s + 1] if the token is in one
 __device__ __forceinline__ int sequence_of(const int32_t* offsets, int S, int64_t t) {
   int lo = 0, hi = S;
@@ -207,11 +218,13 @@ __device__ __forceinline__ void sum_tokens(const void* logits, int64_t ld, int v
     n += live;
 #pragma unroll
     for (int c = 0; c < NB; ++c) p[c] = next[c];
+    const int64_t at = t * ld;
     t += ROWS;
     live = t < to && (!mask || mask[t] != 0);
     load_row<LT, NB>(logits, t * ld, E, vec, live, i16, next);
     float inv;
     const float lse = scores<NB, SOFTMAX, false>(p, q, inv);
+    if (inv != inv) spread_nan<LT, NB>(logits, at, E, vec, i16, p);
 #pragma unroll
     for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -457,6 +470,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const void* __res
     const bool live = was && t >= s_from && t < s_to;
     float inv;
     const float lse = scores<NB, SOFTMAX, true>(p, q, inv);
+    if (inv != inv) spread_nan<LT, NB>(logits, t * ld, E, vec, i16, p);
     float dot = 0.0f;
 #pragma unroll
     for (int c = 0; c < NB; ++c)
@@ -475,7 +489,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const void* __res
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float d = mul0(p[c][j], g[c][j] + add);
-        if (!SOFTMAX) d = mul0(d, q[c][j]);
+        if (!SOFTMAX) d *= q[c][j];
         v[j] = live ? d : 0.0f;
       }
       if (vec_out) {

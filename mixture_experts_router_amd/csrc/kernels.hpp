@@ -31,6 +31,8 @@ void note_launch(const char* name);
 template <typename... KArgs, typename... Args>
 inline hipError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, uint32_t lds, hipStream_t st,
                                 Args... args) {
+  // a launch of 2^32 threads or more runs only a part of them, and reports no error
+  if ((uint64_t)grid.x * block.x >= (uint64_t(1) << 32)) return hipErrorInvalidConfiguration;
   hipEvent_t a = nullptr, b = nullptr;
   if (next_launch_events(&a, &b))
     hipExtLaunchKernelGGL(kernel, grid, block, lds, st, a, b, 0, static_cast<KArgs>(args)...);

@@ -955,6 +955,7 @@ __global__ __launch_bounds__(1024) void linear_sums_kernel(const float* __restri
 // -------------------------------------------------------------- launchers --
 
 constexpr int CUS = 256;
+constexpr int64_t MAX_GRID = 1 << 22;  // workgroups of up to 512 threads: a launch has fewer than 2^32 threads
 
 struct Plan {
   int bm, bn;  // rows and columns of a tile
@@ -977,6 +978,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const double bytes_us = (double)((M + N) * K) * 2.0 / 5.0e6;
   auto offer = [&](int bm, int bn, int64_t at_once, double step, double ends, int64_t splits) {
     const int64_t work = ((M + bm - 1) / bm) * ((N + bn - 1) / bn) * splits;
+    if (work > MAX_GRID && bm * bn < 256 * 256) return;
     const int64_t share = (steps + splits - 1) / splits;
     double us = std::max((double)((work + at_once - 1) / at_once) * ((double)share * step + ends), bytes_us + ends);
     if (splits > 1) us += 3.5 + (double)(splits * M * N) * 4.0 / 2.5e6;
@@ -1059,6 +1061,7 @@ StreamPlan stream_plan(int64_t T, int64_t N, int64_t K, bool gated) {
   };
   const int h = T > 16 && bytes(2) < bytes(1) && ((T + 31) / 32) * ((N + 16 * g - 1) / (16 * g)) >= CUS ? 2 : 1;
   const double us = 2.5 + std::max((double)bytes(h) / 9.0e6, 0.5 * (double)((K + 511) / 512));
+  if (((T + 16 * h - 1) / (16 * h)) * ((N + 16 * g - 1) / (16 * g)) > MAX_GRID) return StreamPlan{0, 0};
   return us <= plan_of(T, N, K).us ? StreamPlan{g, h} : StreamPlan{0, 0};
 }
 

@@ -348,7 +348,9 @@ moe_status check_balance_opts(const moe_balance_opts* o, moe::BalanceDev* b) {
   return MOE_OK;
 }
 
-constexpr int64_t kMaxElements = int64_t(1) << 40;  // of a matrix that moe_linear reads or writes
+// of a matrix that moe_linear reads or writes: more than the device holds, and few
+// enough tiles for one launch
+constexpr int64_t kMaxElements = int64_t(1) << 38;
 
 // sizes of a dense product; what is read of it is checked by the callers
 moe_status check_dense(const moe_dense* d, moe_dtype dt, int T) {

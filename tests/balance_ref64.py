@@ -81,6 +81,7 @@ def gradient(l, counts, tokens, grad_loss, grad_z, k, score, dtype, offsets=None
         v = np.where(p != 0, p * (g - dot + zt) * rest, 0.0)
         out[at] = v
         # p and every term of the bracket to 128 U and the rounding of each step; the sum of 256 products 24 U more
-        mag = p * (np.abs(g) + (np.abs(g) * p).sum(1, keepdims=True) + np.abs(zt)) * rest
+        terms = np.abs(g) + (np.abs(g) * p).sum(1, keepdims=True) + np.abs(zt)
+        mag = np.where(p != 0, p * terms * rest, 0.0)
         bound[at] = 300 * U * mag + HALF[dtype] * np.abs(v) + TINY[dtype]
     return out, bound

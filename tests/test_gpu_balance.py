@@ -36,8 +36,11 @@ def check(l, idx, score, dtype="f32", offsets=None, mask=None, seed=0, dev=None)
         if n in ("counts", "tokens"):
             assert v.dtype == np.int32 and np.array_equal(v, want[n]), n
             continue
-        fine = np.isfinite(want[n])
-        assert np.array_equal(np.isnan(v), np.isnan(want[n])), n
+        with np.errstate(over="ignore"):
+            stored = want[n].astype(np.float32)  # beyond the type's largest value: infinite
+        fine = np.isfinite(stored)
+        assert np.array_equal(np.isnan(v), np.isnan(stored)), n
+        assert np.array_equal(np.isinf(v), np.isinf(stored)), n
         assert np.all(np.abs(v - want[n])[fine] <= bound[n][fine]), (n, np.abs(v - want[n]).max())
     S = len(want["loss"])
     rng = np.random.default_rng(seed)
@@ -141,6 +144,25 @@ def test_nan_and_infinity_stay_in_their_sequence():
                                   offsets=offsets.cuda())
     rows = g.isnan().any(1).nonzero().flatten().tolist()
     assert rows == [10, 50] and g[10, 4] == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [40, 700])
+def test_nan_reaches_every_expert_of_its_row_but_the_masked(T, score):
+    """Also those whose exponential vanishes beside the row's maximum, or whose sigmoid is 0; compared element by
+    element (sums, gradients and where they are NaN) with the formula."""
+    l, idx = make(80, T, 70, 4)
+    l[3, 5], l[3, 60] = np.inf, -np.inf
+    l[9, 0], l[9, 8], l[9, 69] = np.nan, 3e38, -np.inf
+    l[20] = -3e38
+    l[20, 33] = 3e38
+    if score == "softmax":
+        l[21, 2] = 200.0  # the others vanish: 0, not NaN
+    offsets = torch.tensor([0, 8, 15, T], dtype=torch.int32)
+    got, grad = check(l, idx, score, offsets=offsets)
+    inf = 69 if score == "softmax" else 0  # the sigmoid of +inf is 1
+    assert [int(got["prob"][s].isnan().sum()) for s in range(3)] == [inf, 69, 0]
+    assert [int(grad[t].isnan().sum()) for t in (3, 9, 20)] == [inf, 69, 0]
 
 
 def test_rows_of_a_wider_tensor_and_outputs_in_place():
@@ -291,3 +313,29 @@ def test_streams_and_graphs():
         assert torch.equal(g, moe.balance_loss_backward(l2.cuda(), want["counts"], want["tokens"], one, 4))
         torch.cuda.synchronize()
     del eager
+
+
+def test_very_many_tokens_and_sequences():
+    T = (1 << 24) + 3
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    l = torch.randn(T, 4, generator=g, device="cuda")
+    idx = torch.randint(0, 4, (T, 2), generator=g, device="cuda", dtype=torch.int32)
+    r = moe.balance_loss(l, idx)
+    p = torch.softmax(l.double(), 1)
+    counts = torch.bincount(idx.reshape(-1), minlength=4)
+    prob, z = p.mean(0), (torch.logsumexp(l.double(), 1) ** 2).mean()
+    # chunks of T / 512 tokens, 32 at a time: T / 16384 + 300 additions of positive terms, and 128 of a probability
+    steps = (T / 16384 + 428) * ref.U
+    assert torch.equal(r["counts"][0].long(), counts) and int(r["tokens"][0]) == T
+    assert bool(((r["prob"][0].double() - prob).abs() <= steps * prob).all())
+    assert abs(float(r["loss"][0]) - float(4 / (2 * T) * (counts.double() * prob).sum())) <= steps * 2
+    assert abs(float(r["z"][0]) - float(z)) <= (steps + 300 * ref.U) * float(z) + 300 * ref.U
+    one = torch.ones(1, device="cuda")
+    d = moe.balance_loss_backward(l, r["counts"], r["tokens"], one, 2)
+    slope = 4 / (2.0 * T * T) * counts.double()
+    want = p * (slope - (p @ slope)[:, None])
+    assert bool(((d.double() - want).abs() <= 300 * ref.U * p * 2 * slope.max()).all())
+    # a sequence for every token
+    l, idx = make(16, 20000, 8, 2)
+    check(l, idx, "softmax", offsets=torch.arange(20001, dtype=torch.int32))

@@ -110,3 +110,28 @@ def test_plans_of_the_balance_loss():
     assert moe.last_plan() == ["balance_part", "balance_join"]
     moe.balance_loss_backward(l, r["counts"], r["tokens"], r["loss"], 1)
     assert moe.last_plan() == ["balance_backward"]
+
+
+def test_very_many_tokens():
+    """Millions of rows of a few columns; outputs of more than 2^32 elements."""
+    T = (1 << 22) + 37
+    x = rand(1, T, 8).bfloat16()
+    w = rand(2, 3, 8).bfloat16()
+    got = moe.linear(x, w, out_dtype=torch.float32)
+    want, bound, *_ = ref.forward(x, w, out_dtype=torch.float32)
+    near(got, want, bound)
+    g = rand(3, T, 3)
+    r = moe.linear_backward(g, x, w, want=("x", "w", "bias"))
+    exact = ref.backward(g, x, w)
+    for n in r:
+        near(r[n], *exact[n], n)
+    del want, bound, exact
+    T, N = 2_100_000, 2100  # 4.4e9 elements, rows that do not start aligned
+    x, w = rand(4, T, 8).bfloat16(), rand(5, N, 8).bfloat16()
+    out = moe.linear(x, w)
+    for rows in (slice(0, 40), slice(T // 2, T // 2 + 40), slice(T - 40, T)):
+        want, bound, *_ = ref.forward(x[rows], w)
+        near(out[rows], want, bound)
+    back = moe.linear_backward(out, x, w, want=("x", "bias"))
+    for rows in (slice(0, 40), slice(T - 40, T)):
+        near(back["x"][rows], *ref.backward(out[rows], x[rows], w)["x"], "x")
