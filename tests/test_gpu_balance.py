@@ -334,7 +334,7 @@ def test_very_many_tokens_and_sequences():
     one = torch.ones(1, device="cuda")
     d = moe.balance_loss_backward(l, r["counts"], r["tokens"], one, 2)
     slope = 4 / (2.0 * T * T) * counts.double()
-    want = p * (slope - (p @ slope)[:, None])
+    want = p * (slope - (p * slope).sum(1, keepdim=True))  # (a library product of so many rows is wrong at its end)
     assert bool(((d.double() - want).abs() <= 300 * ref.U * p * 2 * slope.max()).all())
     # a sequence for every token
     l, idx = make(16, 20000, 8, 2)
