@@ -272,11 +272,11 @@ __device__ __forceinline__ void finish(const LinearEpi& e, int64_t t, int n, flo
 //
 // A wave of the 256 x 256 tile (eight waves of 128 x 64) reads 12 KB of LDS for
 // 512 cycles of MFMAs, so LDS keeps up; the MFMAs run 62% of the cycles, at about
-// 1.9 GHz under the card's power limit (operands of zeros take 215 us where
-// others take 273).  8192^3 in 782 us, 1406 TFLOP/s; 4096 x 11008 to 4096 in 270
-// us from the caches, 1370 TFLOP/s (292 us with a residual and other operands
+// 1.9 GHz under the card's power limit (operands of zeros took 215 us where
+// others took 273).  8192^3 in 769 us, 1429 TFLOP/s; 4096 x 11008 to 4096 in 261
+// us from the caches, 1414 TFLOP/s (286 us with a residual and other operands
 // each time); smaller tiles wait for LDS: 128 x 128 needs it for 768 cycles a
-// step of 512 cycles of MFMAs (777 x 4096 to 2816 30 us).
+// step of 512 cycles of MFMAs (777 x 4096 to 2816 28 us).
 //
 // Offsets: a descriptor starts at the tile's first element (64-bit), so that
 // offsets within it stay below 2^31; rows, columns and k past the operand's end
@@ -458,23 +458,22 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
     if (i < NIA) la.template issue<false>(i, wave * NIA, st);
     else lb.template issue<GATED>(i - NIA, wave * NIB, st + A_BYTES);
   };
-  // half h of the wave's rows, and its columns, at k-step j
-  auto read_a = [&](const uint8_t* st, int j, int h, u32x4 (&af)[MH]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int mi = 0; mi < MH; ++mi) af[mi] = LA::read(st, (wm * MB + h * MH + mi) * 16, kh * JW + j, lane);
+  // fragment i of half h of the wave's rows, and of its columns, at k-step j
+  auto read_a = [&](const uint8_t* st, int j, int h, int i, u32x4 (&af)[MH]) __attribute__((always_inline)) {
+    af[i] = LA::read(st, (wm * MB + h * MH + i) * 16, kh * JW + j, lane);
   };
-  auto read_b = [&](const uint8_t* st, int j, u32x4 (&bf)[NB]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int ni = 0; ni < NB; ++ni) bf[ni] = LB::read(st + A_BYTES, (wn * NB + ni) * 16, kh * JW + j, lane);
+  auto read_b = [&](const uint8_t* st, int j, int i, u32x4 (&bf)[NB]) __attribute__((always_inline)) {
+    bf[i] = LB::read(st + A_BYTES, (wn * NB + i) * 16, kh * JW + j, lane);
   };
 
-  // A k-step's MFMAs run in two halves of the wave's rows; a half's fragments
-  // are read one half ahead.  Before the last half of a stage its reads are
-  // complete: one wait for the next stage's loads and one barrier, after which
-  // the next stage's first fragments are read, and the loads that refill this
-  // stage NS steps ahead go out between the last MFMAs, so that neither waits
-  // for the other.  16 x 16 x 32 products: 8% faster than 32 x 32 x 16 at 8192^3,
-  // where the card's power sets the clock (four waves of 128 x 128 gained nothing).
+  // A k-step's MFMAs run in two halves of the wave's rows; the next half's
+  // fragments are read behind the first of them.  Before the last half of a stage
+  // its reads are complete: one wait for the next stage's loads and one barrier,
+  // after which the next stage's first fragments are read, and the loads that
+  // refill this stage NS steps ahead go out, behind one MFMA each.  (All reads
+  // before a half's MFMAs: 777 x 4096 to 2816 30.3 against 27.8 us, 4096 x 11008
+  // 267 against 261.)  16 x 16 x 32 products: 8% faster than 32 x 32 x 16 at
+  // 8192^3, where the card's power sets the clock; four waves of 128 x 128 spill.
   if (steps > 0) {
     u32x4 af[2][MH], bf[2][NB];
     for_each<0, NS>([&](auto S_) __attribute__((always_inline)) {
@@ -486,8 +485,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
     });
     wait_vmcnt<(NS - 1) * LOADS>();
     __builtin_amdgcn_s_barrier();
-    read_b(st0, 0, bf[0]);
-    read_a(st0, 0, 0, af[0]);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) read_b(st0, 0, n, bf[0]);
+#pragma unroll
+    for (int n = 0; n < MH; ++n) read_a(st0, 0, 0, n, af[0]);
     auto step = [&](auto S_, int i) __attribute__((always_inline)) {
       constexpr int S = decltype(S_)::value, N = (S + 1) % NS;
       constexpr int B0 = KS == 1 ? 0 : S & 1;  // the columns' registers of the first k-step
@@ -497,31 +498,36 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
       for_each<0, HALVES>([&](auto H_) __attribute__((always_inline)) {
         constexpr int hf = decltype(H_)::value, j = hf / 2, B = (B0 + j) & 1;
         constexpr bool last = hf == HALVES - 1;
-        if constexpr (!last) {
-          if constexpr (hf % 2 == 1) read_b(st, j + 1, bf[B ^ 1]);
-          read_a(st, (hf + 1) / 2, (hf + 1) % 2, af[(hf + 1) & 1]);
-        } else {
+        if constexpr (last) {
           wait_vmcnt<(NS - 2) * LOADS>();      // this wave's loads of the next step have landed
           __builtin_amdgcn_s_waitcnt(0xC07F);  // and its reads of this stage (lgkmcnt 0)
           __builtin_amdgcn_s_barrier();
           __builtin_amdgcn_sched_barrier(0);
           begin(i + NS);
-          read_b(stage(IC<N>{}), 0, bf[B ^ 1]);
-          read_a(stage(IC<N>{}), 0, 0, af[0]);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t* from = last ? stage(IC<N>{}) : st;
+        constexpr int jn = last ? 0 : (hf + 1) / 2, hn = last ? 0 : (hf + 1) % 2;
+        constexpr int NRB = last || hf % 2 == 1 ? NB : 0, READS = NRB + MH;
         constexpr int MMAS = MH * NB;
-#pragma unroll
-        for (int m = 0; m < MMAS; ++m) {
+        for_each<0, MMAS>([&](auto M_) __attribute__((always_inline)) {
+          constexpr int m = decltype(M_)::value;
           f32x4& c = acc[(hf % 2) * MH + m / NB][m % NB];
           c = mfma16<DT>(af[hf & 1][m / NB], bf[B][m % NB], c);
+          __builtin_amdgcn_sched_barrier(0);
+          constexpr int r0 = 2 * m * READS / MMAS, r1 = 2 * (m + 1) * READS / MMAS;
+          for_each<(r0 < READS ? r0 : READS), (r1 < READS ? r1 : READS)>([&](auto R_) __attribute__((always_inline)) {
+            constexpr int r = decltype(R_)::value;
+            if constexpr (r < NRB) read_b(from, jn, r, bf[B ^ 1]);
+            else read_a(from, jn, hn, r - NRB, af[last ? 0 : (hf + 1) & 1]);
+            return true;
+          });
           if constexpr (last) {
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int l = m * LOADS / MMAS; l < (m + 1) * LOADS / MMAS; ++l) issue(S_, l);
-            __builtin_amdgcn_sched_barrier(0);
           }
-        }
+          __builtin_amdgcn_sched_barrier(0);
+          return true;
+        });
         __builtin_amdgcn_sched_barrier(0);
         return true;
       });
