@@ -272,9 +272,9 @@ __device__ __forceinline__ void finish(const LinearEpi& e, int64_t t, int n, flo
 //
 // A wave of the 256 x 256 tile (eight waves of 128 x 64) reads 12 KB of LDS for
 // 512 cycles of MFMAs, so LDS keeps up; the MFMAs run 62% of the cycles, at about
-// 1.9 GHz under the card's power limit (operands of zeros took 215 us where
-// others took 273).  8192^3 in 769 us, 1429 TFLOP/s; 4096 x 11008 to 4096 in 261
-// us from the caches, 1414 TFLOP/s (286 us with a residual and other operands
+// 1.9 GHz under the card's power limit (operands of zeros took 205 us where
+// others took 258).  8192^3 in 745 us, 1475 TFLOP/s; 4096 x 11008 to 4096 in 258
+// us from the caches, 1431 TFLOP/s (282 us with a residual and other operands
 // each time); smaller tiles wait for LDS: 128 x 128 needs it for 768 cycles a
 // step of 512 cycles of MFMAs (777 x 4096 to 2816 28 us).
 //
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
   // after which the next stage's first fragments are read, and the loads that
   // refill this stage NS steps ahead go out, behind one MFMA each.  (All reads
   // before a half's MFMAs: 777 x 4096 to 2816 30.3 against 27.8 us, 4096 x 11008
-  // 267 against 261.)  16 x 16 x 32 products: 8% faster than 32 x 32 x 16 at
+  // 267 against 255.)  16 x 16 x 32 products: 8% faster than 32 x 32 x 16 at
   // 8192^3, where the card's power sets the clock; four waves of 128 x 128 spill.
   if (steps > 0) {
     u32x4 af[2][MH], bf[2][NB];
@@ -972,12 +972,15 @@ struct Plan {
 // The tile and the split of k of a product M x N over K: the least of what the
 // forms are expected to take, rounds of workgroups times (steps of a share times
 // us a step, or the operands' bytes at 5 TB/s, and us to begin and to finish),
-// and the join of the shares.  Measured us a step of 64 k: 256 x 256 1.6, 192 x
-// 256 1.33, 128 x 256 0.95, 128 x 128 0.45 (154 workgroups) to 0.5 (256); 64 x 64
-// 0.25 to 0.45 (512, two a CU).  Results against a fixed tile of 128 in
-// brackets, us: 64 x 2816 to 4096 11.3 (15.1), 777 x 4096 to 2816 30 (30),
-// 2048 x 4096 to 4096 64 (77), 4096 x 11008 to 4096 273 (450).
-Plan plan_of(int64_t M, int64_t N, int64_t K) {
+// and the join of the shares.  Measured us a step of 64 k: 256 x 256 1.52, 192 x
+// 256 1.25, 128 x 256 0.9, 192 x 128 0.66, 128 x 128 0.45 (154 workgroups) to 0.5
+// (256); 64 x 64 0.25 to 0.45 (512, two a CU).  Gated, the waves' 32 gate and 32 up
+// columns leave four waves for 192 x 128, too few (1237 x 4096 to 2 x 2048 55 us
+// against 52 with 128 x 256).  Results against a fixed tile of 128 in brackets, us:
+// 64 x 2816 to 4096 11.6 (15.1), 2048 x 4096 to 4096 63 (77), 4096 x 11008 to 4096
+// 255 (450); against 128 x 256 1237 x 4096 to 4096 48 (54), 8192 x 4096 to 1408 97
+// (112 with 128 x 128).
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated = false) {
   Plan p{128, 128, 1, 0.0};
   if (M < 1 || N < 1) return p;
   const int64_t steps = (K + 63) / 64;
@@ -990,9 +993,10 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
     if (splits > 1) us += 3.5 + (double)(splits * M * N) * 4.0 / 2.5e6;
     if (p.us == 0.0 || us < p.us) p = Plan{bm, bn, (int)splits, us};
   };
-  offer(256, 256, CUS, 1.6, 6.0, 1);
-  offer(192, 256, CUS, 1.33, 5.5, 1);
-  offer(128, 256, CUS, 0.95, 5.0, 1);
+  offer(256, 256, CUS, 1.52, 8.0, 1);
+  offer(192, 256, CUS, 1.25, 7.5, 1);
+  offer(128, 256, CUS, 0.9, 6.0, 1);
+  if (!gated) offer(192, 128, CUS, 0.66, 6.0, 1);
   const int64_t wide = ((M + 127) / 128) * ((N + 127) / 128), small = ((M + 63) / 64) * ((N + 63) / 64);
   auto filled = [](int64_t work, int64_t at_once) { return (double)std::min(work, at_once) / (double)at_once; };
   for (int64_t s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32}) {
@@ -1012,7 +1016,7 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
   prm.K = K;
   prm.e = e;
   prm.part = part;
-  const Plan p = plan_of(a.n, N, K);
+  const Plan p = plan_of(a.n, N, K, GATED);
   const bool split = p.splits > 1;
   if (split && !part) return hipErrorInvalidValue;
   const int64_t steps = (K + 63) / 64;
@@ -1033,6 +1037,10 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
     return launch_kernel(kern, grid, threads, 0, st, prm);
   };
   if (p.bm == 256) return go("linear_256x256", linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 1, 2>, 512);
+  if constexpr (!GATED) {
+    if (p.bm == 192 && p.bn == 128)
+      return go("linear_192x128", linear_tile_kernel<DT, TA, TB, false, 192, 128, 2, 4, 1, 4>, 512);
+  }
   if (p.bm == 192) return go("linear_192x256", linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 1, 2>, 512);
   if (p.bn == 256) return go("linear_128x256", linear_tile_kernel<DT, TA, TB, GATED, 128, 256, 2, 4, 1, 3>, 512);
   if (!split && p.bm == 128) return go("linear_128x128", linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2, 4>, 512);
@@ -1068,7 +1076,7 @@ StreamPlan stream_plan(int64_t T, int64_t N, int64_t K, bool gated) {
   const int h = T > 16 && bytes(2) < bytes(1) && ((T + 31) / 32) * ((N + 16 * g - 1) / (16 * g)) >= CUS ? 2 : 1;
   const double us = 2.5 + std::max((double)bytes(h) / 9.0e6, 0.5 * (double)((K + 511) / 512));
   if (((T + 16 * h - 1) / (16 * h)) * ((N + 16 * g - 1) / (16 * g)) > MAX_GRID) return StreamPlan{0, 0};
-  return us <= plan_of(T, N, K).us ? StreamPlan{g, h} : StreamPlan{0, 0};
+  return us <= plan_of(T, N, K, gated).us ? StreamPlan{g, h} : StreamPlan{0, 0};
 }
 
 template <int DT, bool GATED>
@@ -1145,16 +1153,18 @@ hipError_t backward(const LinearGrad& g, const void* x, int64_t ldx, const void*
 
 }  // namespace
 
-int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K);
-int64_t linear_forward_bytes(int64_t T, int64_t N, int64_t K) {
-  // gated and not: the larger
-  return stream_plan(T, N, K, false).g && stream_plan(T, N, K, true).g ? 0 : linear_part_bytes(T, N, K);
-}
-
-int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K) {
-  const Plan p = plan_of(M, N, K);
+static int64_t part_bytes(const Plan& p, int64_t M, int64_t N) {
   return p.splits > 1 ? (int64_t)p.splits * M * part_row(N) * 4 : 0;
 }
+
+int64_t linear_forward_bytes(int64_t T, int64_t N, int64_t K) {
+  int64_t bytes = 0;  // gated and not: the larger
+  for (bool gated : {false, true})
+    if (!stream_plan(T, N, K, gated).g) bytes = std::max(bytes, part_bytes(plan_of(T, N, K, gated), T, N));
+  return bytes;
+}
+
+int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K) { return part_bytes(plan_of(M, N, K), M, N); }
 
 hipError_t launch_linear(const void* x, int dt, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K,
                          const LinearEpi& e, float* part, hipStream_t st) {

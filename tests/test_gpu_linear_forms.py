@@ -21,6 +21,8 @@ FORWARD = [
     (501, 72, 9002, "linear_128x256", "linear_128x256"), (501, 264, 9016, "linear_128x256", "linear_128x256"),
     (3001, 72, 2602, "linear_192x256", "linear_192x256"), (3001, 200, 2608, "linear_192x256", "linear_192x256"),
     (2501, 72, 5002, "linear_256x256", "linear_256x256"), (2501, 328, 4992, "linear_256x256", "linear_256x256"),
+    (1237, 1096, 4010, "linear_192x128", None), (1333, 2056, 4000, "linear_192x128", None),
+    (2001, 72, 4002, "linear_128x256", "linear_128x256"), (2001, 328, 4008, "linear_128x256", "linear_128x256"),
 ]
 
 
@@ -59,6 +61,8 @@ PRODUCTS = [
     (203, 9000, 77, "linear_128x128"), (70, 3304, 4103, "linear_128x128+join"), (501, 9016, 201, "linear_128x256"),
     (3001, 2608, 70, "linear_192x256"), (3001, 2600, 301, "linear_192x256"), (2501, 5000, 65, "linear_256x256"),
     (2501, 4992, 333, "linear_256x256"), (5, 8, 3, "linear_64x64"),
+    (1237, 4008, 1029, "linear_192x128"), (1333, 4000, 2051, "linear_192x128"),
+    (2001, 4008, 201, "linear_128x256"),
 ]
 
 
