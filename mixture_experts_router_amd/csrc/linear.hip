@@ -271,7 +271,7 @@ __device__ __forceinline__ void finish(const LinearEpi& e, int64_t t, int n, flo
 // the registers.
 //
 // A wave of the 256 x 256 tile (eight waves of 128 x 64) reads 12 KB of LDS for
-// 512 cycles of MFMAs, so LDS keeps up; the MFMAs run 62% of the cycles, at about
+// 512 cycles of MFMAs, so LDS keeps up; the MFMAs run 58% of the cycles, at about
 // 1.9 GHz under the card's power limit (operands of zeros took 205 us where
 // others took 258).  8192^3 in 745 us, 1475 TFLOP/s; 4096 x 11008 to 4096 in 258
 // us from the caches, 1431 TFLOP/s (282 us with a residual and other operands
