@@ -654,9 +654,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
         if (prm.e.res) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const uint32_t h = here.v[it][0][j / 2];
-            z[j] += prm.e.out_f32 ? __builtin_bit_cast(float, here.v[it][j / 4][j % 4])
-                                  : half_to_f32<DT>(j % 2 ? h >> 16 : h & 0xFFFFu);
+            // (a bit cast of a vector's element itself gives element 0)
+            const uint32_t h = here.v[it][0][j / 2], f = here.v[it][j / 4][j % 4];
+            z[j] += prm.e.out_f32 ? __builtin_bit_cast(float, f) : half_to_f32<DT>(j % 2 ? h >> 16 : h & 0xFFFFu);
           }
         }
         store_n<DT, 8>(prm.e.out, prm.e.out_f32, (t0 + r) * prm.e.ldo + w0 + c, 8, true, z);
