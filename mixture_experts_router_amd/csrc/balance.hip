@@ -116,8 +116,7 @@ __device__ __forceinline__ float scores(f32x4 (&l)[NB], f32x4 (&q)[NB], float& i
 #pragma unroll
     for (int c = 0; c < NB; ++c) m = fmaxf(m, fmaxf(fmaxf(l[c].x, l[c].y), fmaxf(l[c].z, l[c].w)));
     m = max16(m);
-    const bool none = m == -INFINITY;
-    m = none ? 0.0f : m;
+    m = m == -INFINITY ? 0.0f : m;  // nothing but masked experts, or NaN (fmaxf passes it over)
 #pragma unroll
     for (int c = 0; c < NB; ++c)
 #pragma unroll
@@ -127,7 +126,7 @@ __device__ __forceinline__ float scores(f32x4 (&l)[NB], f32x4 (&q)[NB], float& i
       }
     sum = sum16(sum);
     inv = __builtin_amdgcn_rcpf(sum);
-    return none ? 0.0f : m + __builtin_amdgcn_logf(sum) * LN2;
+    return sum == 0.0f ? 0.0f : m + __builtin_amdgcn_logf(sum) * LN2;  // a NaN's sum is NaN
   } else {
 #pragma unroll
     for (int c = 0; c < NB; ++c)
