@@ -583,6 +583,7 @@ moe_status moe_balance_loss_backward(const void* logits, moe_dtype lt, int64_t l
  *   2^38
  */
 #define MOE_LINEAR_MAX_COLUMNS (1 << 22)
+#define MOE_LINEAR_TWO_PARTS 256
 typedef enum {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,
@@ -620,13 +621,17 @@ moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const
 /*
  * Its gradients, from g = d loss / d out [T, C] of type grad_dt (dt or MOE_F32):
  *
- *   dz = row_scale * g * act'(preact), rounded to dt where it enters the products
+ *   dz = row_scale * g * act'(preact)
  *   grad_x [T, K] = dz W,  grad_w [N, K] = dz^T x      in dt
  *   grad_bias [N] = sum_t dz,  grad_row_scale [T] = sum_c g act(preact)    fp32
  * (the residual's gradient is g).  Each output may be NULL.  preact [T, N] as
  * moe_linear kept it; it may be NULL with act none where grad_row_scale is NULL.
  * dense->bias is not read; w is read for grad_x only and may be NULL without,
- * and so x for grad_w.  Outputs overlap nothing.  T == 0 writes zeros to grad_w
+ * and so x for grad_w.  dz enters the two products in dt's bits: rounded once, but
+ * for an fp32 gradient with MOE_F16, or with MOE_BF16 and N up to
+ * MOE_LINEAR_TWO_PARTS (a router's experts).  Then it enters in two parts, off by at
+ * most 2^-15 of it (MOE_BF16), or by 2^-20 of it between 2^-6 and 2^13, outside by
+ * 2^-11 of it or 2^-35, the larger, and infinite above 1.6e7 (MOE_F16).  Outputs overlap nothing.  T == 0 writes zeros to grad_w
  * and grad_bias.
  *   ws  moe_linear_backward_workspace_size(T, N, K) bytes, 16-byte aligned
  */

@@ -1013,7 +1013,9 @@ def linear_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, act
     [T, K] and w [N, K] in x's type, bias [N] and row_scale [T] float32.  grad in
     x's type or float32, preact as linear kept it (act "none" without the
     gradient of row_scale needs none), act and row_scale as in the forward call.
-    The residual's gradient is grad itself.  The results have no graph."""
+    The residual's gradient is grad itself.  The results have no graph.  What a
+    float32 grad holds beyond 16 bits reaches the products for float16 operands,
+    and for bfloat16 ones of up to 256 columns (moe_linear_backward)."""
     if not _here(x, stream):
         with _elsewhere(x, stream):
             return linear_backward(grad, x, w, act=act, preact=preact, row_scale=row_scale, want=want)

@@ -216,6 +216,7 @@ struct LinearGrad {
   const void* z;  // [T, N] in the operands' type, rows ldz_in apart; NULL: act is LIN_NONE
   const float* rs;
   uint16_t* dz;  // [T, ldz] out, or NULL
+  int64_t low;   // elements from dz to its second part, written likewise (0: dz is one part)
   float* part;      // column sums of the row blocks [blocks, N], or NULL
   float* row_part;  // row sums of the column blocks [column_blocks, T], or NULL
   int64_t ldg, ldz_in, ldz, T;
@@ -226,14 +227,15 @@ struct LinearGrad {
 };
 constexpr int LINEAR_DZ_ROWS = 64;
 
-// bytes of the partial sums of a product [M, N] over K (0: none)
-int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K);
+// bytes of the partial sums of a product [M, N] over K (0: none), the first operand the sum of `parts`
+int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K, int parts);
 // the same for launch_linear
 int64_t linear_forward_bytes(int64_t T, int64_t N, int64_t K);
 hipError_t launch_linear(const void* x, int dt, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K,
                          const LinearEpi& e, float* part, hipStream_t st);
 // dz: g.dz, or the gradient itself where that is dz (rows ldz apart, ldz % 8 == 0, N values and zeros up to the next
-// multiple of 8).  dx [T, K], dw [N, K], dbias [N] (with g.part), drs [T] (with g.row_part) may be NULL
+// multiple of 8; g.low: in both parts).  dx [T, K], dw [N, K], dbias [N] (with g.part), drs [T] (with g.row_part) may be
+// NULL
 hipError_t launch_linear_backward(const LinearGrad& g, int dt, const void* x, int64_t ldx, const void* w, int64_t ldw,
                                   int K, void* dx, int64_t ldx_out, void* dw, int64_t ldw_out, float* dbias, float* drs,
                                   const uint16_t* dz, int64_t ldz, float* part, hipStream_t st);

@@ -207,6 +207,62 @@ __device__ __forceinline__ void store_n(void* p, bool f32, int64_t at, int left,
   }
 }
 
+// An fp32 gradient's dz in two 16-bit parts of its sign, so that the products keep
+// what its 32 bits hold: rounded once, fp16 loses all that is below 2^-25 (a balance
+// loss's gradient is 1e-8 and less) or above 65504, and a router's gradients in bf16
+// are off by 2.4e-3 where their own rounding is 1.7e-3.  The matrix instructions are
+// twice as many: 36 to 45 us for 4096 x 4096 to 64, at most 30% more up to 256
+// columns; 185 to 320 us for 2816, where bf16 takes one (moe_linear_backward).  The first is dz without its low bits, the second what is left.  fp16: the
+// first holds dz 2^-SHIFT_DZ, the second what is left of that times 2^SHIFT_LOW, in
+// all 2^-37 up to 2^24; where what is left has no room (dz above 2^13), the first is
+// rounded instead.  A second part of 0 is replaced by the smallest that matrix
+// instructions keep, and both have dz's sign, so that an infinite weight or input
+// gives dz's infinity, not NaN.
+constexpr int SHIFT_DZ = 8, SHIFT_LOW = 20;
+
+template <int DT>
+__device__ __forceinline__ void two_parts(float v, uint32_t& first, uint32_t& second) {
+  const uint32_t bits = __builtin_bit_cast(uint32_t, v), sign = bits >> 16 & 0x8000u;
+  if (!(fabsf(v) < INFINITY)) {
+    first = second = pack2<DT>(v, 0.0f) & 0xFFFFu;
+    return;
+  }
+  if constexpr (DT == ACT_BF16) {
+    first = bits >> 16;
+    second = pack2<DT>(v - half_to_f32<DT>(first), 0.0f) & 0xFFFFu;
+    if ((first & 0x7FFFu) && !(second & 0x7FFFu)) second = sign | 0x0080u;
+  } else {
+    const float a = v * (1.0f / (1 << SHIFT_DZ));
+    first = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, 0.0f)) & 0xFFFFu;
+    const float left = (a - half_to_f32<DT>(first)) * (float)(1 << SHIFT_LOW);
+    second = pack2<DT>(left, 0.0f) & 0xFFFFu;
+    if (fabsf(left) > 65504.0f) {
+      first = pack2<DT>(a, 0.0f) & 0xFFFFu;
+      second = sign;
+    }
+    if ((first & 0x7FFFu) && !(second & 0x7FFFu)) second = sign | 1u;
+  }
+}
+
+// eight values in both parts
+template <int DT>
+__device__ __forceinline__ void store_parts(uint16_t* p, int64_t low, int left, bool vec, const float (&v)[8]) {
+  uint32_t a[8], b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) two_parts<DT>(v[j], a[j], b[j]);
+  if (vec) {
+    *(u32x4*)p = u32x4{a[0] | a[1] << 16, a[2] | a[3] << 16, a[4] | a[5] << 16, a[6] | a[7] << 16};
+    *(u32x4*)(p + low) = u32x4{b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) {
+        p[j] = (uint16_t)a[j];
+        p[low + j] = (uint16_t)b[j];
+      }
+  }
+}
+
 // W = 8 or 1 columns from n of output row t from their fp32 sums (gated: u the
 // sums of the up columns).  Everything is fp32 up to the one rounding that gives
 // `out`; the kept z is rounded on its own.  The choices are made once for the
@@ -285,6 +341,7 @@ struct Operand {
   const uint16_t* p;
   int64_t ld;  // elements between rows (of k, or of m)
   int n;       // extent in m (or n)
+  int64_t low = 0;  // elements from p to its second part (0: there is none)
 };
 
 template <bool TR, int R, int NI>
@@ -334,14 +391,15 @@ struct Loader {
       }
     }
   }
-  // The loads of the step k0 .. k0 + 63 up to kend (none of it: zeros, without
-  // memory traffic): their buffers, then load instruction i
+  // The loads of the step k0 .. k0 + 63, of which `end` exist (none of it: zeros,
+  // without memory traffic), `part` elements from the operand's start: their
+  // buffers, then load instruction i
   template <bool GATED>
-  __device__ __forceinline__ void begin(int k0, int kend) {
-    left = kend - k0;
+  __device__ __forceinline__ void begin(int k0, int end, int64_t part = 0) {
+    left = end;
     const uint32_t range = left > 0 ? OUT_OF_RANGE : 0u;
     soff = TR ? 0u : (uint32_t)k0 * 2u;
-    buf = buffer_of(TR ? base + (int64_t)k0 * ld : base, range);
+    buf = buffer_of((TR ? base + (int64_t)k0 * ld : base) + part, range);
     buf2 = buffer_of(GATED ? base2 : base, range);
   }
   template <bool GATED>
@@ -375,7 +433,8 @@ __host__ __device__ constexpr int64_t part_row(int64_t n) { return (n + 7) / 8 *
 
 struct TileParams {
   Operand a, b;
-  int K;
+  int K;         // k of one part
+  int k_all;     // the same, or of both parts, each rounded up to whole steps
   int m_tiles, n_tiles, splits, group_m, per_xcd;
   int k_split;   // k of one split, a multiple of 64
   float* part;   // splits > 1: fp32 sums [splits][M][part_row(N)]
@@ -386,7 +445,9 @@ struct TileParams {
 // KS 2: two waves share a block of C, each half of every stage's k-steps, and
 // add up at the end (a second wave on the SIMD where the tile has only four
 // blocks).
-template <int DT, bool TA, bool TB, bool GATED, int BM, int BN, int WM, int WN, int KS, int NS>
+// PARTS 2: A is the sum of two 16-bit parts, one after the other along k, and B is
+// read twice; the second part first (see two_parts).
+template <int DT, bool TA, bool TB, bool GATED, int BM, int BN, int WM, int WN, int KS, int NS, int PARTS = 1>
 __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileParams prm) {
   constexpr int WAVES = WM * WN * KS;
   constexpr int JW = 2 / KS;  // MFMA k-steps of a stage and wave
@@ -434,8 +495,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
   const int m0 = mt * BM;
   const int c0 = nt * (GATED ? BN / 2 : BN);  // first output column
 
-  const int k_lo = split * prm.k_split, k_hi = min(prm.K, k_lo + prm.k_split);
+  const int k_lo = split * prm.k_split, k_hi = min(prm.k_all, k_lo + prm.k_split);
   const int steps = (k_hi - k_lo + 63) / 64;  // not positive: all sums 0
+  const int k_part = PARTS == 2 ? prm.k_all / 2 : 0;  // where the first part begins
 
   LA la;
   LB lb;
@@ -449,10 +511,25 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
     for (int ni = 0; ni < NB; ++ni) acc[mi][ni] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   auto begin = [&](int step) __attribute__((always_inline)) {
-    const int k0 = k_lo + 64 * step;
-    la.template begin<false>(k0, k_hi);
-    lb.template begin<GATED>(k0, k_hi);
+    int k0 = k_lo + 64 * step, end = k_hi - k0;
+    if constexpr (PARTS == 2) {
+      const bool second = k0 < k_part;
+      k0 -= second ? 0 : k_part;
+      end = min(end, prm.K - k0);
+      la.template begin<false>(k0, end, second ? prm.a.low : 0);
+    } else {
+      la.template begin<false>(k0, end);
+    }
+    lb.template begin<GATED>(k0, end);
   };
+  // fp16's second part is 2^SHIFT times its value: the sums so far, where the first begins
+  auto scale = [&](float by) __attribute__((always_inline)) {
+#pragma unroll
+    for (int mi = 0; mi < MB; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NB; ++ni) acc[mi][ni] *= by;
+  };
+  const int turn = PARTS == 2 ? (k_part - k_lo) / 64 : 0;
   auto issue = [&](auto S_, int i) __attribute__((always_inline)) {  // load i of the step, into stage S
     const uint32_t st = lds_address(stage(S_));
     if (i < NIA) la.template issue<false>(i, wave * NIA, st);
@@ -491,6 +568,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
     for (int n = 0; n < MH; ++n) read_a(st0, 0, 0, n, af[0]);
     auto step = [&](auto S_, int i) __attribute__((always_inline)) {
       constexpr int S = decltype(S_)::value, N = (S + 1) % NS;
+      if constexpr (PARTS == 2 && DT == ACT_F16) {
+        if (i == turn) scale(1.0f / (1 << SHIFT_LOW));
+      }
       constexpr int B0 = KS == 1 ? 0 : S & 1;  // the columns' registers of the first k-step
       static_assert(KS == 1 || NS % 2 == 0, "registers by turns");
       const uint8_t* st = stage(S_);
@@ -544,6 +624,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS, 1) void linear_tile_kernel(TileP
       return true;
     });
   }
+  if constexpr (PARTS == 2 && DT == ACT_F16)
+    scale(k_hi > k_part ? (float)(1 << SHIFT_DZ) : (float)(1 << SHIFT_DZ) / (1 << SHIFT_LOW));
   wait_vmcnt<0>();  // no load into LDS lands after this
   __syncthreads();
 
@@ -848,11 +930,11 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
 // ------------------------------------------------------- gradient of z ----
 //
 // A workgroup takes g.rows rows and 8 g.across columns (gated: of each half), a
-// thread eight columns of every (256 / g.across)-th row.  dz (rounded to the
-// operands' 16 bits: the matrix cores' input) is the operand of both products;
-// the sums of bias and row_scale use it unrounded and go to
-// part[row block][N] and row_part[column block][T], joined in order (one block's
-// are the result).  The last column block writes zeros up to ldz.  Bound by its
+// thread eight columns of every (256 / g.across)-th row.  dz is the
+// operand of both products: rounded to their 16 bits where the gradient that came
+// in has 16 (its own rounding is as large), in two parts where it has 32.  The sums
+// of bias and row_scale use it unrounded and go to part[row block][N] and
+// row_part[column block][T], joined in order (one block's are the result).  The last column block writes zeros up to ldz.  Bound by its
 // bytes: 58 MB of 4096 x 2 x 1408 in 16 us, 3.6 TB/s (one column block a
 // workgroup of 16 rows: 60 us).
 template <int DT>
@@ -896,7 +978,10 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
         cs[j] += d[j];
         cu[j] += d2[j];
       }
-      if (g.dz) {
+      if (g.dz && g.low) {
+        store_parts<DT>(g.dz + t * g.ldz + n, g.low, left, vec, d);
+        if (gated) store_parts<DT>(g.dz + t * g.ldz + g.C + n, g.low, left, vec, d2);
+      } else if (g.dz) {
         store_n<DT, 8>(g.dz, false, t * g.ldz + n, left, vec, d);
         if (gated) store_n<DT, 8>(g.dz, false, t * g.ldz + g.C + n, left, vec, d2);
       }
@@ -908,7 +993,11 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
   }
   if (g.dz && blockIdx.y + 1 == gridDim.y) {
     const int pad = (int)(g.ldz - g.N);
-    for (int i = tid; i < rows * pad; i += 256) g.dz[(t0 + i / pad) * g.ldz + g.N + i % pad] = 0;
+    for (int i = tid; i < rows * pad; i += 256) {
+      uint16_t* z = g.dz + (t0 + i / pad) * g.ldz + g.N + i % pad;
+      z[0] = 0;
+      if (g.low) z[g.low] = 0;
+    }
   }
   if (g.part) {
 #pragma unroll
@@ -963,6 +1052,9 @@ __global__ __launch_bounds__(1024) void linear_sums_kernel(const float* __restri
 constexpr int CUS = 256;
 constexpr int64_t MAX_GRID = 1 << 22;  // workgroups of up to 512 threads: a launch has fewer than 2^32 threads
 
+// the summed index, of both parts (each rounded up to whole steps)
+constexpr int64_t k_of_parts(int64_t K, int parts) { return parts == 2 ? 2 * ((K + 63) / 64 * 64) : K; }
+
 struct Plan {
   int bm, bn;  // rows and columns of a tile
   int splits;
@@ -980,20 +1072,21 @@ struct Plan {
 // 64 x 2816 to 4096 11.6 (15.1), 2048 x 4096 to 4096 63 (77), 4096 x 11008 to 4096
 // 255 (450); against 128 x 256 1237 x 4096 to 4096 48 (54), 8192 x 4096 to 1408 97
 // (112 with 128 x 128).
-Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated = false) {
+// Two parts: 256 x 256 leaves too few registers (up to 38 spilled).
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated = false, int parts = 1) {
   Plan p{128, 128, 1, 0.0};
   if (M < 1 || N < 1) return p;
   const int64_t steps = (K + 63) / 64;
   const double bytes_us = (double)((M + N) * K) * 2.0 / 5.0e6;
   auto offer = [&](int bm, int bn, int64_t at_once, double step, double ends, int64_t splits) {
     const int64_t work = ((M + bm - 1) / bm) * ((N + bn - 1) / bn) * splits;
-    if (work > MAX_GRID && bm * bn < 256 * 256) return;
+    if (work > MAX_GRID && bm * bn < (parts == 1 ? 256 : 192) * 256) return;  // but for the largest tile
     const int64_t share = (steps + splits - 1) / splits;
     double us = std::max((double)((work + at_once - 1) / at_once) * ((double)share * step + ends), bytes_us + ends);
     if (splits > 1) us += 3.5 + (double)(splits * M * N) * 4.0 / 2.5e6;
     if (p.us == 0.0 || us < p.us) p = Plan{bm, bn, (int)splits, us};
   };
-  offer(256, 256, CUS, 1.52, 8.0, 1);
+  if (parts == 1) offer(256, 256, CUS, 1.52, 8.0, 1);
   offer(192, 256, CUS, 1.25, 7.5, 1);
   offer(128, 256, CUS, 0.9, 6.0, 1);
   if (!gated) offer(192, 128, CUS, 0.66, 6.0, 1);
@@ -1007,19 +1100,20 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated = false) {
   return p;
 }
 
-template <int DT, bool TA, bool TB, bool GATED>
+template <int DT, bool TA, bool TB, bool GATED, int PARTS = 1>
 hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const LinearEpi& e, float* part,
                        hipStream_t st) {
   TileParams prm;
   prm.a = a;
   prm.b = b;
   prm.K = K;
+  prm.k_all = (int)k_of_parts(K, PARTS);
   prm.e = e;
   prm.part = part;
-  const Plan p = plan_of(a.n, N, K, GATED);
+  const Plan p = plan_of(a.n, N, prm.k_all, GATED, PARTS);
   const bool split = p.splits > 1;
   if (split && !part) return hipErrorInvalidValue;
-  const int64_t steps = (K + 63) / 64;
+  const int64_t steps = (prm.k_all + 63) / 64;
   prm.splits = p.splits;
   prm.k_split = (int)((steps + p.splits - 1) / p.splits) * 64;
   prm.m_tiles = (a.n + p.bm - 1) / p.bm;
@@ -1036,20 +1130,22 @@ hipError_t launch_tile(const Operand& a, const Operand& b, int N, int K, const L
     note_launch(name);
     return launch_kernel(kern, grid, threads, 0, st, prm);
   };
-  if (p.bm == 256) return go("linear_256x256", linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 1, 2>, 512);
+  if constexpr (PARTS == 1) {
+    if (p.bm == 256) return go("linear_256x256", linear_tile_kernel<DT, TA, TB, GATED, 256, 256, 2, 4, 1, 2>, 512);
+  }
   if constexpr (!GATED) {
     if (p.bm == 192 && p.bn == 128)
-      return go("linear_192x128", linear_tile_kernel<DT, TA, TB, false, 192, 128, 2, 4, 1, 4>, 512);
+      return go("linear_192x128", linear_tile_kernel<DT, TA, TB, false, 192, 128, 2, 4, 1, 4, PARTS>, 512);
   }
-  if (p.bm == 192) return go("linear_192x256", linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 1, 2>, 512);
-  if (p.bn == 256) return go("linear_128x256", linear_tile_kernel<DT, TA, TB, GATED, 128, 256, 2, 4, 1, 3>, 512);
-  if (!split && p.bm == 128) return go("linear_128x128", linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2, 4>, 512);
+  if (p.bm == 192) return go("linear_192x256", linear_tile_kernel<DT, TA, TB, GATED, 192, 256, 2, 4, 1, 2, PARTS>, 512);
+  if (p.bn == 256) return go("linear_128x256", linear_tile_kernel<DT, TA, TB, GATED, 128, 256, 2, 4, 1, 3, PARTS>, 512);
+  if (!split && p.bm == 128) return go("linear_128x128", linear_tile_kernel<DT, TA, TB, GATED, 128, 128, 2, 2, 2, 4, PARTS>, 512);
   if constexpr (GATED) {  // 64 columns of each half
-    if (!split) return go("linear_64x128", linear_tile_kernel<DT, TA, TB, true, 64, 128, 2, 2, 1, 3>, 256);
+    if (!split) return go("linear_64x128", linear_tile_kernel<DT, TA, TB, true, 64, 128, 2, 2, 1, 3, PARTS>, 256);
   }
   const hipError_t r = p.bm == 64
-                           ? go("linear_64x64", linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4>, 256)
-                           : go("linear_128x128", linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4>, 512);
+                           ? go("linear_64x64", linear_tile_kernel<DT, TA, TB, false, 64, 64, 2, 2, 1, 4, PARTS>, 256)
+                           : go("linear_128x128", linear_tile_kernel<DT, TA, TB, false, 128, 128, 2, 2, 2, 4, PARTS>, 512);
   if (r != hipSuccess || !split) return r;
   const int w = e.vec ? 8 : 1;
   const int64_t threads = (int64_t)a.n * ((e.C + w - 1) / w);
@@ -1139,14 +1235,17 @@ hipError_t backward(const LinearGrad& g, const void* x, int64_t ldx, const void*
     if (r != hipSuccess) return r;
   }
   if (dx) {
-    const Operand a{dz, ldz, (int)g.T}, b{(const uint16_t*)w, ldw, K};
-    const hipError_t r =
-        launch_tile<DT, false, true, false>(a, b, K, g.N, plain_out(dx, ldx_out, K), part, st);
+    const Operand a{dz, ldz, (int)g.T, g.low}, b{(const uint16_t*)w, ldw, K};
+    const LinearEpi e = plain_out(dx, ldx_out, K);
+    const hipError_t r = g.low ? launch_tile<DT, false, true, false, 2>(a, b, K, g.N, e, part, st)
+                               : launch_tile<DT, false, true, false>(a, b, K, g.N, e, part, st);
     if (r != hipSuccess) return r;
   }
   if (dw) {
-    const Operand a{dz, ldz, g.N}, b{(const uint16_t*)x, ldx, K};
-    return launch_tile<DT, true, true, false>(a, b, K, (int)g.T, plain_out(dw, ldw_out, K), part, st);
+    const Operand a{dz, ldz, g.N, g.low}, b{(const uint16_t*)x, ldx, K};
+    const LinearEpi e = plain_out(dw, ldw_out, K);
+    return g.low ? launch_tile<DT, true, true, false, 2>(a, b, K, (int)g.T, e, part, st)
+                 : launch_tile<DT, true, true, false>(a, b, K, (int)g.T, e, part, st);
   }
   return hipSuccess;
 }
@@ -1164,7 +1263,9 @@ int64_t linear_forward_bytes(int64_t T, int64_t N, int64_t K) {
   return bytes;
 }
 
-int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K) { return part_bytes(plan_of(M, N, K), M, N); }
+int64_t linear_part_bytes(int64_t M, int64_t N, int64_t K, int parts) {
+  return part_bytes(plan_of(M, N, k_of_parts(K, parts), false, parts), M, N);
+}
 
 hipError_t launch_linear(const void* x, int dt, int64_t ldx, int T, const void* w, int64_t ldw, int N, int K,
                          const LinearEpi& e, float* part, hipStream_t st) {

@@ -389,8 +389,9 @@ struct LinearGradLayout {
   int rows, blocks, across, column_blocks;
 };
 
-// N: rows of W; a gated product has half as many columns, and fewer blocks of them than is reserved
-LinearGradLayout linear_grad_layout(int64_t T, int64_t N, int64_t K, int64_t C) {
+// N: rows of W; a gated product has half as many columns, and fewer blocks of them than is reserved.
+// parts: of dz, 1 or 2
+LinearGradLayout linear_grad_layout(int64_t T, int64_t N, int64_t K, int64_t C, int parts) {
   LinearGradLayout L{};
   L.ldz = (N + 7) / 8 * 8;
   // 16 rows a workgroup, so that a few thousand fill the CUs, and at most 64 threads (512 columns) across
@@ -405,11 +406,11 @@ LinearGradLayout linear_grad_layout(int64_t T, int64_t N, int64_t K, int64_t C) 
     at += align_up(bytes);
     return r;
   };
-  L.dz = take((size_t)(T * L.ldz * 2));
+  L.dz = take((size_t)(parts * T * L.ldz * 2));
   L.sums = take((size_t)((int64_t)L.blocks * N * 4));
   L.row_sums = take((size_t)((N + 511) / 512 * T * 4));
   // the two products run one after the other
-  L.part = take((size_t)std::max(moe::linear_part_bytes(T, K, N), moe::linear_part_bytes(N, K, T)));
+  L.part = take((size_t)std::max(moe::linear_part_bytes(T, K, N, parts), moe::linear_part_bytes(N, K, T, parts)));
   L.total = at;
   return L;
 }
@@ -1106,7 +1107,7 @@ moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const
 
 size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t K) {
   if (T < 0 || N < 1 || K < 1) return 0;
-  return linear_grad_layout(T, N, K, N).total;
+  return std::max(linear_grad_layout(T, N, K, N, 1).total, linear_grad_layout(T, N, K, N, 2).total);
 }
 
 moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_grad, const void* x, moe_dtype dt,
@@ -1132,9 +1133,14 @@ moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_g
       if (!preact && (dense->act != MOE_ACT_NONE || grad_row_scale)) return MOE_ERR_NULL;
       if (preact && (s = check_matrix(preact, dt, ld_preact, N)) != MOE_OK) return s;
     }
-    const LinearGradLayout L = linear_grad_layout(T, N, K, C);
-    if (L.total) {
-      if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    // two where one would lose bits of the gradient: by its range in fp16; by its
+    // rounding, and as far as the products are not bound by the matrix cores, in bf16
+    const int parts = grad_dt == MOE_F32 && (dt == MOE_F16 || N <= MOE_LINEAR_TWO_PARTS) ? 2 : 1;
+    const LinearGradLayout L = linear_grad_layout(T, N, K, C, parts);
+    // what the size function says, whatever the gradient's type
+    const size_t need = std::max(L.total, linear_grad_layout(T, N, K, C, 3 - parts).total);
+    if (need) {
+      if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
       if (!aligned16(ws)) return MOE_ERR_ALIGN;
     }
     DevProps props;
@@ -1152,6 +1158,7 @@ moe_status moe_linear_backward(const void* grad, moe_dtype grad_dt, int64_t ld_g
     g.rs = row_scale;
     g.dz = direct || !(grad_x || grad_w) || T == 0 ? nullptr : (uint16_t*)(W + L.dz);
     g.ldz = L.ldz;
+    g.low = parts == 2 ? (int64_t)T * L.ldz : 0;
     // one block's sums are the result
     g.part = !grad_bias ? nullptr : L.blocks == 1 ? grad_bias : (float*)(W + L.sums);
     g.row_part = !grad_row_scale ? nullptr : L.column_blocks == 1 ? grad_row_scale : (float*)(W + L.row_sums);
