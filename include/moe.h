@@ -625,7 +625,8 @@ moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const
  *   grad_x [T, K] = dz W,  grad_w [N, K] = dz^T x      in dt
  *   grad_bias [N] = sum_t dz,  grad_row_scale [T] = sum_c g act(preact)    fp32
  * (the residual's gradient is g).  Each output may be NULL.  preact [T, N] as
- * moe_linear kept it; it may be NULL with act none where grad_row_scale is NULL.
+ * moe_linear kept it (infinite where z left dt's range: act and its slope have
+ * their limits there); it may be NULL with act none where grad_row_scale is NULL.
  * dense->bias is not read; w is read for grad_x only and may be NULL without,
  * and so x for grad_w.  dz enters the two products in dt's bits: rounded once, but
  * for an fp32 gradient with MOE_F16, or with MOE_BF16 and N up to

@@ -46,9 +46,6 @@ bool whole_sequences(int T) { return T <= 512; }
 
 constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.69314718055994531f;
 
-// a b, and 0 where a or b is 0 whatever the other is (v_mul_legacy_f32)
-__device__ float mul0(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
-
 template <int LT>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
   if constexpr (LT == GATE_F32) return ((const float*)p)[i];

@@ -19,6 +19,10 @@ enum { ACT_F16 = 1, ACT_BF16 = 2 };
 
 constexpr int WAVE = 64;
 
+// a b, and 0 where a or b is 0 whatever the other is (v_mul_legacy_f32; there is no
+// builtin, and inline assembly would hide it from the compiler's hazard checks)
+__device__ float mul0(float a, float b) __asm("llvm.amdgcn.fmul.legacy");
+
 // ------------------------------------------------------------ conversions --
 
 __device__ __forceinline__ float f16_bits_to_f32(uint32_t b) {

@@ -104,7 +104,7 @@ __device__ __forceinline__ float normal_(float z, float& e) {
   return z > 0.0f ? 1.0f - tail : tail;
 }
 
-// act(z) and its slope
+// act(z) and its slope; at infinities (products beyond fp16's range) their limits
 __device__ __forceinline__ float activate_slope(int act, float z, float& slope) {
   switch (act) {
     case LIN_RELU:
@@ -112,14 +112,14 @@ __device__ __forceinline__ float activate_slope(int act, float z, float& slope) 
       return z > 0.0f ? z : (z != z ? z : 0.0f);
     case LIN_SILU: {
       const float s = sigmoid_(z);
-      slope = s * (1.0f + z * sigmoid_(-z));
-      return z * s;
+      slope = mul0(s, 1.0f + mul0(z, sigmoid_(-z)));
+      return mul0(z, s);
     }
     case LIN_GELU: {
       float e;
       const float c = normal_(z, e);
-      slope = e != 0.0f ? c + z * (0.39894228040143268f * e) : c;
-      return z * c;
+      slope = c + mul0(z, 0.39894228040143268f * e);
+      return mul0(z, c);
     }
     case LIN_SIGMOID: {
       const float s = sigmoid_(z);
