@@ -20,6 +20,7 @@ import os
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_amd.so")
@@ -561,6 +562,14 @@ def _no_graph(name: str) -> None:
                            "detached tensors" % name)
 
 
+def _no_tangent(name: str, *inputs) -> None:
+    """Refuses forward-mode dual tensors: the call would drop their tangents silently."""
+    if _forward_ad._current_level >= 0:
+        for t in inputs:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise RuntimeError("%s has no forward-mode derivative, and an input has a tangent" % name)
+
+
 class _GateFromLogits(torch.autograd.Function):
     """gate_from_logits for logits that require grad, with gate_backward as its gradient."""
 
@@ -594,6 +603,7 @@ def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bi
         with _elsewhere(logits, stream):
             return gate_from_logits(logits, k, score=score, bias=bias, groups=groups, group_k=group_k,
                                     group_best=group_best, renorm=renorm, scale=scale, out=out)
+    _no_tangent("gate_from_logits", logits)
     if logits.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise RuntimeError("gate_from_logits: `out` has no graph, and the logits require grad")
@@ -624,6 +634,7 @@ def gate(x: torch.Tensor, router_w: torch.Tensor, k: int, *, score: str = "softm
         with _elsewhere(x, stream):
             return gate(x, router_w, k, score=score, bias=bias, groups=groups, group_k=group_k,
                         group_best=group_best, renorm=renorm, scale=scale, want_logits=want_logits, out=out)
+    _no_tangent("gate", x, router_w)
     if x.requires_grad or router_w.requires_grad:
         _no_graph("gate")
     code = _dtype_code(x)
@@ -655,6 +666,7 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
     if not _here(logits, stream):
         with _elsewhere(logits, stream):
             return gate_backward(logits, idx, grad_w, score=score, renorm=renorm, scale=scale, out=out)
+    _no_tangent("gate_backward", logits, grad_w)
     code = _gate_type(logits)
     logits, T, E, ld = _rows(logits, "logits")
     if idx.dim() != 2:
@@ -688,6 +700,7 @@ def layer_forward_gated(x: torch.Tensor, router_w: Optional[torch.Tensor], k: in
             return layer_forward_gated(x, router_w, k, down, gate_up, gate, up, flags, taps, out, workspace,
                                        logits=logits, score=score, bias=bias, groups=groups, group_k=group_k,
                                        group_best=group_best, renorm=renorm, scale=scale, capacity=capacity)
+    _no_tangent("layer_forward_gated", x, router_w, logits)
     if any(t is not None and t.requires_grad for t in (x, router_w, logits)):
         _no_graph("layer_forward_gated")
     code = _dtype_code(x)
@@ -728,6 +741,7 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
     if not _here(x, stream):
         with _elsewhere(x, stream):
             return lora_add(x, base, ids, a, b, scale=scale, ranks=ranks, out=out)
+    _no_tangent("lora_add", x, base, a, b, scale)
     if (x.requires_grad or base.requires_grad or a.requires_grad or b.requires_grad or
             (scale is not None and scale.requires_grad)):
         _no_graph("lora_add")
@@ -827,6 +841,7 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor, *, score: str = "softm
     if not _here(logits, stream):
         with _elsewhere(logits, stream):
             return balance_loss(logits, idx, score=score, offsets=offsets, mask=mask)
+    _no_tangent("balance_loss", logits)
     if logits.requires_grad and torch.is_grad_enabled():
         _capture_refused("balance_loss", "balance_loss_backward")
         loss, z, prob, counts, tokens = _BalanceLoss.apply(logits, idx, dict(score=score, offsets=offsets, mask=mask))
@@ -874,6 +889,7 @@ def balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: to
         with _elsewhere(logits, stream):
             return balance_loss_backward(logits, counts, tokens, grad_loss, k, grad_z=grad_z, score=score,
                                          offsets=offsets, mask=mask, out=out)
+    _no_tangent("balance_loss_backward", logits, grad_loss, grad_z)
     code = _gate_type(logits)
     logits, T, E, ld = _rows(logits, "logits")
     dev = logits.get_device()
@@ -961,6 +977,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
         with _elsewhere(x, stream):
             return linear(x, w, bias, act=act, residual=residual, row_scale=row_scale, out_dtype=out_dtype,
                           want_preact=want_preact, out=out)
+    _no_tangent("linear", x, w, bias, residual, row_scale)
     code, dtype = _dtype_code(x), x.dtype
     odt = dtype if out_dtype is None else out_dtype
     if odt is not dtype and odt is not torch.float32:
@@ -1019,6 +1036,7 @@ def linear_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, act
     if not _here(x, stream):
         with _elsewhere(x, stream):
             return linear_backward(grad, x, w, act=act, preact=preact, row_scale=row_scale, want=want)
+    _no_tangent("linear_backward", grad, x, w, preact, row_scale)
     unknown = [n for n in want if n not in ("x", "w", "bias", "row_scale")]
     if unknown:
         raise ValueError('want names "x", "w", "bias" and "row_scale", got %r' % (unknown,))
