@@ -406,6 +406,8 @@ def layer_forward(x: torch.Tensor, router_w: torch.Tensor, k: int, down: Weights
         st = lib().moe_layer_forward_ex(_ptr(x), _dtype_code(x), T, H, _ptr(router_w), E, k, ctypes.byref(o),
                                         *wargs)
     _check(st, "moe_layer_forward")
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -430,6 +432,8 @@ def layer_forward_noalloc(x: torch.Tensor, router_w: torch.Tensor, k: int, down:
                                          ref(up), ref(down), _ptr(y), flags,
                                          ctypes.byref(ctaps) if ctaps is not None else None, _stream(stream))
     _check(st, "moe_layer_forward_noalloc")
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -570,6 +574,16 @@ def _no_tangent(name: str, *inputs) -> None:
                 raise RuntimeError("%s has no forward-mode derivative, and an input has a tangent" % name)
 
 
+# counts a tensor's changes: 0.3 us a call
+_increment_version = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
+
+
+def _written(*tensors) -> None:
+    """Tells autograd that the caller's tensors hold other values now: a graph that saved one refuses to go back
+    through it, as after any operation in place."""
+    _increment_version(tensors)
+
+
 class _GateFromLogits(torch.autograd.Function):
     """gate_from_logits for logits that require grad, with gate_backward as its gradient."""
 
@@ -621,6 +635,8 @@ def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bi
     idx, w = _routing_out(logits, T, k, out)
     _check(lib().moe_gate_from_logits(logits.data_ptr(), code, ld, T, E, k, o, idx.data_ptr(), w.data_ptr(),
                                       _current(dev)), "moe_gate_from_logits")
+    if out is not None:
+        _written(idx, w)
     return dict(idx=idx, w=w)
 
 
@@ -649,6 +665,8 @@ def gate(x: torch.Tensor, router_w: torch.Tensor, k: int, *, score: str = "softm
     logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
     _check(lib().moe_gate(x.data_ptr(), code, T, H, pw, E, k, o, idx.data_ptr(), w.data_ptr(), logits.data_ptr(), None,
                           0, _current(dev)), "moe_gate")
+    if out is not None:
+        _written(idx, w)
     r = dict(idx=idx, w=w)
     if want_logits:
         r["logits"] = logits
@@ -682,6 +700,8 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
     o = _gate_opts(dev, E, score, None, 0, 0, 1, renorm, scale)
     _check(lib().moe_gate_backward(logits.data_ptr(), code, ld, T, E, k, o, pi, pg, g.data_ptr(), ldg, _current(dev)),
            "moe_gate_backward")
+    if out is not None:
+        _written(out)
     return g
 
 
@@ -724,6 +744,8 @@ def layer_forward_gated(x: torch.Tensor, router_w: Optional[torch.Tensor], k: in
     _check(lib().moe_layer_forward_gated(x.data_ptr(), code, T, H, pw, pl, E, k, o, ref(gate_up), ref(gate), ref(up),
                                          down.c(), y.data_ptr(), flags, ctaps, ws.data_ptr(), ws.numel(), _current(dev)),
            "moe_layer_forward_gated")
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -762,6 +784,7 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
                  _operand(scale, "scale", dev, torch.float32, (L,)), _operand(ranks, "ranks", dev, torch.int32, (L,)),
                  L, R, K, N)
     pids = _operand(ids, "ids", dev, torch.int32, (T,))
+    given = out
     if out is None:
         base, _, _, ldb = _rows(base, "base")
         out, ldo = _new(base, T, N, odt), N
@@ -773,6 +796,8 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
             base, _, _, ldb = _rows(base, "base")
     _check(lib().moe_lora_add(x.data_ptr(), code, ldx, T, lora, pids, base.data_ptr(), ldb, out.data_ptr(), ldo,
                               _TYPES[odt], _current(dev)), "moe_lora_add")
+    if given is not None:
+        _written(out)
     return out
 
 
@@ -904,6 +929,8 @@ def balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: to
         g, ldg = out, _out_rows(out, "out", dev, logits.dtype, (T, E))
     _check(lib().moe_balance_loss_backward(logits.data_ptr(), code, ld, T, E, k, o, pc, pt, pg, pz, g.data_ptr(), ldg,
                                            _current(dev)), "moe_balance_loss_backward")
+    if out is not None:
+        _written(out)
     return g
 
 
@@ -1010,6 +1037,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
         else:
             residual, ldr = _beside(residual, "residual", dev, odt, (T, C))
         pr = residual.data_ptr()
+    given = out
     if out is None:
         out, ldo = _new(x, T, C, odt), C
     else:
@@ -1020,6 +1048,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     _check(lib().moe_linear(x.data_ptr(), code, ldx, T, CDense(w.data_ptr(), ldw, pb, bcode, N, K, kind), pr, ldr, ps,
                             None if z is None else z.data_ptr(), N, out.data_ptr(), ldo, _TYPES[odt],
                             None if ws is None else ws.data_ptr(), need, _current(dev)), "moe_linear")
+    if given is not None:
+        _written(out)
     return (out, z) if want_preact else out
 
 
