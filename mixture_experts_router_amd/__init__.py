@@ -574,6 +574,12 @@ def _no_tangent(name: str, *inputs) -> None:
                 raise RuntimeError("%s has no forward-mode derivative, and an input has a tangent" % name)
 
 
+def _no_graph_of_out(name: str, *outs) -> None:
+    """Refuses to write over tensors that autograd follows: their graph would belong to other values."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in outs):
+        raise RuntimeError("%s: `out` has no graph, and a tensor given for it requires grad" % name)
+
+
 # counts a tensor's changes: 0.3 us a call
 _increment_version = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
 
@@ -618,6 +624,8 @@ def gate_from_logits(logits: torch.Tensor, k: int, *, score: str = "softmax", bi
             return gate_from_logits(logits, k, score=score, bias=bias, groups=groups, group_k=group_k,
                                     group_best=group_best, renorm=renorm, scale=scale, out=out)
     _no_tangent("gate_from_logits", logits)
+    if out is not None:
+        _no_graph_of_out("gate_from_logits", *out)
     if logits.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise RuntimeError("gate_from_logits: `out` has no graph, and the logits require grad")
@@ -651,6 +659,8 @@ def gate(x: torch.Tensor, router_w: torch.Tensor, k: int, *, score: str = "softm
             return gate(x, router_w, k, score=score, bias=bias, groups=groups, group_k=group_k,
                         group_best=group_best, renorm=renorm, scale=scale, want_logits=want_logits, out=out)
     _no_tangent("gate", x, router_w)
+    if out is not None:
+        _no_graph_of_out("gate", *out)
     if x.requires_grad or router_w.requires_grad:
         _no_graph("gate")
     code = _dtype_code(x)
@@ -685,6 +695,8 @@ def gate_backward(logits: torch.Tensor, idx: torch.Tensor, grad_w: torch.Tensor,
         with _elsewhere(logits, stream):
             return gate_backward(logits, idx, grad_w, score=score, renorm=renorm, scale=scale, out=out)
     _no_tangent("gate_backward", logits, grad_w)
+    if out is not None:
+        _no_graph_of_out("gate_backward", out)
     code = _gate_type(logits)
     logits, T, E, ld = _rows(logits, "logits")
     if idx.dim() != 2:
@@ -721,6 +733,8 @@ def layer_forward_gated(x: torch.Tensor, router_w: Optional[torch.Tensor], k: in
                                        logits=logits, score=score, bias=bias, groups=groups, group_k=group_k,
                                        group_best=group_best, renorm=renorm, scale=scale, capacity=capacity)
     _no_tangent("layer_forward_gated", x, router_w, logits)
+    if out is not None:
+        _no_graph_of_out("layer_forward_gated", out)
     if any(t is not None and t.requires_grad for t in (x, router_w, logits)):
         _no_graph("layer_forward_gated")
     code = _dtype_code(x)
@@ -764,6 +778,8 @@ def lora_add(x: torch.Tensor, base: torch.Tensor, ids: torch.Tensor, a: torch.Te
         with _elsewhere(x, stream):
             return lora_add(x, base, ids, a, b, scale=scale, ranks=ranks, out=out)
     _no_tangent("lora_add", x, base, a, b, scale)
+    if out is not None:
+        _no_graph_of_out("lora_add", out)
     if (x.requires_grad or base.requires_grad or a.requires_grad or b.requires_grad or
             (scale is not None and scale.requires_grad)):
         _no_graph("lora_add")
@@ -915,6 +931,8 @@ def balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: to
             return balance_loss_backward(logits, counts, tokens, grad_loss, k, grad_z=grad_z, score=score,
                                          offsets=offsets, mask=mask, out=out)
     _no_tangent("balance_loss_backward", logits, grad_loss, grad_z)
+    if out is not None:
+        _no_graph_of_out("balance_loss_backward", out)
     code = _gate_type(logits)
     logits, T, E, ld = _rows(logits, "logits")
     dev = logits.get_device()
@@ -1005,6 +1023,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
             return linear(x, w, bias, act=act, residual=residual, row_scale=row_scale, out_dtype=out_dtype,
                           want_preact=want_preact, out=out)
     _no_tangent("linear", x, w, bias, residual, row_scale)
+    if out is not None:
+        _no_graph_of_out("linear", out)
     code, dtype = _dtype_code(x), x.dtype
     odt = dtype if out_dtype is None else out_dtype
     if odt is not dtype and odt is not torch.float32:

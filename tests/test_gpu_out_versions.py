@@ -64,6 +64,19 @@ def test_autograd_sees_what_out_overwrites(name):
 
 
 @pytest.mark.parametrize("name", NAMES)
+def test_an_out_that_requires_grad(name):
+    """Writing over it would leave a graph that belongs to another value."""
+    call, like = writers()[name]
+    leaf = like.clone().requires_grad_()
+    node = leaf * 1.0
+    for out in (leaf, node):
+        with pytest.raises(RuntimeError, match="require"):
+            call(out)
+        with torch.no_grad():
+            call(out)
+
+
+@pytest.mark.parametrize("name", NAMES)
 def test_inference_mode(name):
     """Tensors of inference mode have no version: written as ever."""
     with torch.inference_mode():
