@@ -852,11 +852,11 @@ class _BalanceLoss(torch.autograd.Function):
         r = balance_loss(logits, idx, **opts)  # grad mode is off in here
         ctx.save_for_backward(logits, r["counts"], r["tokens"], opts["offsets"], opts["mask"])
         ctx.k, ctx.score = idx.shape[1], opts["score"]
-        z = r.get("z")
+        z, fixed = r.get("z"), (r["prob"], r["counts"], r["tokens"])
         if z is None:
             z = r["loss"].new_empty(0)
-            ctx.mark_non_differentiable(z)
-        ctx.mark_non_differentiable(r["prob"], r["counts"], r["tokens"])
+            fixed += (z,)
+        ctx.mark_non_differentiable(*fixed)
         return r["loss"], z, r["prob"], r["counts"], r["tokens"]
 
     @staticmethod

@@ -222,7 +222,7 @@ struct LinearGrad {
   int64_t ldg, ldz_in, ldz, T;
   int C, N, act;
   int rows, blocks;           // rows of a block: at most LINEAR_DZ_ROWS
-  int across, column_blocks;  // threads across a row: a power of two
+  int across, column_blocks;  // threads across a row: a power of two, at most 64
   bool g_f32, vec;
 };
 constexpr int LINEAR_DZ_ROWS = 64;
