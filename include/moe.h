@@ -628,12 +628,13 @@ moe_status moe_linear(const void* x, moe_dtype dt, int64_t ldx, int32_t T, const
  * moe_linear kept it (infinite where z left dt's range: act and its slope have
  * their limits there); it may be NULL with act none where grad_row_scale is NULL.
  * dense->bias is not read; w is read for grad_x only and may be NULL without,
- * and so x for grad_w.  dz enters the two products in dt's bits: rounded once, but
- * for an fp32 gradient with MOE_F16, or with MOE_BF16 and N up to
- * MOE_LINEAR_TWO_PARTS (a router's experts).  Then it enters in two parts, off by at
- * most 2^-15 of it (MOE_BF16), or by 2^-20 of it between 2^-6 and 2^13, outside by
- * 2^-11 of it or 2^-35, the larger, and infinite above 1.6e7 (MOE_F16).  Outputs overlap nothing.  T == 0 writes zeros to grad_w
- * and grad_bias.
+ * and so x for grad_w.  dz enters the two products in dt's bits: rounded once
+ * (MOE_F16: 0 below 2^-25, infinite above 65504, as g itself would be), but for an
+ * fp32 gradient with MOE_F16, or with MOE_BF16 and N up to MOE_LINEAR_TWO_PARTS (a
+ * router's experts).  Then it enters in two parts, off by at most 2^-15 of it
+ * (MOE_BF16), or by 2^-20 of it between 2^-6 and 2^13, outside by 2^-11 of it or
+ * 2^-35, the larger, and infinite above 1.6e7 (MOE_F16).  Outputs overlap nothing.
+ * T == 0 writes zeros to grad_w and grad_bias.
  *   ws  moe_linear_backward_workspace_size(T, N, K) bytes, 16-byte aligned
  */
 size_t moe_linear_backward_workspace_size(int32_t T, int32_t N, int32_t K);

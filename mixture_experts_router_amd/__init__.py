@@ -1014,10 +1014,10 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     row_scale [T] float32.  The result [T, N] (swiglu: [T, N / 2]) and residual
     have x's type or, with out_dtype, float32.  K a multiple of 8.  want_preact:
     (result, x w^T + bias in x's type), the latter for linear_backward.  out:
-    written instead of a new tensor; the residual itself adds in place.  For
-    inputs that require grad (and no `out` or want_preact) the result carries the
-    graph of linear_backward, of first order; refused while the stream is
-    captured."""
+    written instead of a new tensor; the residual itself adds in place (otherwise
+    it must not overlap an input).  For inputs that require grad (and no `out` or
+    want_preact) the result carries the graph of linear_backward, of first order;
+    refused while the stream is captured."""
     if not _here(x, stream):
         with _elsewhere(x, stream):
             return linear(x, w, bias, act=act, residual=residual, row_scale=row_scale, out_dtype=out_dtype,

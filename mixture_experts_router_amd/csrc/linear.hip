@@ -212,12 +212,13 @@ __device__ __forceinline__ void store_n(void* p, bool f32, int64_t at, int left,
 // loss's gradient is 1e-8 and less) or above 65504, and a router's gradients in bf16
 // are off by 2.4e-3 where their own rounding is 1.7e-3.  The matrix instructions are
 // twice as many: 36 to 45 us for 4096 x 4096 to 64, at most 30% more up to 256
-// columns; 185 to 320 us for 2816, where bf16 takes one (moe_linear_backward).  The first is dz without its low bits, the second what is left.  fp16: the
-// first holds dz 2^-SHIFT_DZ, the second what is left of that times 2^SHIFT_LOW, in
-// all 2^-37 up to 2^24; where what is left has no room (dz above 2^13), the first is
-// rounded instead.  A second part of 0 is replaced by the smallest that matrix
-// instructions keep, and both have dz's sign, so that an infinite weight or input
-// gives dz's infinity, not NaN.
+// columns; 185 to 320 us for 2816, where bf16 takes one (moe_linear_backward).
+// The first is dz without its low bits, the second what is left.  fp16: the first
+// holds dz 2^-SHIFT_DZ, the second what is left of that times 2^SHIFT_LOW, together
+// 2^-37 up to 2^24; where what is left has no room (dz above 2^13), the first is
+// rounded instead.  A second part of 0 beside a first is replaced by a tiny one, and
+// both have dz's sign, so that an infinite weight or input gives dz's infinity, not
+// NaN.
 constexpr int SHIFT_DZ = 8, SHIFT_LOW = 20;
 
 template <int DT>
@@ -330,8 +331,9 @@ __device__ __forceinline__ void finish(const LinearEpi& e, int64_t t, int n, flo
 // 512 cycles of MFMAs, so LDS keeps up; the MFMAs run 58% of the cycles, at about
 // 1.9 GHz under the card's power limit (operands of zeros took 205 us where
 // others took 258).  8192^3 in 745 us, 1475 TFLOP/s; 4096 x 11008 to 4096 in 258
-// us from the caches, 1431 TFLOP/s (282 us with a residual and other operands
-// each time); smaller tiles wait for LDS: 128 x 128 needs it for 768 cycles a
+// us from the caches, 1431 TFLOP/s (282 to 292 us, by the box, with a residual and
+// other operands each time); smaller tiles wait for LDS: 128 x 128 needs it for 768
+// cycles a
 // step of 512 cycles of MFMAs (777 x 4096 to 2816 28 us).
 //
 // Offsets: a descriptor starts at the tile's first element (64-bit), so that
@@ -930,13 +932,13 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
 // ------------------------------------------------------- gradient of z ----
 //
 // A workgroup takes g.rows rows and 8 g.across columns (gated: of each half), a
-// thread eight columns of every (256 / g.across)-th row.  dz is the
-// operand of both products: rounded to their 16 bits where the gradient that came
-// in has 16 (its own rounding is as large), in two parts where it has 32.  The sums
-// of bias and row_scale use it unrounded and go to part[row block][N] and
-// row_part[column block][T], joined in order (one block's are the result).  The last column block writes zeros up to ldz.  Bound by its
-// bytes: 58 MB of 4096 x 2 x 1408 in 16 us, 3.6 TB/s (one column block a
-// workgroup of 16 rows: 60 us).
+// thread eight columns of every (256 / g.across)-th row.  dz is the operand of both
+// products: rounded to their 16 bits, which is what the gradient that came in was
+// rounded by, or in two parts where that has more (g.low).  The sums of bias and
+// row_scale use it unrounded and go to part[row block][N] and row_part[column
+// block][T], joined in order (one block's are the result).  The
+// last column block writes zeros up to ldz.  Bound by its bytes: 58 MB of 4096 x 2 x
+// 1408 in 16 to 17.5 us, 3.5 TB/s (one column block a workgroup of 16 rows: 60 us).
 template <int DT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearGrad g) {
   __shared__ float sums[256][17];
