@@ -333,8 +333,7 @@ __device__ __forceinline__ void finish(const LinearEpi& e, int64_t t, int n, flo
 // others took 258).  8192^3 in 745 us, 1475 TFLOP/s; 4096 x 11008 to 4096 in 258
 // us from the caches, 1431 TFLOP/s (282 to 292 us, by the box, with a residual and
 // other operands each time); smaller tiles wait for LDS: 128 x 128 needs it for 768
-// cycles a
-// step of 512 cycles of MFMAs (777 x 4096 to 2816 28 us).
+// cycles a step of 512 cycles of MFMAs (777 x 4096 to 2816 28 us).
 //
 // Offsets: a descriptor starts at the tile's first element (64-bit), so that
 // offsets within it stay below 2^31; rows, columns and k past the operand's end
@@ -1070,7 +1069,8 @@ struct Plan {
 // 64 x 2816 to 4096 11.6 (15.1), 2048 x 4096 to 4096 63 (77), 4096 x 11008 to 4096
 // 255 (450); against 128 x 256 1237 x 4096 to 4096 48 (54), 8192 x 4096 to 1408 97
 // (112 with 128 x 128).
-// Two parts: 256 x 256 leaves too few registers (up to 38 spilled).
+// Two parts: 256 x 256 leaves too few registers (up to 38 spilled; where none is, the
+// router's gradients take as long with it).
 Plan plan_of(int64_t M, int64_t N, int64_t K, bool gated = false, int parts = 1) {
   Plan p{128, 128, 1, 0.0};
   if (M < 1 || N < 1) return p;
